@@ -1,7 +1,7 @@
 """ctypes binding of ``libkt_rawint4.so`` (argument marshalling only).
 
 Every function has the name and argument order of its C entry point in
-``include/kt_rawint4.h``.  Tensors are passed as raw pointers (``data_ptr()``),
+``include/kt_rawint4.h`` or ``include/kt_block.h``.  Tensors are passed as raw pointers (``data_ptr()``),
 ``stream`` defaults to torch's current HIP stream, and a nonzero return code
 raises ``KtRawInt4Error`` with the library's message.  There is no fallback:
 without the built library every call raises.
@@ -26,6 +26,18 @@ KT_RAWINT4_STATIC_SCRATCH_BYTES = 64 << 20
 KT_RAWINT4_FORMAT_RAWINT4 = 0
 KT_RAWINT4_FORMAT_MXFP4 = 1
 FORMATS = {"rawint4": KT_RAWINT4_FORMAT_RAWINT4, "mxfp4": KT_RAWINT4_FORMAT_MXFP4}
+
+KT_TYPE_BF16 = 0
+KT_TYPE_F32 = 1
+KT_SCORE_SOFTMAX = 0
+KT_SCORE_SIGMOID = 1
+SCORES = {"softmax": KT_SCORE_SOFTMAX, "sigmoid": KT_SCORE_SIGMOID}
+KT_ROUTER_MAX_GROUPS = 64
+KT_CKPT8_INT8 = 0
+KT_CKPT8_E4M3 = 1
+CKPT8_FORMATS = {"int8": KT_CKPT8_INT8, "e4m3": KT_CKPT8_E4M3}
+KT_CKPT8_GROUP = 32
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _vp = ctypes.c_void_p
 
@@ -61,6 +73,34 @@ class kt_rawint4_moe_layer(ctypes.Structure):  # noqa: N801 - the C struct's nam
     ]
 
 
+class kt_router(ctypes.Structure):  # noqa: N801 - the C struct's name
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("logits_type", ctypes.c_int32),
+    ]
+
+
+class kt_linear(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("weight", _vp),
+        ("bias", _vp),
+    ]
+
+
+class kt_ckpt8(ctypes.Structure):  # noqa: N801
+    _fields_ = [("format", ctypes.c_int32), ("codes", _vp), ("scales", _vp)]
+
+
 _lib = None
 
 
@@ -72,6 +112,7 @@ def load_library() -> ctypes.CDLL:
         raise KtRawInt4Error(KT_RAWINT4_EHIP, f"{LIBRARY_PATH} is not built; run __graft_entry__.build()")
     lib = ctypes.CDLL(LIBRARY_PATH)
     lp = ctypes.POINTER(kt_rawint4_moe_layer)
+    rp, np_, cp = ctypes.POINTER(kt_router), ctypes.POINTER(kt_linear), ctypes.POINTER(kt_ckpt8)
     i32, i64, f32, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     sigs = {
         "kt_rawint4_moe_workspace_bytes": (sz, [lp, i32]),
@@ -82,6 +123,19 @@ def load_library() -> ctypes.CDLL:
         "kt_rawint4_moe_bwd": (ctypes.c_int, [lp, i32, _vp, _vp, _vp, _vp, _vp, _vp] + [_vp] * 6 + [i32, f32, _vp, sz, _vp]),
         "kt_rawint4_moe_bwd_recompute": (ctypes.c_int,
                                          [lp, i32, _vp, _vp, _vp, _vp, _vp, _vp] + [_vp] * 6 + [i32, f32, _vp, sz, _vp]),
+        "kt_moe_bwd_ckpt8_workspace_bytes": (sz, [lp, i32]),
+        "kt_moe_bwd_ckpt8": (ctypes.c_int,
+                             [lp, i32, i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp] + [_vp] * 6 + [i32, f32, _vp, sz, _vp]),
+        "kt_ckpt8_pack": (ctypes.c_int, [_vp, i64, i64, i32, _vp, _vp, _vp]),
+        "kt_ckpt8_unpack": (ctypes.c_int, [_vp, _vp, i64, i64, i32, _vp, _vp]),
+        "kt_router_fwd": (ctypes.c_int, [rp, i32, _vp, _vp, _vp, _vp, _vp, _vp, i32, _vp]),
+        "kt_router_bwd": (ctypes.c_int, [rp, i32, _vp, _vp, _vp, _vp, _vp]),
+        "kt_router_update_bias": (ctypes.c_int, [_vp, _vp, i32, f32, _vp]),
+        "kt_linear_workspace_bytes": (sz, [np_, i32]),
+        "kt_linear_fwd": (ctypes.c_int, [np_, i32, _vp, _vp, _vp, i32, _vp, _vp, sz, _vp]),
+        "kt_linear_bwd_workspace_bytes": (sz, [np_, i32, i32]),
+        "kt_linear_bwd": (ctypes.c_int,
+                          [np_, i32, _vp, cp, _vp, _vp, i32, _vp, _vp, _vp, _vp, i32, f32, _vp, sz, _vp]),
         "kt_rawint4_unpack": (ctypes.c_int, [_vp, i64, i64, _vp, _vp]),
         "kt_rawint4_dequant": (ctypes.c_int, [_vp, _vp, i64, i64, _vp, _vp]),
         "kt_rawint4_dequant_mxfp4": (ctypes.c_int, [_vp, _vp, i64, i64, _vp, _vp]),
@@ -193,6 +247,84 @@ def kt_rawint4_moe_bwd_recompute(layer, qlen, inputs, expert_ids, route_weights,
         ctypes.byref(layer), int(qlen), _ptr(inputs), _ptr(expert_ids), _ptr(route_weights), _ptr(grad_output),
         _ptr(grad_input), _ptr(grad_route), _ptr(d_gate_a), _ptr(d_gate_b), _ptr(d_up_a), _ptr(d_up_b),
         _ptr(d_down_a), _ptr(d_down_b), int(bool(accumulate)), float(grad_scale), _ptr(workspace),
+        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_moe_bwd_ckpt8_workspace_bytes(layer: kt_rawint4_moe_layer, qlen: int) -> int:
+    n = load_library().kt_moe_bwd_ckpt8_workspace_bytes(ctypes.byref(layer), int(qlen))
+    if n == 0:
+        raise KtRawInt4Error(KT_RAWINT4_EINVAL, kt_rawint4_last_error())
+    return int(n)
+
+
+def kt_moe_bwd_ckpt8(layer, qlen, format, codes, scales, expert_ids, route_weights, grad_output, grad_input, grad_route,
+                     d_gate_a, d_gate_b, d_up_a, d_up_b, d_down_a, d_down_b, accumulate, grad_scale, workspace,
+                     stream=None) -> None:
+    _check(load_library().kt_moe_bwd_ckpt8(
+        ctypes.byref(layer), int(qlen), int(format), _ptr(codes), _ptr(scales), _ptr(expert_ids), _ptr(route_weights),
+        _ptr(grad_output), _ptr(grad_input), _ptr(grad_route), _ptr(d_gate_a), _ptr(d_gate_b), _ptr(d_up_a),
+        _ptr(d_up_b), _ptr(d_down_a), _ptr(d_down_b), int(bool(accumulate)), float(grad_scale), _ptr(workspace),
+        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_ckpt8_pack(x, rows, cols, format, codes, scales, stream=None) -> None:
+    _check(load_library().kt_ckpt8_pack(_ptr(x), rows, cols, format, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def kt_ckpt8_unpack(codes, scales, rows, cols, format, x, stream=None) -> None:
+    _check(load_library().kt_ckpt8_unpack(_ptr(codes), _ptr(scales), rows, cols, format, _ptr(x), _stream(stream)))
+
+
+def kt_router_fwd(router, tokens, logits, bias, token_mask, expert_ids, route_weights, load, accumulate,
+                  stream=None) -> None:
+    _check(load_library().kt_router_fwd(ctypes.byref(router), tokens, _ptr(logits), _ptr(bias), _ptr(token_mask),
+                                        _ptr(expert_ids), _ptr(route_weights), _ptr(load), int(bool(accumulate)),
+                                        _stream(stream)))
+
+
+def kt_router_bwd(router, tokens, logits, expert_ids, grad_route, grad_logits, stream=None) -> None:
+    _check(load_library().kt_router_bwd(ctypes.byref(router), tokens, _ptr(logits), _ptr(expert_ids),
+                                        _ptr(grad_route), _ptr(grad_logits), _stream(stream)))
+
+
+def kt_router_update_bias(bias, load, num_experts, rate, stream=None) -> None:
+    _check(load_library().kt_router_update_bias(_ptr(bias), _ptr(load), int(num_experts), float(rate),
+                                                _stream(stream)))
+
+
+def make_linear(weight, bias=None, activation="none") -> kt_linear:
+    """Fill the C struct of a dense layer from its weight [out, in]; the caller keeps the tensors alive."""
+    return kt_linear(int(weight.shape[1]), int(weight.shape[0]), ACTIVATIONS[activation], _ptr(weight), _ptr(bias))
+
+
+def _checked_size(n: int) -> int:
+    # a size of 0 is a valid answer; an error leaves its message
+    if n == 0 and kt_rawint4_last_error():
+        raise KtRawInt4Error(KT_RAWINT4_EINVAL, kt_rawint4_last_error())
+    return int(n)
+
+
+def kt_linear_workspace_bytes(linear, tokens) -> int:
+    return _checked_size(load_library().kt_linear_workspace_bytes(ctypes.byref(linear), int(tokens)))
+
+
+def kt_linear_fwd(linear, tokens, inputs, residual, output, output_type, preact, workspace, stream=None) -> None:
+    _check(load_library().kt_linear_fwd(ctypes.byref(linear), tokens, _ptr(inputs), _ptr(residual), _ptr(output),
+                                        output_type, _ptr(preact), _ptr(workspace),
+                                        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_linear_bwd_workspace_bytes(linear, tokens, from_checkpoint=False) -> int:
+    return _checked_size(load_library().kt_linear_bwd_workspace_bytes(ctypes.byref(linear), int(tokens),
+                                                                      int(bool(from_checkpoint))))
+
+
+def kt_linear_bwd(linear, tokens, inputs, checkpoint, preact, grad_output, grad_output_type, grad_residual, grad_input,
+                  d_weight, d_bias, accumulate, grad_scale, workspace, stream=None) -> None:
+    _check(load_library().kt_linear_bwd(
+        ctypes.byref(linear), tokens, _ptr(inputs), None if checkpoint is None else ctypes.byref(checkpoint),
+        _ptr(preact), _ptr(grad_output), grad_output_type, _ptr(grad_residual), _ptr(grad_input), _ptr(d_weight),
+        _ptr(d_bias), int(bool(accumulate)), float(grad_scale), _ptr(workspace),
         _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
 
 

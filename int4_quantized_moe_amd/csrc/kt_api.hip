@@ -234,6 +234,9 @@ static int launched(hipError_t err = hipSuccess) {
   return KT_RAWINT4_OK;
 }
 
+int finish_launches() { return launched(); }
+int check_caller_workspace(void* ws, size_t bytes, size_t need) { return check_workspace(ws, bytes, need); }
+
 static RowView view_tok_bf16(const uint16_t* p, int64_t ld, const float* slot_scale = nullptr) {
   RowView v{};
   v.kind = kSrcTokBf16;
@@ -472,16 +475,24 @@ int kt_rawint4_moe_infer(const kt_rawint4_moe_layer* layer, int32_t qlen, const 
   return run_forward(layer, d, inputs, expert_ids, route_weights, output, workspace, workspace_bytes, stream);
 }
 
+// bytes of a call's unpacked input rows
+static size_t ckpt8_rows_bytes(const Dims& d) { return align_up(2 * (size_t)d.qlen * (size_t)d.H); }
+
 // The backward; recompute: first rerun the forward's front into the workspace
-// (the checkpoint-recompute form, no saved forward needed).
+// (the checkpoint-recompute form, no saved forward needed).  With a checkpoint
+// in 8 bits (recompute only, inputs NULL), its rows are unpacked behind the
+// recompute's part of the workspace before anything else.
 static int run_backward(const kt_rawint4_moe_layer* layer, int32_t qlen, const uint16_t* inputs,
                         const int64_t* expert_ids, const float* route_weights, const uint16_t* grad_output,
                         uint16_t* grad_input, float* grad_route, float* d_gate_a, float* d_gate_b, float* d_up_a,
                         float* d_up_b, float* d_down_a, float* d_down_b, int32_t accumulate, float grad_scale,
-                        void* workspace, size_t workspace_bytes, void* stream, bool recompute) {
+                        void* workspace, size_t workspace_bytes, void* stream, bool recompute,
+                        const kt_ckpt8* ckpt = nullptr) {
   Dims d;
   int rc = check_layer(layer, qlen, &d);
   if (rc) return rc;
+  if (ckpt && ckpt->format != KT_CKPT8_INT8 && ckpt->format != KT_CKPT8_E4M3)
+    return fail(KT_RAWINT4_EINVAL, "format must be KT_CKPT8_INT8 or KT_CKPT8_E4M3");
   float* grads[6] = {d_gate_a, d_gate_b, d_up_a, d_up_b, d_down_a, d_down_b};
   for (float* g : grads) {
     if (!g) return fail(KT_RAWINT4_EINVAL, "the six LoRA gradient buffers must be non-NULL");
@@ -497,17 +508,25 @@ static int run_backward(const kt_rawint4_moe_layer* layer, int32_t qlen, const u
       for (int j = 0; j < 6; ++j) launch_fill_zero_f32(grads[j], gsz[j], st);
     return launched();
   }
-  if (!inputs || !expert_ids || !route_weights || !grad_output || !grad_input)
+  if (ckpt && (!ckpt->codes || !ckpt->scales)) return fail(KT_RAWINT4_EINVAL, "codes and scales must be non-NULL");
+  if (ckpt && (!aligned(ckpt->codes, 4) || !aligned(ckpt->scales, 4)))
+    return fail(KT_RAWINT4_EINVAL, "codes and scales must be 4-byte aligned");
+  if ((!inputs && !ckpt) || !expert_ids || !route_weights || !grad_output || !grad_input)
     return fail(KT_RAWINT4_EINVAL, "inputs, expert_ids, route_weights, grad_output and grad_input must be non-NULL");
   if (!aligned(inputs, 16) || !aligned(grad_output, 16) || !aligned(grad_input, 8) || !aligned(expert_ids, 8) ||
       !aligned(route_weights, 4) || (grad_route && !aligned(grad_route, 4)))
     return fail(KT_RAWINT4_EINVAL, "inputs and grad_output must be 16-byte aligned, grad_input 8-byte aligned");
   const WsMap w = plan_workspace(d);
-  rc = check_workspace(workspace, workspace_bytes, w.total);
+  rc = check_workspace(workspace, workspace_bytes, w.total + (ckpt ? ckpt8_rows_bytes(d) : 0));
   if (rc) return rc;
   const LayerPtrs L = layer_ptrs(layer);
   void* ws = workspace;
   begin_launches();
+  if (ckpt) {
+    uint16_t* rows = ws_ptr<uint16_t>(ws, w.total);
+    launch_ckpt8_unpack(ckpt->codes, ckpt->scales, d.qlen, d.H, ckpt->format, rows, st);
+    inputs = rows;
+  }
   if (recompute) launch_forward_front(layer, d, w, ws, L, inputs, expert_ids, route_weights, st);
 
   {
@@ -577,6 +596,23 @@ int kt_rawint4_moe_bwd_recompute(const kt_rawint4_moe_layer* layer, int32_t qlen
   return run_backward(layer, qlen, inputs, expert_ids, route_weights, grad_output, grad_input, grad_route, d_gate_a,
                       d_gate_b, d_up_a, d_up_b, d_down_a, d_down_b, accumulate, grad_scale, workspace,
                       workspace_bytes, stream, true);
+}
+
+size_t kt_moe_bwd_ckpt8_workspace_bytes(const kt_rawint4_moe_layer* layer, int32_t qlen) {
+  Dims d;
+  if (check_layer(layer, qlen, &d) != KT_RAWINT4_OK) return 0;
+  return plan_workspace(d).total + ckpt8_rows_bytes(d);
+}
+
+int kt_moe_bwd_ckpt8(const kt_rawint4_moe_layer* layer, int32_t qlen, int32_t format, const uint8_t* codes,
+                     const uint8_t* scales, const int64_t* expert_ids, const float* route_weights,
+                     const uint16_t* grad_output, uint16_t* grad_input, float* grad_route, float* d_gate_a,
+                     float* d_gate_b, float* d_up_a, float* d_up_b, float* d_down_a, float* d_down_b,
+                     int32_t accumulate, float grad_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const kt_ckpt8 ckpt{format, codes, scales};
+  return run_backward(layer, qlen, nullptr, expert_ids, route_weights, grad_output, grad_input, grad_route, d_gate_a,
+                      d_gate_b, d_up_a, d_up_b, d_down_a, d_down_b, accumulate, grad_scale, workspace,
+                      workspace_bytes, stream, true, &ckpt);
 }
 
 int kt_rawint4_unpack(const uint8_t* packed, int64_t n, int64_t k, int8_t* codes, void* stream) {

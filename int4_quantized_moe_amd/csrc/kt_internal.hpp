@@ -6,6 +6,7 @@
 #include <stdint.h>
 #include <stdlib.h>
 
+#include "../../include/kt_block.h"
 #include "../../include/kt_rawint4.h"
 
 namespace kt {
@@ -173,7 +174,19 @@ int run_forward_no_alloc(const kt_rawint4_moe_layer* layer, Dims d, const uint16
                          const int64_t* expert_ids, const float* route_weights, uint16_t* output, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+// The end of an entry point's launches: its first launch error as a return
+// code and message, or KT_RAWINT4_OK; the checks of a caller's workspace and of
+// a pointer's alignment.
+int finish_launches();
+int check_caller_workspace(void* ws, size_t bytes, size_t need);
+inline bool is_aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
+inline size_t round256(size_t v) { return (v + 255) & ~(size_t)255; }
+
 // ---------------------------------------------------------------- launchers (enqueue only)
+
+// 8-bit activation checkpoints (KT_CKPT8_*)
+void launch_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int format,
+                         uint16_t* x, hipStream_t st);
 
 void launch_group(const Dims& d, const WsMap& w, void* ws, const int64_t* ids, hipStream_t st);
 void launch_rows_to_half(const uint16_t* src, int64_t rows, int64_t cols, uint16_t* dst, int32_t* exps,
