@@ -53,16 +53,26 @@ __device__ __forceinline__ float act_slope(int act, float z) {
 
 // ---------------------------------------------------------------- product
 
-// C[m, n] = sum_k A(m, k) B(n, k) with A(m, k) = a[m * am + k * ak] and likewise
-// B, then the epilogue of one of the three products.
+// C[m, n] = sum_k A(m, k) B(n, k) with the epilogue of one of the three products:
+//   forward      A = x  [T][K]       B = W [N][K]       contraction contiguous in both
+//   grad_input   A = dz [T][N]       B = W [N][K]       contraction (N) contiguous in A, across B's rows
+//   d_weight     A = dz [T][N]       B = x [T][K]       contraction (T) across both operands' rows
+// An operand whose contraction is contiguous lies in memory as [rows][ld], the
+// other kind as [contraction][ld].
 enum LinearKind { kLinFwd, kLinDx, kLinDw };
+
+constexpr int kMaxPlanes = 3;
 
 struct LinearGemm {
   const uint16_t *a, *b;
-  int64_t am, ak, bn, bk;
+  int64_t lda, ldb;      // row pitch (elements, a multiple of 8)
+  int64_t a_width;       // columns of A's rows that exist (a multiple of 8), for a contraction across them
   int64_t M, N, K;
-  int planes;       // A is the sum of so many bf16 planes ...
-  int64_t a_plane;  // ... so many elements apart
+  int planes;            // A is the sum of so many bf16 planes ...
+  int64_t a_plane;       // ... so many elements apart
+  int splits;            // the steps of the contraction are dealt to so many blocks; over 1: part
+  float* part;           // [splits][M][pn] partial sums
+  int64_t pn;            // N rounded up to a multiple of 4
   // forward: bias, act, residual, out (type), preact; dx: residual, out; dw: out (fp32), accumulate, scale
   const float* bias;
   const uint16_t* residual;
@@ -74,81 +84,312 @@ struct LinearGemm {
   float scale;
 };
 
+// Outputs m, n .. n + 3 (n a multiple of 4; those below N exist).
 template <int KIND>
-__device__ __forceinline__ void finish(const LinearGemm& g, int64_t m, int64_t n, float v) {
+__device__ __forceinline__ void finish4(const LinearGemm& g, int64_t m, int64_t n, floatx4 v) {
   const int64_t i = m * g.N + n;
+  const bool whole = (g.N & 3) == 0;  // then every quad is whole and aligned
+  const int cnt = whole ? 4 : (int)(g.N - n < 4 ? g.N - n : 4);
   if (KIND == kLinDw) {
     float* o = static_cast<float*>(g.out) + i;
-    *o = (g.accumulate ? *o : 0.f) + g.scale * v;
+    if (whole) {
+      floatx4 old = {};
+      if (g.accumulate) old = *reinterpret_cast<floatx4*>(o);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) old[r] += g.scale * v[r];
+      *reinterpret_cast<floatx4*>(o) = old;
+    } else {
+      for (int r = 0; r < cnt; ++r) o[r] = (g.accumulate ? o[r] : 0.f) + g.scale * v[r];
+    }
     return;
   }
   if (KIND == kLinFwd) {
-    if (g.bias) v += g.bias[n];
-    if (g.preact) g.preact[i] = float_to_bf16(v);
-    v = act_value(g.act, v);
-  }
-  if (g.residual) v += bf16_to_float(g.residual[i]);
-  if (KIND == kLinFwd && g.out_f32)
-    static_cast<float*>(g.out)[i] = v;
-  else
-    static_cast<uint16_t*>(g.out)[i] = float_to_bf16(v);
-}
-
-// 64 x 64 outputs per block of four waves (32 x 32 each), 32 values of the
-// contraction per step, staged through LDS one element at a time.
-template <int KIND>
-__global__ __launch_bounds__(256) void k_linear(LinearGemm g) {
-  __shared__ __align__(16) uint16_t sa[64][40], sb[64][40];
-  const int64_t nt = (g.N + 63) / 64;
-  const int64_t m0 = (int64_t)blockIdx.x / nt * 64, n0 = (int64_t)blockIdx.x % nt * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  floatx4 acc[2][2] = {};
-  for (int p = 0; p < g.planes; ++p)
-    for (int64_t k0 = 0; k0 < g.K; k0 += 32) {
-      for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        // consecutive threads along the operand's contiguous direction
-        const int ra = g.ak == 1 ? i >> 5 : i & 63, ka = g.ak == 1 ? i & 31 : i >> 6;
-        const int rb = g.bk == 1 ? i >> 5 : i & 63, kb = g.bk == 1 ? i & 31 : i >> 6;
-        sa[ra][ka] = m0 + ra < g.M && k0 + ka < g.K ? g.a[p * g.a_plane + (m0 + ra) * g.am + (k0 + ka) * g.ak] : 0;
-        sb[rb][kb] = n0 + rb < g.N && k0 + kb < g.K ? g.b[(n0 + rb) * g.bn + (k0 + kb) * g.bk] : 0;
+    if (g.bias) {
+      if (whole) {
+        v += *reinterpret_cast<const floatx4*>(g.bias + n);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < cnt) v[r] += g.bias[n + r];
       }
-      __syncthreads();
-      u32x4 fa[2], fb[2];
+    }
+    if (g.preact) {
+      uint16_t z[4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        fa[q] = *reinterpret_cast<const u32x4*>(&sa[wm + 16 * q + (lane & 15)][8 * (lane >> 4)]);
-        fb[q] = *reinterpret_cast<const u32x4*>(&sb[wn + 16 * q + (lane & 15)][8 * (lane >> 4)]);
+      for (int r = 0; r < 4; ++r) z[r] = float_to_bf16(v[r]);
+      if (whole) {
+        *reinterpret_cast<u32x2*>(g.preact + i) = u32x2{pack2(z[0], z[1]), pack2(z[2], z[3])};
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (r < cnt) g.preact[i + r] = z[r];
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_bf16(fa[i], fb[j], acc[i][j]);
-      __syncthreads();
     }
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int r = 0; r < 4; ++r) v[r] = act_value(g.act, v[r]);
+  }
+  if (g.residual) {
+    if (whole) {
+      const u32x2 q = *reinterpret_cast<const u32x2*>(g.residual + i);
+      v[0] += bf16_to_float((uint16_t)q.x);
+      v[1] += bf16_to_float((uint16_t)(q.x >> 16));
+      v[2] += bf16_to_float((uint16_t)q.y);
+      v[3] += bf16_to_float((uint16_t)(q.y >> 16));
+    } else {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int r = 0; r < 4; ++r)
+        if (r < cnt) v[r] += bf16_to_float(g.residual[i + r]);
+    }
+  }
+  if (KIND == kLinFwd && g.out_f32) {
+    float* o = static_cast<float*>(g.out) + i;
+    if (whole) {
+      *reinterpret_cast<floatx4*>(o) = v;
+    } else {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t m = m0 + wm + 16 * i + 4 * (lane >> 4) + r, n = n0 + wn + 16 * j + (lane & 15);
-        if (m < g.M && n < g.N) finish<KIND>(g, m, n, acc[i][j][r]);
+      for (int r = 0; r < 4; ++r)
+        if (r < cnt) o[r] = v[r];
+    }
+  } else {
+    uint16_t* o = static_cast<uint16_t*>(g.out) + i;
+    if (whole) {
+      *reinterpret_cast<u32x2*>(o) =
+          u32x2{pack2(float_to_bf16(v[0]), float_to_bf16(v[1])), pack2(float_to_bf16(v[2]), float_to_bf16(v[3]))};
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (r < cnt) o[r] = float_to_bf16(v[r]);
+    }
+  }
+}
+
+// 16 zero bytes that copies past the end of a contraction read
+__device__ const uint32_t kZero16[4] = {0, 0, 0, 0};
+
+__device__ __forceinline__ uint64_t uniform64(const void* p) {
+  const uint64_t v = (uint64_t)p;
+  // (readfirstlane gives an int: without the casts the low half's sign would fill the high half)
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32));
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  return (uint64_t)hi << 32 | lo;
+}
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// dma16 with a wave-uniform base and a 32-bit byte offset per lane.  A load may read a scalar that a
+// vector instruction wrote (readfirstlane) after five wait states; the compiler does not see the load.
+__device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32_t lds_base) {
+  const uint32_t lb = __builtin_amdgcn_readfirstlane(lds_base);
+  const uint64_t ub = uniform64(base);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(ub), "s"(lb)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+constexpr int kLinBK = 64;  // contraction values per step
+
+// One operand's tile of R rows (or columns) x kLinBK contraction values in LDS,
+// R * 128 bytes, filled by 16-byte copies straight from memory: a wave's copy
+// fills 1024 consecutive bytes, so the arrangement is made on the source side.
+//
+// Contiguous contraction: row r at r * 128, its 16-byte chunk c (8 values) at
+// position c ^ (r & 7).  A fragment read takes one chunk of 16 consecutive
+// rows: the 8 rows of a 1 KiB block then lie on 8 different bank groups.
+//
+// Contraction across rows: value k of all R columns at k * 2R, the 32-byte pair
+// p (16 columns) at position p ^ h(k), h(k) = (k & 3) | (k >> 3 & 1) << 2.  A
+// fragment (16 columns x 8 values per lane) is two transposing reads, each of 4
+// values k for 16 columns per 16 lanes; h spreads the 8 rows that two
+// 16-lane groups read together over all banks.
+template <int R, bool ACROSS>
+struct LinTile {
+  static constexpr int kBytes = R * 2 * kLinBK;
+  static constexpr int kRowsPerCopy = ACROSS ? 512 / R : 8;
+  static constexpr int kCopies = kBytes / 1024;
+
+  // tile row (contraction value if ACROSS) and element within it that lane l of copy q fills
+  __device__ static void place(int q, int l, int& row, int& col) {
+    if (ACROSS) {
+      constexpr int kChunks = R / 8;
+      row = q * kRowsPerCopy + l / kChunks;
+      const int pos = l % kChunks, h = (row & 3) | ((row >> 3) & 1) << 2;
+      col = (((pos >> 1) ^ h) * 2 + (pos & 1)) * 8;
+    } else {
+      row = q * 8 + (l >> 3);
+      col = ((l & 7) ^ (row & 7)) * 8;
+    }
+  }
+
+  // the 8 contraction values ks * 32 + 8 (lane / 16) .. + 7 of row (column) r0 + lane % 16
+  __device__ static u32x4 fragment(const uint8_t* tile, int r0, int ks, int lane) {
+    const int g = lane >> 4, j = lane & 15;
+    if (ACROSS) {
+      const int h = (j >> 2) | (g & 1) << 2;
+      const uint8_t* p = tile + (ks * 32 + 8 * g + (j >> 2)) * (2 * R) + (((r0 >> 4) ^ h) * 32) + (j & 3) * 8;
+      typedef short4_t __attribute__((address_space(3))) * lds_p;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(p)));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(p + 8 * R)));
+      return u32x4{lo.x, lo.y, hi.x, hi.y};
+    }
+    const int row = r0 + j;
+    return *reinterpret_cast<const u32x4*>(tile + row * 128 + (((ks * 4 + g) ^ (row & 7)) * 16));
+  }
+};
+
+// A block of WM x WN waves computes BM x BN outputs, each wave BM / WM x BN / WN
+// of them as 16 x 16 MFMA tiles.  Two LDS buffers: while one step's tiles are
+// multiplied, the next step's are copied into the other.
+template <int KIND, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
+  constexpr bool kAcrossA = KIND == kLinDw, kAcrossB = KIND != kLinFwd;
+  typedef LinTile<BM, kAcrossA> TA;
+  typedef LinTile<BN, kAcrossB> TB;
+  constexpr int kWaves = WM * WN, kFm = BM / WM / 16, kFn = BN / WN / 16;
+  constexpr int kCa = TA::kCopies / kWaves, kCb = TB::kCopies / kWaves;
+  __shared__ __align__(1024) uint8_t lds[2][TA::kBytes + TB::kBytes];
+
+  // tiles: each XCD (blocks reach them in turn) takes a contiguous run of the
+  // order below, in which kGroup rows of tiles are walked column by column, so
+  // that the operand rows a run shares stay in that XCD's L2
+  constexpr int kGroup = 4;
+  const int mt = (int)((g.M + BM - 1) / BM), nt = (int)((g.N + BN - 1) / BN), tiles = mt * nt;
+  const int xcd = blockIdx.x & 7, q8 = tiles >> 3, r8 = tiles & 7;
+  const int tile = __builtin_amdgcn_readfirstlane(xcd * q8 + min(xcd, r8) + (int)(blockIdx.x >> 3));
+  const int span = kGroup * nt, grp = tile / span, in = tile - grp * span;
+  const int rows = min(kGroup, mt - grp * kGroup);
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(grp * kGroup + in % rows) * BM;
+  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(in / rows) * BN;
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the steps of this split: planes one after another, each of ceil(K / 64)
+  const int per_plane = (int)((g.K + kLinBK - 1) / kLinBK), total = per_plane * g.planes;
+  const int s0 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * blockIdx.y / g.splits));
+  const int s1 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * (blockIdx.y + 1) / g.splits));
+
+  // byte offsets of this lane's copies from the tile's first element; rows and
+  // columns past the operand's end repeat its last ones (their outputs are not stored)
+  uint32_t off_a[kCa], off_b[kCb];
+#pragma unroll
+  for (int c = 0; c < kCa; ++c) {
+    int row, col;
+    TA::place(wave * kCa + c, lane, row, col);
+    off_a[c] = kAcrossA ? (uint32_t)((row * g.lda + min((int64_t)col, g.a_width - 8 - m0)) * 2)
+                        : (uint32_t)((min((int64_t)row, g.M - 1 - m0) * g.lda + col) * 2);
+  }
+#pragma unroll
+  for (int c = 0; c < kCb; ++c) {
+    int row, col;
+    TB::place(wave * kCb + c, lane, row, col);
+    off_b[c] = kAcrossB ? (uint32_t)((row * g.ldb + min((int64_t)col, g.ldb - 8 - n0)) * 2)
+                        : (uint32_t)((min((int64_t)row, g.N - 1 - n0) * g.ldb + col) * 2);
+  }
+  const uint8_t* base_a = reinterpret_cast<const uint8_t*>(g.a + (kAcrossA ? m0 : m0 * g.lda));
+  const uint8_t* base_b = reinterpret_cast<const uint8_t*>(g.b + (kAcrossB ? n0 : n0 * g.ldb));
+  const int64_t step_a = kAcrossA ? 2 * kLinBK * g.lda : 2 * kLinBK, step_b = kAcrossB ? 2 * kLinBK * g.ldb : 2 * kLinBK;
+
+  int p = __builtin_amdgcn_readfirstlane(s0 / per_plane), ks = s0 - p * per_plane;  // plane and step of the next copy
+  auto copy = [&](int buf) {
+    const uint8_t* pa = base_a + 2 * p * g.a_plane + ks * step_a;
+    const uint8_t* pb = base_b + ks * step_b;
+    const uint32_t la = lds_addr(&lds[buf][0]) + wave * kCa * 1024;
+    const uint32_t lb = lds_addr(&lds[buf][TA::kBytes]) + wave * kCb * 1024;
+    if ((int64_t)(ks + 1) * kLinBK <= g.K) {
+#pragma unroll
+      for (int c = 0; c < kCa; ++c) dma16_off(pa, off_a[c], la + c * 1024);
+#pragma unroll
+      for (int c = 0; c < kCb; ++c) dma16_off(pb, off_b[c], lb + c * 1024);
+    } else {
+      const int left = (int)(g.K - (int64_t)ks * kLinBK);  // values that exist
+#pragma unroll
+      for (int c = 0; c < kCa; ++c) {
+        int row, col;
+        TA::place(wave * kCa + c, lane, row, col);
+        dma16((kAcrossA ? row : col) < left ? (const void*)(pa + off_a[c]) : kZero16, la + c * 1024);
       }
+#pragma unroll
+      for (int c = 0; c < kCb; ++c) {
+        int row, col;
+        TB::place(wave * kCb + c, lane, row, col);
+        dma16((kAcrossB ? row : col) < left ? (const void*)(pb + off_b[c]) : kZero16, lb + c * 1024);
+      }
+    }
+    if (++ks == per_plane) {
+      ks = 0;
+      ++p;
+    }
+  };
+
+  const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
+  floatx4 acc[kFm][kFn] = {};
+  if (s0 < s1) copy(0);
+  for (int s = s0; s < s1; ++s) {
+    const int buf = (s - s0) & 1;
+    // this step's copies of every wave have landed, and every wave has read the other buffer
+    wait_vm_lgkm<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (s + 1 < s1) copy(buf ^ 1);
+    const uint8_t* ta = &lds[buf][0];
+    const uint8_t* tb = &lds[buf][TA::kBytes];
+#pragma unroll
+    for (int h = 0; h < kLinBK / 32; ++h) {
+      u32x4 fa[kFm], fb[kFn];
+#pragma unroll
+      for (int j = 0; j < kFn; ++j) fb[j] = TB::fragment(tb, wn + 16 * j, h, lane);
+#pragma unroll
+      for (int i = 0; i < kFm; ++i) fa[i] = TA::fragment(ta, wm + 16 * i, h, lane);
+#pragma unroll
+      for (int i = 0; i < kFm; ++i)
+#pragma unroll
+        for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
+    }
+  }
+  // lane: m = lane % 16 of its tile, n = 4 (lane / 16) .. + 3
+#pragma unroll
+  for (int i = 0; i < kFm; ++i) {
+    const int64_t m = m0 + wm + 16 * i + (lane & 15);
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int j = 0; j < kFn; ++j) {
+      const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
+      if (n >= g.N) continue;
+      if (g.splits > 1)
+        *reinterpret_cast<floatx4*>(g.part + ((int64_t)blockIdx.y * g.M + m) * g.pn + n) = acc[i][j];
+      else
+        finish4<KIND>(g, m, n, acc[i][j]);
+    }
+  }
+}
+
+// The splits' partial sums, in their order, and the epilogue.
+template <int KIND>
+__global__ __launch_bounds__(256) void k_linear_join(LinearGemm g) {
+  const int64_t quads = g.pn / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= g.M * quads) return;
+  const int64_t m = i / quads, n = (i - m * quads) * 4;
+  const float* p = g.part + m * g.pn + n;
+  floatx4 v = *reinterpret_cast<const floatx4*>(p);
+  for (int s = 1; s < g.splits; ++s) v += *reinterpret_cast<const floatx4*>(p + s * g.M * g.pn);
+  finish4<KIND>(g, m, n, v);
 }
 
 // ---------------------------------------------------------------- dz and its column sums
 
-// dz = grad_output * act'(preact) as one or two bf16 planes (hi and, where a
-// product needs more than bf16 holds, lo = bf16(dz - hi)).
+// dz = grad_output * act'(preact) as bf16 planes that sum to it: one for
+// grad_input, three (24 bits: dz itself, but for the smallest parts) for d_weight.
 struct DzArgs {
   const void* dy;
   int dy_f32;
   const uint16_t* z;
   int act;
-  int64_t T, N;
-  uint16_t *hi, *lo;
-  float* part;  // [row blocks][N] column sums
+  int64_t T, N, pitch;  // planes are [T][pitch], zeros from N on
+  uint16_t* plane;
+  int64_t plane_size;   // elements from one plane to the next
+  int planes;
+  float* part;          // [row blocks][N] column sums
 };
 
 __device__ __forceinline__ float dz_at(const DzArgs& a, int64_t i) {
@@ -160,17 +401,17 @@ __device__ __forceinline__ float dz_at(const DzArgs& a, int64_t i) {
   return dy * act_slope(a.act, z);
 }
 
-// hi + lo with a relative error of at most 2^-17; the sum stays finite where v is, and infinite
-// where v is infinite.
-__device__ __forceinline__ void split_planes(float v, uint16_t& hi, uint16_t& lo) {
-  split_bf16(v, hi, lo);
-  if ((hi & 0x7fff) == 0x7f80) {
-    if (fabsf(v) < INFINITY) {
-      hi -= 1;  // the largest finite number of bf16
-      lo = float_to_bf16(v - bf16_to_float(hi));
-    } else {
-      lo = 0;
-    }
+// The planes of v: each the nearest bf16 number to what the ones before leave.
+// An infinite v is one infinite plane; a finite v above bf16's largest number
+// starts with that number, so that the sum stays finite.
+__device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes]) {
+  float rest = v;
+#pragma unroll
+  for (int q = 0; q < kMaxPlanes; ++q) {
+    uint16_t h = float_to_bf16(rest);
+    if ((h & 0x7fff) == 0x7f80 && fabsf(rest) < INFINITY) h -= 1;
+    p[q] = h;
+    rest = (h & 0x7f80) == 0x7f80 ? 0.f : rest - bf16_to_float(h);
   }
 }
 
@@ -182,17 +423,17 @@ __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
   const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int64_t n = (int64_t)blockIdx.x * 64 + c;
   float sum = 0.f;
-  if (n < a.N)
+  if (n < a.pitch)
     for (int r = q; r < kDzRows; r += 4) {
       const int64_t t = (int64_t)blockIdx.y * kDzRows + r;
       if (t >= a.T) break;
-      const int64_t i = t * a.N + n;
-      const float v = dz_at(a, i);
+      const float v = n < a.N ? dz_at(a, t * a.N + n) : 0.f;
       sum += v;
-      uint16_t hi, lo;
-      split_planes(v, hi, lo);
-      if (a.hi) a.hi[i] = hi;
-      if (a.lo) a.lo[i] = lo;
+      if (a.plane) {
+        uint16_t p[kMaxPlanes];
+        split_planes(v, p);
+        for (int k = 0; k < a.planes; ++k) a.plane[k * a.plane_size + t * a.pitch + n] = p[k];
+      }
     }
   red[q][c] = sum;
   __syncthreads();
@@ -226,28 +467,76 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
   return KT_RAWINT4_OK;
 }
 
+// Splits of a product whose tiles alone would leave compute units idle: enough
+// blocks for two rounds of the chip, each with at least kMinSteps steps.
+constexpr int kBlocksWanted = 512, kMinSteps = 4, kMaxSplits = 64;
+
+struct LinearShape {
+  bool big;  // 256 x 256 tiles (else 128 x 128)
+  int64_t tiles;
+  int splits;
+};
+
+static LinearShape linear_shape(int64_t M, int64_t N, int64_t steps) {
+  LinearShape s;
+  const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
+  s.big = big >= 192;
+  s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
+  int64_t splits = s.big || s.tiles == 0 ? 1 : kBlocksWanted / s.tiles;
+  if (splits > steps / kMinSteps) splits = steps / kMinSteps;
+  if (splits > kMaxSplits) splits = kMaxSplits;
+  s.splits = splits > 1 ? (int)splits : 1;
+  return s;
+}
+
+static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+static size_t part_bytes(const LinearShape& s, int64_t M, int64_t N) {
+  return s.splits > 1 ? round256(4 * (size_t)s.splits * (size_t)M * (size_t)round_up(N, 4)) : 0;
+}
+
+static int64_t contraction_steps(int64_t K, int planes) { return (K + kLinBK - 1) / kLinBK * planes; }
+
+// The workspace of a backward.  Every part has room of its own except the
+// splits' partial sums, which the two products use one after the other.
 struct LinearBwdPlan {
-  size_t hi, lo, part, x, total;
-  int64_t nb;
+  LinearShape dx, dw;
+  size_t planes, part, db, x, total;
+  int64_t pitch, nb;
 };
 
 static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   LinearBwdPlan p{};
-  const size_t plane = round256(2 * (size_t)T * (size_t)L->out_features);
+  const int64_t N = L->out_features, K = L->in_features;
+  p.pitch = round_up(N, 8);
   p.nb = (T + kDzRows - 1) / kDzRows;
-  p.hi = 0;
-  p.lo = p.hi + plane;
-  p.part = p.lo + plane;
-  p.x = p.part + round256(4 * (size_t)p.nb * (size_t)L->out_features);
-  p.total = p.x + (ckpt ? round256(2 * (size_t)T * (size_t)L->in_features) : 0);
+  // the shapes of calls with one plane need no more
+  p.dx = linear_shape(T, K, contraction_steps(N, 1));
+  p.dw = linear_shape(N, K, contraction_steps(T, kMaxPlanes));
+  p.planes = 0;
+  p.db = p.planes + round256(2 * kMaxPlanes * (size_t)T * (size_t)p.pitch);
+  p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
+  const size_t a = part_bytes(p.dx, T, K), b = part_bytes(p.dw, N, K);
+  p.x = p.part + (a > b ? a : b);
+  p.total = p.x + (ckpt ? round256(2 * (size_t)T * (size_t)K) : 0);
   return p;
 }
 
 template <int KIND>
-static void launch_linear(const LinearGemm& g, hipStream_t st) {
-  const int64_t blocks = (g.M + 63) / 64 * ((g.N + 63) / 64);
-  k_linear<KIND><<<(unsigned)blocks, 256, 0, st>>>(g);
+static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipStream_t st) {
+  g.splits = s.splits;
+  g.part = part;
+  g.pn = round_up(g.N, 4);
+  const dim3 grid((unsigned)s.tiles, (unsigned)s.splits);
+  if (s.big)
+    k_linear<KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
+  else
+    k_linear<KIND, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g);
   note_launch();
+  if (s.splits > 1) {
+    k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 4) + 255) / 256), 256, 0, st>>>(g);
+    note_launch();
+  }
 }
 
 }  // namespace kt
@@ -259,7 +548,8 @@ extern "C" {
 size_t kt_linear_workspace_bytes(const kt_linear* linear, int32_t tokens) {
   if (check_linear(linear, tokens)) return 0;
   (void)set_error(KT_RAWINT4_OK, "");  // 0 is a valid size: no message stays
-  return 0;
+  return part_bytes(linear_shape(tokens, linear->out_features, contraction_steps(linear->in_features, 1)), tokens,
+                    linear->out_features);
 }
 
 int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* inputs, const uint16_t* residual,
@@ -273,17 +563,19 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   if (!is_aligned(inputs, 16) || !is_aligned(residual, 16) || !is_aligned(output, 16) || !is_aligned(preact, 16))
     return set_error(KT_RAWINT4_EINVAL, "inputs, residual, output and preact must be 16-byte aligned");
   const int64_t K = linear->in_features, N = linear->out_features;
-  (void)workspace;
-  (void)workspace_bytes;
+  const LinearShape s = linear_shape(tokens, N, contraction_steps(K, 1));
+  const size_t need = part_bytes(s, tokens, N);
+  if (need) {
+    rc = check_caller_workspace(workspace, workspace_bytes, need);
+    if (rc) return rc;
+  }
   begin_launches();
   if (tokens > 0) {
     LinearGemm g{};
     g.a = inputs;
-    g.am = K;
-    g.ak = 1;
+    g.lda = K;
     g.b = linear->weight;
-    g.bn = K;
-    g.bk = 1;
+    g.ldb = K;
     g.M = tokens;
     g.N = N;
     g.K = K;
@@ -294,7 +586,7 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.out_f32 = output_type == KT_TYPE_F32;
     g.preact = preact;
     g.act = linear->activation;
-    launch_linear<kLinFwd>(g, static_cast<hipStream_t>(stream));
+    launch_linear<kLinFwd>(g, s, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
   }
   return finish_launches();
 }
@@ -342,9 +634,11 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   rc = check_caller_workspace(workspace, workspace_bytes, p.total);
   if (rc) return rc;
   begin_launches();
-  // a bf16 grad_output without activation is dz itself
-  const bool direct = !act && grad_output_type == KT_TYPE_BF16;
+  // a bf16 grad_output without activation is dz itself (its rows must start at 16 bytes)
+  const bool exact = !act && grad_output_type == KT_TYPE_BF16, direct = exact && N % 8 == 0;
   const uint16_t* dz = static_cast<const uint16_t*>(grad_output);
+  const int64_t pitch = direct ? N : p.pitch;
+  const int planes = exact || !d_weight ? 1 : kMaxPlanes;
   if (!direct || d_bias) {
     DzArgs a{};
     a.dy = grad_output;
@@ -353,12 +647,14 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     a.act = linear->activation;
     a.T = T;
     a.N = N;
-    a.hi = direct ? nullptr : ws_ptr<uint16_t>(workspace, p.hi);
-    a.lo = direct || !d_weight ? nullptr : ws_ptr<uint16_t>(workspace, p.lo);
-    a.part = d_bias ? ws_ptr<float>(workspace, p.part) : nullptr;
-    k_linear_dz<<<dim3((unsigned)((N + 63) / 64), (unsigned)p.nb), 256, 0, st>>>(a);
+    a.pitch = p.pitch;
+    a.plane = direct ? nullptr : ws_ptr<uint16_t>(workspace, p.planes);
+    a.plane_size = T * p.pitch;
+    a.planes = planes;
+    a.part = d_bias ? ws_ptr<float>(workspace, p.db) : nullptr;
+    k_linear_dz<<<dim3((unsigned)((p.pitch + 63) / 64), (unsigned)p.nb), 256, 0, st>>>(a);
     note_launch();
-    if (!direct) dz = a.hi;
+    if (!direct) dz = a.plane;
     if (d_bias) {
       k_linear_db<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(a.part, p.nb, N, d_bias, accumulate, grad_scale);
       note_launch();
@@ -367,18 +663,16 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   LinearGemm g{};
   if (grad_input) {
     g.a = dz;
-    g.am = N;
-    g.ak = 1;
+    g.lda = pitch;
     g.b = linear->weight;
-    g.bn = 1;
-    g.bk = K;
+    g.ldb = K;
     g.M = T;
     g.N = K;
     g.K = N;
     g.planes = 1;
     g.residual = grad_residual;
     g.out = grad_input;
-    launch_linear<kLinDx>(g, st);
+    launch_linear<kLinDx>(g, p.dx, ws_ptr<float>(workspace, p.part), st);
   }
   if (d_weight) {
     const uint16_t* x = inputs;
@@ -389,20 +683,20 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     }
     g = LinearGemm{};
     g.a = dz;
-    g.am = 1;
-    g.ak = N;
+    g.lda = pitch;
+    g.a_width = pitch;
     g.b = x;
-    g.bn = 1;
-    g.bk = K;
+    g.ldb = K;
     g.M = N;
     g.N = K;
     g.K = T;
-    g.planes = direct ? 1 : 2;
-    g.a_plane = (int64_t)(p.lo - p.hi) / 2;
+    g.planes = planes;
+    g.a_plane = T * p.pitch;
     g.out = d_weight;
     g.accumulate = accumulate;
     g.scale = grad_scale;
-    launch_linear<kLinDw>(g, st);
+    const LinearShape s = linear_shape(N, K, contraction_steps(T, planes));
+    launch_linear<kLinDw>(g, s, ws_ptr<float>(workspace, p.part), st);
   }
   return finish_launches();
 }
