@@ -129,7 +129,8 @@ int kt_router_update_bias(float* bias, const int32_t* load, int32_t num_experts,
  * Error of a value: at most amax / 127 (INT8), or max(2^-4 |x|, 2^-17 amax)
  * (E4M3), amax the group's largest magnitude (and up to 2^-128 where the
  * exponent is at its lowest).
- * x must be 16-byte aligned, codes and scales 4-byte; rows * cols below 2^40.
+ * x must be 16-byte aligned, codes and scales 4-byte; at most
+ * 2^32 groups a call.
  */
 int kt_ckpt8_pack(const uint16_t* x, int64_t rows, int64_t cols, int32_t format, uint8_t* codes, uint8_t* scales,
                   void* stream);

@@ -47,81 +47,224 @@ __device__ __forceinline__ uint32_t ckpt8_code(float v, float inv, float limit) 
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, 0.f, 0, false) & 0xffu;
 }
 
-template <int FMT>
-__device__ __forceinline__ float ckpt8_value(uint32_t code) {
-  if (FMT == KT_CKPT8_INT8) return (float)(int8_t)code;
-  return __builtin_amdgcn_cvt_f32_fp8((int)code, 0);
-}
-
 // The scale a byte stands for; NaN for 255.
 __device__ __forceinline__ float ckpt8_mult(int byte) {
   return byte == 255 ? __uint_as_float(0x7fc00000u) : pow2f(byte - 127);
 }
 
-// Any column count: half a wave per group, one value per lane.
-template <int FMT>
-__global__ __launch_bounds__(256) void k_ckpt8_pack(const uint16_t* __restrict__ x, int64_t rows, int64_t cols,
-                                                    int64_t ng, uint8_t* __restrict__ codes,
-                                                    uint8_t* __restrict__ scales) {
-  const int64_t total = rows * ng;
-  const int lane = threadIdx.x & 31;
-  for (int64_t g = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); g < total; g += (int64_t)gridDim.x * 8) {
-    const int64_t row = g / ng, c = (g - row * ng) * 32 + lane;
-    const bool in = c < cols;
-    const uint32_t bits = in ? (uint32_t)x[row * cols + c] << 16 : 0u;
-    uint32_t a = bits & 0x7fffffffu;
+// Two neighbouring lanes share a group, 16 values each: two 16-byte loads and
+// one 16-byte store a lane.  FLAT: rows are whole groups, so the tensor is one
+// run of groups.  Otherwise rows start at any 2-byte (codes: 1-byte) address, for
+// which the hardware's unaligned accesses serve as well, and the last group
+// of a row, if it is shorter, goes value by value.
+struct Ckpt8Args {
+  int64_t rows, cols, ng;  // ng: groups per row
+  const uint16_t* x;
+  uint8_t* codes;
+  uint8_t* scales;
+  uint16_t* y;
+};
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_byte __attribute__((aligned(1)));
+
+// start of half group i (2 per group) in the tensor and how many of its 16 values exist
+template <bool FLAT>
+__device__ __forceinline__ int64_t half_group(const Ckpt8Args& a, int64_t i, int& n) {
+  if (FLAT) {
+    n = 16;
+    return i * 16;
+  }
+  const int64_t g = i >> 1;
+  int64_t row;
+  if (a.rows * a.ng < ((int64_t)1 << 31))
+    row = (uint32_t)g / (uint32_t)a.ng;
+  else
+    row = g / a.ng;
+  const int64_t c = (g - row * a.ng) * 32 + (i & 1) * 16, left = a.cols - c;
+  n = left >= 16 ? 16 : left > 0 ? (int)left : 0;
+  return row * a.cols + c;
+}
+
+template <int FMT, bool FLAT, int UNITS>
+__global__ __launch_bounds__(256) void k_ckpt8_pack(Ckpt8Args a) {
+  const int64_t total = a.rows * a.ng * 2, i0 = (int64_t)blockIdx.x * (256 * UNITS) + threadIdx.x;
+  uint32_t w[UNITS][8];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) a = max(a, (uint32_t)__shfl_xor((int)a, off));
-    const int s = ckpt8_scale<FMT>(a);
-    const uint32_t code = s == 255 ? 0u : ckpt8_code<FMT>(__uint_as_float(bits), pow2f(127 - s), ckpt8_limit<FMT>(s));
-    if (in) codes[row * cols + c] = (uint8_t)code;
-    if (lane == 0) scales[g] = (uint8_t)s;
+  for (int u = 0; u < UNITS; ++u) {
+    const int64_t i = i0 + u * 256;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[u][q] = 0;
+    if (i >= total) continue;
+    int n;
+    const int64_t at = half_group<FLAT>(a, i, n);
+    if (FLAT || n == 16) {
+      const u32x4 p = *reinterpret_cast<const u32x4_any*>(a.x + at), q = *reinterpret_cast<const u32x4_any*>(a.x + at + 8);
+      w[u][0] = p.x, w[u][1] = p.y, w[u][2] = p.z, w[u][3] = p.w;
+      w[u][4] = q.x, w[u][5] = q.y, w[u][6] = q.z, w[u][7] = q.w;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (q < n) w[u][q >> 1] |= (uint32_t)a.x[at + q] << (16 * (q & 1));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int64_t i = i0 + u * 256;
+    uint32_t hi = 0, lo = 0;  // largest magnitudes of the high and low halves
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      hi = max(hi, w[u][q] & 0x7fff0000u);
+      lo = max(lo, w[u][q] & 0x7fffu);
+    }
+    uint32_t amax = max(hi, lo << 16);
+    // the other lane of the group (both are in the range or neither)
+    amax = max(amax, (uint32_t)__builtin_amdgcn_mov_dpp((int)amax, 0xB1, 0xf, 0xf, true));
+    if (i >= total) continue;
+    const int s = ckpt8_scale<FMT>(amax);
+    const float inv = s == 255 ? 0.f : pow2f(127 - s), limit = ckpt8_limit<FMT>(s);
+    uint32_t c[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t v = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t d = w[u][2 * q + h];
+        v |= (ckpt8_code<FMT>(__uint_as_float(d << 16), inv, limit) |
+              ckpt8_code<FMT>(__uint_as_float(d & 0xffff0000u), inv, limit) << 8)
+             << (16 * h);
+      }
+      c[q] = s == 255 ? 0u : v;
+    }
+    int n;
+    const int64_t at = half_group<FLAT>(a, i, n);
+    if (FLAT || n == 16) {
+      *reinterpret_cast<u32x4_byte*>(a.codes + at) = u32x4{c[0], c[1], c[2], c[3]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (q < n) a.codes[at + q] = (uint8_t)(c[q >> 2] >> (8 * (q & 3)));
+    }
+    if ((i & 1) == 0) a.scales[i >> 1] = (uint8_t)s;
   }
 }
 
-template <int FMT>
-__global__ __launch_bounds__(256) void k_ckpt8_unpack(const uint8_t* __restrict__ codes,
-                                                      const uint8_t* __restrict__ scales, int64_t rows, int64_t cols,
-                                                      int64_t ng, uint16_t* __restrict__ x) {
-  const int64_t total = rows * ng;
-  const int lane = threadIdx.x & 31;
-  for (int64_t g = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); g < total; g += (int64_t)gridDim.x * 8) {
-    const int64_t row = g / ng, c = (g - row * ng) * 32 + lane;
-    if (c < cols) x[row * cols + c] = float_to_bf16(ckpt8_value<FMT>(codes[row * cols + c]) * ckpt8_mult(scales[g]));
+// Two values of a code dword (low or high half) times the group's scale as two bf16.
+template <int FMT, bool HIGH>
+__device__ __forceinline__ uint32_t ckpt8_pair(uint32_t c, float mult) {
+  float v0, v1;
+  if (FMT == KT_CKPT8_INT8) {
+    v0 = (float)(int8_t)(c >> (HIGH ? 16 : 0));
+    v1 = (float)(int8_t)(c >> (HIGH ? 24 : 8));
+  } else {
+    const float2_t f = __builtin_amdgcn_cvt_pk_f32_fp8((int)c, HIGH);
+    v0 = f.x;
+    v1 = f.y;
+  }
+  v0 *= mult;
+  v1 *= mult;
+  return pack2(float_to_bf16(v0), float_to_bf16(v1));
+}
+
+template <int FMT, bool FLAT, int UNITS>
+__global__ __launch_bounds__(256) void k_ckpt8_unpack(Ckpt8Args a) {
+  const int64_t total = a.rows * a.ng * 2, i0 = (int64_t)blockIdx.x * (256 * UNITS) + threadIdx.x;
+  uint32_t c[UNITS][4];
+  int s[UNITS];
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int64_t i = i0 + u * 256;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) c[u][q] = 0;
+    s[u] = 0;
+    if (i >= total) continue;
+    s[u] = a.scales[i >> 1];
+    int n;
+    const int64_t at = half_group<FLAT>(a, i, n);
+    if (FLAT || n == 16) {
+      const u32x4 v = *reinterpret_cast<const u32x4_byte*>(a.codes + at);
+      c[u][0] = v.x, c[u][1] = v.y, c[u][2] = v.z, c[u][3] = v.w;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (q < n) c[u][q >> 2] |= (uint32_t)a.codes[at + q] << (8 * (q & 3));
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) {
+    const int64_t i = i0 + u * 256;
+    if (i >= total) continue;
+    const float mult = ckpt8_mult(s[u]);
+    uint32_t o[8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      o[2 * q] = ckpt8_pair<FMT, false>(c[u][q], mult);
+      o[2 * q + 1] = ckpt8_pair<FMT, true>(c[u][q], mult);
+    }
+    int n;
+    const int64_t at = half_group<FLAT>(a, i, n);
+    if (FLAT || n == 16) {
+      *reinterpret_cast<u32x4_any*>(a.y + at) = u32x4{o[0], o[1], o[2], o[3]};
+      *reinterpret_cast<u32x4_any*>(a.y + at + 8) = u32x4{o[4], o[5], o[6], o[7]};
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (q < n) a.y[at + q] = (uint16_t)(o[q >> 1] >> (16 * (q & 1)));
+    }
   }
 }
 
-static unsigned group_blocks(int64_t groups) {
-  const int64_t b = (groups + 7) / 8;
-  return (unsigned)(b < 65536 ? b : 65536);
+template <int FMT, bool FLAT, int UNITS>
+static void launch_ckpt8_as(const Ckpt8Args& a, bool pack, hipStream_t st) {
+  const int64_t blocks = (a.rows * a.ng * 2 + 256 * UNITS - 1) / (256 * UNITS);
+  if (pack)
+    k_ckpt8_pack<FMT, FLAT, UNITS><<<(unsigned)blocks, 256, 0, st>>>(a);
+  else
+    k_ckpt8_unpack<FMT, FLAT, UNITS><<<(unsigned)blocks, 256, 0, st>>>(a);
+  note_launch();
+}
+
+template <int FMT, bool FLAT>
+static void launch_ckpt8_units(const Ckpt8Args& a, bool pack, hipStream_t st) {
+  // four units a thread keep more loads in flight once the chip is full without them
+  if (a.rows * a.ng * 2 >= (int64_t)8 * 256 * 1024)
+    launch_ckpt8_as<FMT, FLAT, 4>(a, pack, st);
+  else
+    launch_ckpt8_as<FMT, FLAT, 1>(a, pack, st);
+}
+
+static void launch_ckpt8(Ckpt8Args a, int format, bool pack, hipStream_t st) {
+  a.ng = (a.cols + 31) / 32;
+  if (a.rows * a.ng == 0) return;
+  const bool flat = a.cols % 32 == 0;
+  if (format == KT_CKPT8_INT8) {
+    if (flat)
+      launch_ckpt8_units<KT_CKPT8_INT8, true>(a, pack, st);
+    else
+      launch_ckpt8_units<KT_CKPT8_INT8, false>(a, pack, st);
+  } else {
+    if (flat)
+      launch_ckpt8_units<KT_CKPT8_E4M3, true>(a, pack, st);
+    else
+      launch_ckpt8_units<KT_CKPT8_E4M3, false>(a, pack, st);
+  }
 }
 
 static void launch_ckpt8_pack(const uint16_t* x, int64_t rows, int64_t cols, int format, uint8_t* codes,
                               uint8_t* scales, hipStream_t st) {
-  const int64_t ng = (cols + 31) / 32;
-  if (rows * ng == 0) return;
-  if (format == KT_CKPT8_INT8)
-    k_ckpt8_pack<KT_CKPT8_INT8><<<group_blocks(rows * ng), 256, 0, st>>>(x, rows, cols, ng, codes, scales);
-  else
-    k_ckpt8_pack<KT_CKPT8_E4M3><<<group_blocks(rows * ng), 256, 0, st>>>(x, rows, cols, ng, codes, scales);
-  note_launch();
+  launch_ckpt8({rows, cols, 0, x, codes, scales, nullptr}, format, true, st);
 }
 
 void launch_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, int format,
                          uint16_t* x, hipStream_t st) {
-  const int64_t ng = (cols + 31) / 32;
-  if (rows * ng == 0) return;
-  if (format == KT_CKPT8_INT8)
-    k_ckpt8_unpack<KT_CKPT8_INT8><<<group_blocks(rows * ng), 256, 0, st>>>(codes, scales, rows, cols, ng, x);
-  else
-    k_ckpt8_unpack<KT_CKPT8_E4M3><<<group_blocks(rows * ng), 256, 0, st>>>(codes, scales, rows, cols, ng, x);
-  note_launch();
+  launch_ckpt8({rows, cols, 0, nullptr, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), x}, format, false,
+               st);
 }
 
 static int check_ckpt8(const void* x, int64_t rows, int64_t cols, int32_t format, const void* codes,
                        const void* scales) {
-  if (rows < 0 || cols < 0 || (cols > 0 && rows >= ((int64_t)1 << 40) / cols))
-    return set_error(KT_RAWINT4_EINVAL, "rows and cols must be non-negative and rows * cols below 2^40");
+  if (rows < 0 || cols < 0 || cols > ((int64_t)1 << 32) || (cols > 0 && rows > ((int64_t)1 << 32) / ((cols + 31) / 32)))
+    return set_error(KT_RAWINT4_EINVAL, "rows and cols must be non-negative, the groups at most 2^32");
   if (format != KT_CKPT8_INT8 && format != KT_CKPT8_E4M3)
     return set_error(KT_RAWINT4_EINVAL, "format must be KT_CKPT8_INT8 or KT_CKPT8_E4M3");
   if (rows * cols == 0) return KT_RAWINT4_OK;

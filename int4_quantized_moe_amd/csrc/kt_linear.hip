@@ -18,14 +18,15 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
   const float c = fminf(fmaxf(z, -16.f), 16.f);
   return 2.f * kSqrt2OverPi * (c + 0.044715f * c * c * c);
 }
-__device__ __forceinline__ float sigmoid_lin(float u) { return 1.f / (1.f + expf(-u)); }
+// sigmoid_f (kt_common.hpp) is within a few roundings; a NaN stays one
+__device__ __forceinline__ float sigmoid_lin(float u) { return u != u ? u : sigmoid_f(u); }
 
 __device__ __forceinline__ float act_value(int act, float z) {
   switch (act) {
     case KT_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
-    case KT_ACT_SILU: return z * sigmoid_lin(z);
+    case KT_ACT_SILU: return fmaxf(z, -128.f) * sigmoid_lin(z);  // the sigmoid ends at 2^-127, not at 0
     case KT_ACT_GELU: return 0.5f * z * (1.f + erff(z * kInvSqrt2));
-    case KT_ACT_GELU_TANH: return z * sigmoid_lin(z != z ? z : gelu_tanh_arg(z));
+    case KT_ACT_GELU_TANH: return fmaxf(z, -16.f) * sigmoid_lin(z != z ? z : gelu_tanh_arg(z));
     default: return z;
   }
 }
@@ -392,13 +393,10 @@ struct DzArgs {
   float* part;          // [row blocks][N] column sums
 };
 
-__device__ __forceinline__ float dz_at(const DzArgs& a, int64_t i) {
-  const float dy =
-      a.dy_f32 ? static_cast<const float*>(a.dy)[i] : bf16_to_float(static_cast<const uint16_t*>(a.dy)[i]);
-  if (a.act == KT_ACT_NONE) return dy;
-  const float z = bf16_to_float(a.z[i]);
-  if (a.act == KT_ACT_RELU) return z > 0.f ? dy : z != z ? z : 0.f;
-  return dy * act_slope(a.act, z);
+__device__ __forceinline__ float dz_of(int act, float dy, float z) {
+  if (act == KT_ACT_NONE) return dy;
+  if (act == KT_ACT_RELU) return z > 0.f ? dy : z != z ? z : 0.f;
+  return dy * act_slope(act, z);
 }
 
 // The planes of v: each the nearest bf16 number to what the ones before leave.
@@ -415,38 +413,98 @@ __device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes])
   }
 }
 
-constexpr int kDzRows = 64;
+constexpr int kDzRows = 32, kDzCols = 256;
 
-// 64 columns x kDzRows rows per block.
+// kDzCols columns x kDzRows rows per block, 8 columns a thread.  WIDE: N is a
+// multiple of 8, so that a thread's values are 16-byte pieces.
+template <bool WIDE>
 __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
-  __shared__ float red[4][64];
-  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t n = (int64_t)blockIdx.x * 64 + c;
-  float sum = 0.f;
-  if (n < a.pitch)
-    for (int r = q; r < kDzRows; r += 4) {
-      const int64_t t = (int64_t)blockIdx.y * kDzRows + r;
+  __shared__ float red[8][kDzCols + 4];
+  const int c = (threadIdx.x & 31) * 8, q = threadIdx.x >> 5;
+  const int64_t n = (int64_t)blockIdx.x * kDzCols + c;
+  float sum[8] = {};
+  if (n < a.pitch) {
+#pragma unroll
+    for (int r = 0; r < kDzRows / 8; ++r) {
+      const int64_t t = (int64_t)blockIdx.y * kDzRows + r * 8 + q;
       if (t >= a.T) break;
-      const float v = n < a.N ? dz_at(a, t * a.N + n) : 0.f;
-      sum += v;
+      const int64_t i = t * a.N + n;
+      float v[8], z[8];
+      if (WIDE) {
+        if (a.dy_f32) {
+          const floatx4* p = reinterpret_cast<const floatx4*>(static_cast<const float*>(a.dy) + i);
+          const floatx4 lo = p[0], hi = p[1];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = k < 4 ? lo[k & 3] : hi[k & 3];
+        } else {
+          const u32x4 p = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.dy) + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = bf16_to_float((uint16_t)(p[k >> 1] >> (16 * (k & 1))));
+        }
+        if (a.act != KT_ACT_NONE) {
+          const u32x4 p = *reinterpret_cast<const u32x4*>(a.z + i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) z[k] = bf16_to_float((uint16_t)(p[k >> 1] >> (16 * (k & 1))));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const bool in = n + k < a.N;
+          v[k] = !in        ? 0.f
+                 : a.dy_f32 ? static_cast<const float*>(a.dy)[i + k]
+                            : bf16_to_float(static_cast<const uint16_t*>(a.dy)[i + k]);
+          if (a.act != KT_ACT_NONE) z[k] = in ? bf16_to_float(a.z[i + k]) : 0.f;
+        }
+      }
+      if (a.act != KT_ACT_NONE) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = dz_of(a.act, v[k], z[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += v[k];
       if (a.plane) {
-        uint16_t p[kMaxPlanes];
-        split_planes(v, p);
-        for (int k = 0; k < a.planes; ++k) a.plane[k * a.plane_size + t * a.pitch + n] = p[k];
+        uint16_t p[8][kMaxPlanes];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) split_planes(v[k], p[k]);
+#pragma unroll
+        for (int w = 0; w < kMaxPlanes; ++w)
+          if (w < a.planes)
+            *reinterpret_cast<u32x4*>(a.plane + w * a.plane_size + t * a.pitch + n) =
+                u32x4{pack2(p[0][w], p[1][w]), pack2(p[2][w], p[3][w]), pack2(p[4][w], p[5][w]),
+                      pack2(p[6][w], p[7][w])};
       }
     }
-  red[q][c] = sum;
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) red[q][c + k] = sum[k];
   __syncthreads();
-  if (a.part && q == 0 && n < a.N)
-    a.part[(int64_t)blockIdx.y * a.N + n] = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+  const int64_t col = (int64_t)blockIdx.x * kDzCols + threadIdx.x;
+  if (col < a.N) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x];
+    a.part[(int64_t)blockIdx.y * a.N + col] = s;
+  }
 }
 
-__global__ __launch_bounds__(256) void k_linear_db(const float* __restrict__ part, int64_t nb, int64_t N,
-                                                   float* __restrict__ db, int accumulate, float scale) {
-  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (n >= N) return;
+// Column sums of the row blocks' parts: 64 columns x 16 runs of parts per block.
+__global__ __launch_bounds__(1024) void k_linear_db(const float* __restrict__ part, int64_t nb, int64_t N,
+                                                    float* __restrict__ db, int accumulate, float scale) {
+  __shared__ float red[16][64];
+  const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t n = (int64_t)blockIdx.x * 64 + c;
   float s = 0.f;
-  for (int64_t b = 0; b < nb; ++b) s += part[b * N + n];
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t b = q; b < nb; b += 16) s += part[b * N + n];
+  }
+  red[q][c] = s;
+  __syncthreads();
+  if (q || n >= N) return;
+  s = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) s += red[k][c];
   db[n] = (accumulate ? db[n] : 0.f) + scale * s;
 }
 
@@ -652,11 +710,15 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     a.plane_size = T * p.pitch;
     a.planes = planes;
     a.part = d_bias ? ws_ptr<float>(workspace, p.db) : nullptr;
-    k_linear_dz<<<dim3((unsigned)((p.pitch + 63) / 64), (unsigned)p.nb), 256, 0, st>>>(a);
+    const dim3 grid((unsigned)((p.pitch + kDzCols - 1) / kDzCols), (unsigned)p.nb);
+    if (N % 8 == 0)
+      k_linear_dz<true><<<grid, 256, 0, st>>>(a);
+    else
+      k_linear_dz<false><<<grid, 256, 0, st>>>(a);
     note_launch();
     if (!direct) dz = a.plane;
     if (d_bias) {
-      k_linear_db<<<(unsigned)((N + 255) / 256), 256, 0, st>>>(a.part, p.nb, N, d_bias, accumulate, grad_scale);
+      k_linear_db<<<(unsigned)((N + 63) / 64), 1024, 0, st>>>(a.part, p.nb, N, d_bias, accumulate, grad_scale);
       note_launch();
     }
   }
