@@ -2,6 +2,8 @@
 // their gradients.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kt_common.hpp"
 #include "kt_internal.hpp"
 
@@ -73,7 +75,7 @@ struct LinearGemm {
   int64_t a_plane;       // ... so many elements apart
   int splits;            // the steps of the contraction are dealt to so many blocks; over 1: part
   float* part;           // [splits][M][pn] partial sums
-  int64_t pn;            // N rounded up to a multiple of 4
+  int64_t pn;            // N rounded up to a multiple of 8
   // forward: bias, act, residual, out (type), preact; dx: residual, out; dw: out (fp32), accumulate, scale
   const float* bias;
   const uint16_t* residual;
@@ -85,82 +87,91 @@ struct LinearGemm {
   float scale;
 };
 
-// Outputs m, n .. n + 3 (n a multiple of 4; those below N exist).
-template <int KIND>
-__device__ __forceinline__ void finish4(const LinearGemm& g, int64_t m, int64_t n, floatx4 v) {
+// Outputs m, n .. n + 7 (n a multiple of 8; those below N exist), ACT the
+// forward's activation.
+template <int KIND, int ACT>
+__device__ __forceinline__ void finish8(const LinearGemm& g, int64_t m, int64_t n, float (&v)[8]) {
   const int64_t i = m * g.N + n;
-  const bool whole = (g.N & 3) == 0;  // then every quad is whole and aligned
-  const int cnt = whole ? 4 : (int)(g.N - n < 4 ? g.N - n : 4);
-  if (KIND == kLinDw) {
-    float* o = static_cast<float*>(g.out) + i;
-    if (whole) {
-      floatx4 old = {};
-      if (g.accumulate) old = *reinterpret_cast<floatx4*>(o);
+  if ((g.N & 7) == 0) {  // rows of whole, aligned 16-byte pieces
+    auto put16 = [&](uint16_t* p) {
+      *reinterpret_cast<u32x4*>(p) =
+          u32x4{pack2(float_to_bf16(v[0]), float_to_bf16(v[1])), pack2(float_to_bf16(v[2]), float_to_bf16(v[3])),
+                pack2(float_to_bf16(v[4]), float_to_bf16(v[5])), pack2(float_to_bf16(v[6]), float_to_bf16(v[7]))};
+    };
+    auto put32 = [&](float* p) {
+      *reinterpret_cast<floatx4*>(p) = floatx4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<floatx4*>(p + 4) = floatx4{v[4], v[5], v[6], v[7]};
+    };
+    u32x4 res = {};
+    if (KIND != kLinDw && g.residual) res = *reinterpret_cast<const u32x4*>(g.residual + i);
+    if (KIND == kLinDw) {
+      float* o = static_cast<float*>(g.out) + i;
+      floatx4 lo = {}, hi = {};
+      if (g.accumulate) {
+        lo = *reinterpret_cast<const floatx4*>(o);
+        hi = *reinterpret_cast<const floatx4*>(o + 4);
+      }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) old[r] += g.scale * v[r];
-      *reinterpret_cast<floatx4*>(o) = old;
-    } else {
-      for (int r = 0; r < cnt; ++r) o[r] = (g.accumulate ? o[r] : 0.f) + g.scale * v[r];
+      for (int r = 0; r < 8; ++r) v[r] = (r < 4 ? lo[r & 3] : hi[r & 3]) + g.scale * v[r];
+      put32(o);
+      return;
     }
+    if (KIND == kLinFwd) {
+      if (g.bias) {
+        const floatx4 lo = *reinterpret_cast<const floatx4*>(g.bias + n);
+        const floatx4 hi = *reinterpret_cast<const floatx4*>(g.bias + n + 4);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) v[r] += r < 4 ? lo[r & 3] : hi[r & 3];
+      }
+      if (g.preact) put16(g.preact + i);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] = act_value(ACT, v[r]);
+    }
+    if (g.residual) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] += bf16_to_float((uint16_t)(res[r >> 1] >> (16 * (r & 1))));
+    }
+    if (KIND == kLinFwd && g.out_f32)
+      put32(static_cast<float*>(g.out) + i);
+    else
+      put16(static_cast<uint16_t*>(g.out) + i);
     return;
   }
-  if (KIND == kLinFwd) {
-    if (g.bias) {
-      if (whole) {
-        v += *reinterpret_cast<const floatx4*>(g.bias + n);
-      } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < cnt) v[r] += g.bias[n + r];
-      }
+  for (int r = 0; r < 8; ++r) {
+    if (n + r >= g.N) break;
+    float u = v[r];
+    if (KIND == kLinDw) {
+      float* o = static_cast<float*>(g.out) + i + r;
+      *o = (g.accumulate ? *o : 0.f) + g.scale * u;
+      continue;
     }
-    if (g.preact) {
-      uint16_t z[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) z[r] = float_to_bf16(v[r]);
-      if (whole) {
-        *reinterpret_cast<u32x2*>(g.preact + i) = u32x2{pack2(z[0], z[1]), pack2(z[2], z[3])};
-      } else {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (r < cnt) g.preact[i + r] = z[r];
-      }
+    if (KIND == kLinFwd) {
+      if (g.bias) u += g.bias[n + r];
+      if (g.preact) g.preact[i + r] = float_to_bf16(u);
+      u = act_value(ACT, u);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = act_value(g.act, v[r]);
+    if (g.residual) u += bf16_to_float(g.residual[i + r]);
+    if (KIND == kLinFwd && g.out_f32)
+      static_cast<float*>(g.out)[i + r] = u;
+    else
+      static_cast<uint16_t*>(g.out)[i + r] = float_to_bf16(u);
   }
-  if (g.residual) {
-    if (whole) {
-      const u32x2 q = *reinterpret_cast<const u32x2*>(g.residual + i);
-      v[0] += bf16_to_float((uint16_t)q.x);
-      v[1] += bf16_to_float((uint16_t)(q.x >> 16));
-      v[2] += bf16_to_float((uint16_t)q.y);
-      v[3] += bf16_to_float((uint16_t)(q.y >> 16));
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < cnt) v[r] += bf16_to_float(g.residual[i + r]);
-    }
+}
+
+// body(ACT as a constant) for the forward's activation
+template <int KIND, typename F>
+__device__ __forceinline__ void with_act(int act, F body) {
+  if (KIND != kLinFwd) {
+    body(std::integral_constant<int, KT_ACT_NONE>());
+    return;
   }
-  if (KIND == kLinFwd && g.out_f32) {
-    float* o = static_cast<float*>(g.out) + i;
-    if (whole) {
-      *reinterpret_cast<floatx4*>(o) = v;
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < cnt) o[r] = v[r];
-    }
-  } else {
-    uint16_t* o = static_cast<uint16_t*>(g.out) + i;
-    if (whole) {
-      *reinterpret_cast<u32x2*>(o) =
-          u32x2{pack2(float_to_bf16(v[0]), float_to_bf16(v[1])), pack2(float_to_bf16(v[2]), float_to_bf16(v[3]))};
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (r < cnt) o[r] = float_to_bf16(v[r]);
-    }
+  switch (act) {
+    case KT_ACT_RELU: body(std::integral_constant<int, KT_ACT_RELU>()); break;
+    case KT_ACT_SILU: body(std::integral_constant<int, KT_ACT_SILU>()); break;
+    case KT_ACT_GELU: body(std::integral_constant<int, KT_ACT_GELU>()); break;
+    case KT_ACT_GELU_TANH: body(std::integral_constant<int, KT_ACT_GELU_TANH>()); break;
+    default: body(std::integral_constant<int, KT_ACT_NONE>());
   }
 }
 
@@ -188,6 +199,12 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32
                : "memory", "m0");
 }
 #pragma clang diagnostic pop
+
+// orders a wave's LDS writes before its later LDS reads of other lanes' values, and the other way round
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 constexpr int kLinBK = 64;  // contraction values per step
 
@@ -348,33 +365,57 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
         for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
     }
   }
-  // lane: m = lane % 16 of its tile, n = 4 (lane / 16) .. + 3
+  // An MFMA tile's lane holds m = lane % 16 and n = 4 (lane / 16) .. + 3.  Each
+  // wave turns 16 rows at a time in LDS of its own, so that a lane then holds 8
+  // neighbours of a row and rows are read and written in whole runs.
+  constexpr int kCols = BN / WN, kPitch = kCols + 4, kLanesPerRow = kCols / 8, kRowsPerPass = 64 / kLanesPerRow;
+  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds), "epilogue buffers");
+  float* turn = reinterpret_cast<float*>(&lds[0][0]) + wave * 16 * kPitch;
+  __syncthreads();  // every wave has read its last tiles
+  with_act<KIND>(g.act, [&](auto act) {
 #pragma unroll
-  for (int i = 0; i < kFm; ++i) {
-    const int64_t m = m0 + wm + 16 * i + (lane & 15);
-    if (m >= g.M) continue;
+    for (int i = 0; i < kFm; ++i) {
 #pragma unroll
-    for (int j = 0; j < kFn; ++j) {
-      const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
-      if (n >= g.N) continue;
-      if (g.splits > 1)
-        *reinterpret_cast<floatx4*>(g.part + ((int64_t)blockIdx.y * g.M + m) * g.pn + n) = acc[i][j];
-      else
-        finish4<KIND>(g, m, n, acc[i][j]);
+      for (int j = 0; j < kFn; ++j)
+        *reinterpret_cast<floatx4*>(turn + (lane & 15) * kPitch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
+      wave_fence();
+#pragma unroll
+      for (int h = 0; h < 16 / kRowsPerPass; ++h) {
+        const int r = h * kRowsPerPass + lane / kLanesPerRow, c = lane % kLanesPerRow * 8;
+        const floatx4 lo = *reinterpret_cast<const floatx4*>(turn + r * kPitch + c);
+        const floatx4 hi = *reinterpret_cast<const floatx4*>(turn + r * kPitch + c + 4);
+        const int64_t m = m0 + wm + 16 * i + r, n = n0 + wn + c;
+        if (m < g.M && n < g.N) {
+          if (g.splits > 1) {
+            float* p = g.part + ((int64_t)blockIdx.y * g.M + m) * g.pn + n;
+            *reinterpret_cast<floatx4*>(p) = lo;
+            *reinterpret_cast<floatx4*>(p + 4) = hi;
+          } else {
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            finish8<KIND, decltype(act)::value>(g, m, n, v);
+          }
+        }
+      }
+      wave_fence();
     }
-  }
+  });
 }
 
 // The splits' partial sums, in their order, and the epilogue.
 template <int KIND>
 __global__ __launch_bounds__(256) void k_linear_join(LinearGemm g) {
-  const int64_t quads = g.pn / 4, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= g.M * quads) return;
-  const int64_t m = i / quads, n = (i - m * quads) * 4;
+  const int64_t eights = g.pn / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= g.M * eights) return;
+  const int64_t m = i / eights, n = (i - m * eights) * 8, step = g.M * g.pn;
   const float* p = g.part + m * g.pn + n;
-  floatx4 v = *reinterpret_cast<const floatx4*>(p);
-  for (int s = 1; s < g.splits; ++s) v += *reinterpret_cast<const floatx4*>(p + s * g.M * g.pn);
-  finish4<KIND>(g, m, n, v);
+  floatx4 lo = {}, hi = {};
+#pragma unroll 8
+  for (int s = 0; s < g.splits; ++s) {
+    lo += *reinterpret_cast<const floatx4*>(p + s * step);
+    hi += *reinterpret_cast<const floatx4*>(p + s * step + 4);
+  }
+  float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  with_act<KIND>(g.act, [&](auto act) { finish8<KIND, decltype(act)::value>(g, m, n, v); });
 }
 
 // ---------------------------------------------------------------- dz and its column sums
@@ -550,7 +591,7 @@ static LinearShape linear_shape(int64_t M, int64_t N, int64_t steps) {
 static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 static size_t part_bytes(const LinearShape& s, int64_t M, int64_t N) {
-  return s.splits > 1 ? round256(4 * (size_t)s.splits * (size_t)M * (size_t)round_up(N, 4)) : 0;
+  return s.splits > 1 ? round256(4 * (size_t)s.splits * (size_t)M * (size_t)round_up(N, 8)) : 0;
 }
 
 static int64_t contraction_steps(int64_t K, int planes) { return (K + kLinBK - 1) / kLinBK * planes; }
@@ -584,7 +625,7 @@ template <int KIND>
 static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipStream_t st) {
   g.splits = s.splits;
   g.part = part;
-  g.pn = round_up(g.N, 4);
+  g.pn = round_up(g.N, 8);
   const dim3 grid((unsigned)s.tiles, (unsigned)s.splits);
   if (s.big)
     k_linear<KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
@@ -592,7 +633,7 @@ static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipSt
     k_linear<KIND, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g);
   note_launch();
   if (s.splits > 1) {
-    k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 4) + 255) / 256), 256, 0, st>>>(g);
+    k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 8) + 255) / 256), 256, 0, st>>>(g);
     note_launch();
   }
 }
