@@ -341,50 +341,99 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
 
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
   floatx4 acc[kFm][kFn] = {};
-  if (s0 < s1) copy(0);
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
-    // this step's copies of every wave have landed, and every wave has read the other buffer
-    wait_vm_lgkm<0>();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (s + 1 < s1) copy(buf ^ 1);
+  struct Frags {
+    u32x4 a[kFm], b[kFn];
+  };
+  auto load = [&](Frags& f, int buf, int h) {
     const uint8_t* ta = &lds[buf][0];
     const uint8_t* tb = &lds[buf][TA::kBytes];
 #pragma unroll
-    for (int h = 0; h < kLinBK / 32; ++h) {
-      u32x4 fa[kFm], fb[kFn];
+    for (int j = 0; j < kFn; ++j) f.b[j] = TB::fragment(tb, wn + 16 * j, h, lane);
 #pragma unroll
-      for (int j = 0; j < kFn; ++j) fb[j] = TB::fragment(tb, wn + 16 * j, h, lane);
+    for (int i = 0; i < kFm; ++i) f.a[i] = TA::fragment(ta, wm + 16 * i, h, lane);
+  };
+  auto multiply = [&](const Frags& f) {
 #pragma unroll
-      for (int i = 0; i < kFm; ++i) fa[i] = TA::fragment(ta, wm + 16 * i, h, lane);
+    for (int i = 0; i < kFm; ++i)
 #pragma unroll
-      for (int i = 0; i < kFm; ++i)
+      for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(f.b[j], f.a[i], acc[i][j]);
+  };
+  // spreads a phase's LDS reads over its MFMAs
+  auto spread = [] {
+    constexpr int kReads = kFm * (kAcrossA ? 2 : 1) + kFn * (kAcrossB ? 2 : 1), kMfma = kFm * kFn;
+    constexpr int kPer = kMfma / kReads > 0 ? kMfma / kReads : 1;
 #pragma unroll
-        for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(fb[j], fa[i], acc[i][j]);
+    for (int r = 0; r < kReads; ++r) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, kPer, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto fence = [] {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // A step is two halves of 32 contraction values.  While one half is
+  // multiplied, the other half's (or the next step's first half's) fragments are
+  // read.  In the middle of a step every wave holds all of its tile in
+  // registers, so the copies of the step after next may overwrite it, and the
+  // next step's copies, issued a step ago, must have landed.
+  if (s0 < s1) {
+    copy(0);
+    if (s0 + 1 < s1) {
+      copy(1);
+      wait_vm_lgkm<kCa + kCb>();
+    } else {
+      wait_vm_lgkm<0>();
+    }
+    fence();
+    __builtin_amdgcn_s_barrier();
+    fence();
+    Frags f0, f1;
+    load(f0, 0, 0);
+    int buf = 0;
+    for (int s = s0; s + 1 < s1; ++s, buf ^= 1) {
+      load(f1, buf, 1);
+      multiply(f0);
+      spread();
+      wait_vm_lgkm<0>();
+      fence();
+      __builtin_amdgcn_s_barrier();
+      fence();
+      if (s + 2 < s1) copy(buf);
+      load(f0, buf ^ 1, 0);
+      multiply(f1);
+      spread();
+    }
+    load(f1, buf, 1);
+    multiply(f0);
+    multiply(f1);
   }
   // An MFMA tile's lane holds m = lane % 16 and n = 4 (lane / 16) .. + 3.  Each
-  // wave turns 16 rows at a time in LDS of its own, so that a lane then holds 8
-  // neighbours of a row and rows are read and written in whole runs.
-  constexpr int kCols = BN / WN, kPitch = kCols + 4, kLanesPerRow = kCols / 8, kRowsPerPass = 64 / kLanesPerRow;
-  static_assert(kWaves * 16 * kPitch * 4 <= (int)sizeof(lds), "epilogue buffers");
-  float* turn = reinterpret_cast<float*>(&lds[0][0]) + wave * 16 * kPitch;
+  // wave turns 64 rows at a time in LDS of its own, so that a lane then holds 8
+  // neighbours of a row and rows are read and written in whole runs.  Quad q
+  // (4 values) of row r lies at position q ^ (r & 15).
+  constexpr int kCols = BN / WN, kLanesPerRow = kCols / 8, kRowsPerPass = 64 / kLanesPerRow;
+  static_assert(kCols == 64 && kFm % 4 == 0 && kWaves * 64 * kCols * 4 <= (int)sizeof(lds), "epilogue buffers");
+  floatx4* turn = reinterpret_cast<floatx4*>(&lds[0][0]) + wave * 64 * (kCols / 4);
   __syncthreads();  // every wave has read its last tiles
-  with_act<KIND>(g.act, [&](auto act) {
 #pragma unroll
-    for (int i = 0; i < kFm; ++i) {
+  for (int i0 = 0; i0 < kFm; i0 += 4) {
 #pragma unroll
-      for (int j = 0; j < kFn; ++j)
-        *reinterpret_cast<floatx4*>(turn + (lane & 15) * kPitch + 16 * j + 4 * (lane >> 4)) = acc[i][j];
-      wave_fence();
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int h = 0; h < 16 / kRowsPerPass; ++h) {
-        const int r = h * kRowsPerPass + lane / kLanesPerRow, c = lane % kLanesPerRow * 8;
-        const floatx4 lo = *reinterpret_cast<const floatx4*>(turn + r * kPitch + c);
-        const floatx4 hi = *reinterpret_cast<const floatx4*>(turn + r * kPitch + c + 4);
-        const int64_t m = m0 + wm + 16 * i + r, n = n0 + wn + c;
+      for (int j = 0; j < kFn; ++j) {
+        const int r = 16 * i + (lane & 15), q = 4 * j + (lane >> 4);
+        turn[r * (kCols / 4) + (q ^ (r & 15))] = acc[i0 + i][j];
+      }
+    wave_fence();
+    with_act<KIND>(g.act, [&](auto act) {
+#pragma unroll 1
+      for (int r = lane / kLanesPerRow; r < 64; r += kRowsPerPass) {
+        const int c = lane % kLanesPerRow;
+        const floatx4 lo = turn[r * (kCols / 4) + ((2 * c) ^ (r & 15))];
+        const floatx4 hi = turn[r * (kCols / 4) + ((2 * c + 1) ^ (r & 15))];
+        const int64_t m = m0 + wm + 16 * i0 + r, n = n0 + wn + 8 * c;
         if (m < g.M && n < g.N) {
           if (g.splits > 1) {
             float* p = g.part + ((int64_t)blockIdx.y * g.M + m) * g.pn + n;
@@ -396,9 +445,9 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
           }
         }
       }
-      wave_fence();
-    }
-  });
+    });
+    wave_fence();
+  }
 }
 
 // The splits' partial sums, in their order, and the epilogue.
