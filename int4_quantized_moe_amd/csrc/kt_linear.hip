@@ -87,8 +87,28 @@ struct LinearGemm {
   float scale;
 };
 
-// Outputs m, n .. n + 7 (n a multiple of 8; those below N exist), ACT the
-// forward's activation.
+// One output, ACT the forward's activation.
+template <int KIND, int ACT>
+__device__ __forceinline__ void finish1(const LinearGemm& g, int64_t m, int64_t n, float v) {
+  const int64_t i = m * g.N + n;
+  if (KIND == kLinDw) {
+    float* o = static_cast<float*>(g.out) + i;
+    *o = (g.accumulate ? *o : 0.f) + g.scale * v;
+    return;
+  }
+  if (KIND == kLinFwd) {
+    if (g.bias) v += g.bias[n];
+    if (g.preact) g.preact[i] = float_to_bf16(v);
+    v = act_value(ACT, v);
+  }
+  if (g.residual) v += bf16_to_float(g.residual[i]);
+  if (KIND == kLinFwd && g.out_f32)
+    static_cast<float*>(g.out)[i] = v;
+  else
+    static_cast<uint16_t*>(g.out)[i] = float_to_bf16(v);
+}
+
+// Outputs m, n .. n + 7 (n a multiple of 8; those below N exist).
 template <int KIND, int ACT>
 __device__ __forceinline__ void finish8(const LinearGemm& g, int64_t m, int64_t n, float (&v)[8]) {
   const int64_t i = m * g.N + n;
@@ -138,25 +158,8 @@ __device__ __forceinline__ void finish8(const LinearGemm& g, int64_t m, int64_t 
     return;
   }
 #pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    if (n + r >= g.N) break;
-    float u = v[r];
-    if (KIND == kLinDw) {
-      float* o = static_cast<float*>(g.out) + i + r;
-      *o = (g.accumulate ? *o : 0.f) + g.scale * u;
-      continue;
-    }
-    if (KIND == kLinFwd) {
-      if (g.bias) u += g.bias[n + r];
-      if (g.preact) g.preact[i + r] = float_to_bf16(u);
-      u = act_value(ACT, u);
-    }
-    if (g.residual) u += bf16_to_float(g.residual[i + r]);
-    if (KIND == kLinFwd && g.out_f32)
-      static_cast<float*>(g.out)[i + r] = u;
-    else
-      static_cast<uint16_t*>(g.out)[i + r] = float_to_bf16(u);
-  }
+  for (int r = 0; r < 8; ++r)
+    if (n + r < g.N) finish1<KIND, ACT>(g, m, n + r, v[r]);
 }
 
 // body(ACT as a constant) for the forward's activation
@@ -213,30 +216,33 @@ constexpr int kLinBK = 64;  // contraction values per step
 // fills 1024 consecutive bytes, so the arrangement is made on the source side.
 //
 // Contiguous contraction: row r at r * 128, its 16-byte chunk c (8 values) at
-// position c ^ (r & 7).  A fragment read takes one chunk of 16 consecutive
-// rows: the 8 rows of a 1 KiB block then lie on 8 different bank groups.
+// position c ^ (r >> 1 & 7).  A fragment read takes one chunk of 16 consecutive
+// rows; even rows lie in the lower and odd rows in the upper 32 banks, eight
+// different chunks of each: all 64 banks once.
 //
 // Contraction across rows: value k of all R columns at k * 2R, the 32-byte pair
-// p (16 columns) at position p ^ h(k), h(k) = (k & 3) | (k >> 3 & 1) << 2.  A
-// fragment (16 columns x 8 values per lane) is two transposing reads, each of 4
-// values k for 16 columns per 16 lanes; h spreads the 8 rows that two
-// 16-lane groups read together over all banks.
+// p (16 columns) at position p ^ h(k).  A fragment (16 columns x 8 values per
+// lane) is two transposing reads, each of 4 values k for 16 columns per 16
+// lanes; h(k) = (k & 3) | (k >> 3 & 1) << 2 spreads the 8 rows that two 16-lane
+// groups read together over all banks.
 template <int R, bool ACROSS>
 struct LinTile {
   static constexpr int kBytes = R * 2 * kLinBK;
-  static constexpr int kRowsPerCopy = ACROSS ? 512 / R : 8;
   static constexpr int kCopies = kBytes / 1024;
+
+  // the pair swizzle of contraction value k
+  __device__ static int spread(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
 
   // tile row (contraction value if ACROSS) and element within it that lane l of copy q fills
   __device__ static void place(int q, int l, int& row, int& col) {
     if (ACROSS) {
-      constexpr int kChunks = R / 8;
-      row = q * kRowsPerCopy + l / kChunks;
-      const int pos = l % kChunks, h = (row & 3) | ((row >> 3) & 1) << 2;
-      col = (((pos >> 1) ^ h) * 2 + (pos & 1)) * 8;
+      const int at = q * 64 + l;  // 16-byte chunk of the tile
+      row = at / (R / 8);
+      const int pos = at % (R / 8);
+      col = (((pos >> 1) ^ spread(row)) * 2 + (pos & 1)) * 8;
     } else {
       row = q * 8 + (l >> 3);
-      col = ((l & 7) ^ (row & 7)) * 8;
+      col = ((l & 7) ^ ((row >> 1) & 7)) * 8;
     }
   }
 
@@ -244,7 +250,7 @@ struct LinTile {
   __device__ static u32x4 fragment(const uint8_t* tile, int r0, int ks, int lane) {
     const int g = lane >> 4, j = lane & 15;
     if (ACROSS) {
-      const int h = (j >> 2) | (g & 1) << 2;
+      const int h = spread(8 * g + (j >> 2));
       const uint8_t* p = tile + (ks * 32 + 8 * g + (j >> 2)) * (2 * R) + (((r0 >> 4) ^ h) * 32) + (j & 3) * 8;
       typedef short4_t __attribute__((address_space(3))) * lds_p;
       const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_p)(p)));
@@ -252,7 +258,7 @@ struct LinTile {
       return u32x4{lo.x, lo.y, hi.x, hi.y};
     }
     const int row = r0 + j;
-    return *reinterpret_cast<const u32x4*>(tile + row * 128 + (((ks * 4 + g) ^ (row & 7)) * 16));
+    return *reinterpret_cast<const u32x4*>(tile + row * 128 + (((ks * 4 + g) ^ ((row >> 1) & 7)) * 16));
   }
 };
 
@@ -260,7 +266,7 @@ struct LinTile {
 // of them as 16 x 16 MFMA tiles.  Two LDS buffers: while one step's tiles are
 // multiplied, the next step's are copied into the other.
 template <int KIND, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
+__global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(LinearGemm g) {
   constexpr bool kAcrossA = KIND == kLinDw, kAcrossB = KIND != kLinFwd;
   typedef LinTile<BM, kAcrossA> TA;
   typedef LinTile<BN, kAcrossB> TB;
@@ -392,16 +398,18 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
     Frags f0, f1;
     load(f0, 0, 0);
     int buf = 0;
-    for (int s = s0; s + 1 < s1; ++s, buf ^= 1) {
+    for (int s = s0; s + 1 < s1; ++s) {
       load(f1, buf, 1);
       multiply(f0);
       spread();
+      fence();
       wait_vm_lgkm<0>();
       fence();
       __builtin_amdgcn_s_barrier();
       fence();
       if (s + 2 < s1) copy(buf);
-      load(f0, buf ^ 1, 0);
+      buf ^= 1;
+      load(f0, buf, 0);
       multiply(f1);
       spread();
     }
@@ -410,29 +418,26 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
     multiply(f1);
   }
   // An MFMA tile's lane holds m = lane % 16 and n = 4 (lane / 16) .. + 3.  Each
-  // wave turns 64 rows at a time in LDS of its own, so that a lane then holds 8
-  // neighbours of a row and rows are read and written in whole runs.  Quad q
-  // (4 values) of row r lies at position q ^ (r & 15).
-  constexpr int kCols = BN / WN, kLanesPerRow = kCols / 8, kRowsPerPass = 64 / kLanesPerRow;
-  static_assert(kCols == 64 && kFm % 4 == 0 && kWaves * 64 * kCols * 4 <= (int)sizeof(lds), "epilogue buffers");
-  floatx4* turn = reinterpret_cast<floatx4*>(&lds[0][0]) + wave * 64 * (kCols / 4);
+  // wave turns 32 rows at a time in LDS of its own, so that a lane then holds 8
+  // neighbours of a row and rows are read and written in whole runs.  Rows lie a
+  // quad (4 values) more than their width apart.
+  constexpr int kCols = BN / WN, kEights = kCols / 8, kPitch = kCols / 4 + 1;
+  static_assert(kFm % 2 == 0 && kWaves * 32 * kPitch * 16 <= (int)sizeof(lds), "epilogue buffers");
+  floatx4* turn = reinterpret_cast<floatx4*>(&lds[0][0]) + wave * 32 * kPitch;
   __syncthreads();  // every wave has read its last tiles
 #pragma unroll
-  for (int i0 = 0; i0 < kFm; i0 += 4) {
+  for (int i0 = 0; i0 < kFm; i0 += 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < kFn; ++j) {
-        const int r = 16 * i + (lane & 15), q = 4 * j + (lane >> 4);
-        turn[r * (kCols / 4) + (q ^ (r & 15))] = acc[i0 + i][j];
-      }
+      for (int j = 0; j < kFn; ++j)
+        turn[(16 * i + (lane & 15)) * kPitch + 4 * j + (lane >> 4)] = acc[i0 + i][j];
     wave_fence();
     with_act<KIND>(g.act, [&](auto act) {
 #pragma unroll 1
-      for (int r = lane / kLanesPerRow; r < 64; r += kRowsPerPass) {
-        const int c = lane % kLanesPerRow;
-        const floatx4 lo = turn[r * (kCols / 4) + ((2 * c) ^ (r & 15))];
-        const floatx4 hi = turn[r * (kCols / 4) + ((2 * c + 1) ^ (r & 15))];
+      for (int at = lane; at < 32 * kEights; at += 64) {
+        const int r = at / kEights, c = at % kEights;
+        const floatx4 lo = turn[r * kPitch + 2 * c], hi = turn[r * kPitch + 2 * c + 1];
         const int64_t m = m0 + wm + 16 * i0 + r, n = n0 + wn + 8 * c;
         if (m < g.M && n < g.N) {
           if (g.splits > 1) {
@@ -450,21 +455,105 @@ __global__ __launch_bounds__(64 * WM* WN) void k_linear(LinearGemm g) {
   }
 }
 
-// The splits' partial sums, in their order, and the epilogue.
+// The splits' partial sums and the epilogue: 64 outputs of 8 columns per block,
+// each wave sums every fourth split (so that their loads are in flight
+// together), wave 0 joins the four in order.
 template <int KIND>
 __global__ __launch_bounds__(256) void k_linear_join(LinearGemm g) {
-  const int64_t eights = g.pn / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= g.M * eights) return;
-  const int64_t m = i / eights, n = (i - m * eights) * 8, step = g.M * g.pn;
+  __shared__ floatx4 red[3][2][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t eights = g.pn / 8, i = (int64_t)blockIdx.x * 64 + lane, step = g.M * g.pn;
+  const bool in = i < g.M * eights;
+  const int64_t m = i / eights, n = (i - m * eights) * 8;
   const float* p = g.part + m * g.pn + n;
   floatx4 lo = {}, hi = {};
+  if (in) {
 #pragma unroll 8
-  for (int s = 0; s < g.splits; ++s) {
-    lo += *reinterpret_cast<const floatx4*>(p + s * step);
-    hi += *reinterpret_cast<const floatx4*>(p + s * step + 4);
+    for (int s = wave; s < g.splits; s += 4) {
+      lo += *reinterpret_cast<const floatx4*>(p + s * step);
+      hi += *reinterpret_cast<const floatx4*>(p + s * step + 4);
+    }
+  }
+  if (wave) {
+    red[wave - 1][0][lane] = lo;
+    red[wave - 1][1][lane] = hi;
+  }
+  __syncthreads();
+  if (wave || !in) return;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    lo += red[q][0][lane];
+    hi += red[q][1][lane];
   }
   float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   with_act<KIND>(g.act, [&](auto act) { finish8<KIND, decltype(act)::value>(g, m, n, v); });
+}
+
+// ---------------------------------------------------------------- few rows
+
+// The forward for up to 16 MT tokens, which is bound by reading the weight once:
+// a block computes `cols` (4, 8 or 16) output columns for all tokens.  Its 16
+// waves deal the contraction's 64-value pieces out in turn, read weight and
+// inputs straight into fragments (32 bytes of a row per lane: a wave reads whole
+// 128-byte lines of 16 rows; lanes past the last column or token repeat it), and
+// their sums are joined through LDS in the waves' order.  One launch, no workspace.
+template <int MT>
+__global__ __launch_bounds__(1024) void k_linear_few(LinearGemm g, int cols) {
+  constexpr int kWaves = 16, kUnroll = MT == 1 ? 4 : MT == 2 ? 2 : 1;
+  __shared__ float red[kWaves][MT][16 * 17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane & 15, q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * cols;
+  const int64_t n = min(n0 + min(j, cols - 1), g.N - 1);
+  const uint16_t* pw = g.b + n * g.ldb + 16 * q;
+  const uint16_t* px[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) px[i] = g.a + min((int64_t)(16 * i + j), g.M - 1) * g.lda + 16 * q;
+  floatx4 acc[MT] = {};
+  const int full = (int)(g.K / 64), pieces = (int)((g.K + 63) / 64);
+  auto step = [&](int b, auto count) {
+    constexpr int U = decltype(count)::value;
+    u32x4 w[U][2], x[U][MT][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = (int64_t)(b + u * kWaves) * 64 + 8 * h;
+        w[u][h] = *reinterpret_cast<const u32x4*>(pw + k);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[u][i][h] = *reinterpret_cast<const u32x4*>(px[i] + k);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = mfma_bf16(w[u][h], x[u][i][h], acc[i]);
+  };
+  int b = wave;
+  for (; b + (kUnroll - 1) * kWaves < full; b += kUnroll * kWaves) step(b, std::integral_constant<int, kUnroll>());
+  for (; b < full; b += kWaves) step(b, std::integral_constant<int, 1>());
+  if (b == full && full < pieces) {  // the last piece is short: values past K are zeros
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t k = (int64_t)full * 64 + 8 * h;
+      const bool in = k + 16 * q < g.K;
+      const u32x4 w = in ? *reinterpret_cast<const u32x4*>(pw + k) : u32x4{};
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i] = mfma_bf16(w, in ? *reinterpret_cast<const u32x4*>(px[i] + k) : u32x4{}, acc[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) red[wave][i][(4 * q + r) * 17 + j] = acc[i][r];
+  __syncthreads();
+  const int c = threadIdx.x & 15, m = threadIdx.x >> 4;
+  if (m >= g.M || m >= 16 * MT || c >= cols || n0 + c >= g.N) return;
+  float v = 0.f;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) v += red[k][m >> 4][c * 17 + (m & 15)];
+  with_act<kLinFwd>(g.act, [&](auto act) { finish1<kLinFwd, decltype(act)::value>(g, m, n0 + c, v); });
 }
 
 // ---------------------------------------------------------------- dz and its column sums
@@ -615,25 +704,42 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
   return KT_RAWINT4_OK;
 }
 
-// Splits of a product whose tiles alone would leave compute units idle: enough
-// blocks for two rounds of the chip, each with at least kMinSteps steps.
+// How a product runs.
+//   few      forward of few tokens: k_linear_few.  7168 x 384: 6.7 us for one token and 11.2 for 16 against
+//            12.2 and 13.4 us by tiles; 512 x 384: 4.4 us for 64 against 8.3.  It reads the inputs once per
+//            block, so it loses where tokens and K are large (7168 x 384, 64 tokens: 30 against 14.5 us).
+//   big      256 x 256 tiles, where they fill three quarters of the chip.  d_weight of 8192 x 7168 x 2048:
+//            1.24 against 1.06 PFLOP/s with 128 x 128 tiles; grad_input of 16384 x 2048 x 7168: 1.25 against
+//            1.01.  Not in the forward, whose operands both lie in rows of K: a copy's 1024 bytes then come
+//            from 8 rows instead of 2 (twice the requests to the address path), which two blocks of 128 x 128
+//            per unit hide better than one of 256 x 256 (8192 x 7168 x 2048: 1.15 against 0.95 PFLOP/s).
+//   splits   of the contraction, where 128 x 128 tiles alone leave units without the two blocks they can
+//            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 137 us with
+//            1, 93 with 2, 84 with 3 and 99 with 4), each with at least four steps.
 constexpr int kBlocksWanted = 512, kMinSteps = 4, kMaxSplits = 64;
 
 struct LinearShape {
-  bool big;  // 256 x 256 tiles (else 128 x 128)
+  int few;   // 16-row tiles of k_linear_few (0: not used)
+  bool big;
   int64_t tiles;
   int splits;
 };
 
-static LinearShape linear_shape(int64_t M, int64_t N, int64_t steps) {
-  LinearShape s;
+static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K, int planes) {
+  LinearShape s{};
+  s.splits = 1;
+  if (kind == kLinFwd && (M <= 16 || (M <= 64 && M * K <= 65536))) {
+    s.few = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    return s;
+  }
+  const int64_t steps = (K + kLinBK - 1) / kLinBK * planes;
   const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
-  s.big = big >= 192;
+  s.big = kind != kLinFwd && big >= 192;
   s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
   int64_t splits = s.big || s.tiles == 0 ? 1 : kBlocksWanted / s.tiles;
   if (splits > steps / kMinSteps) splits = steps / kMinSteps;
   if (splits > kMaxSplits) splits = kMaxSplits;
-  s.splits = splits > 1 ? (int)splits : 1;
+  if (splits > 1) s.splits = (int)splits;
   return s;
 }
 
@@ -642,8 +748,6 @@ static int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; 
 static size_t part_bytes(const LinearShape& s, int64_t M, int64_t N) {
   return s.splits > 1 ? round256(4 * (size_t)s.splits * (size_t)M * (size_t)round_up(N, 8)) : 0;
 }
-
-static int64_t contraction_steps(int64_t K, int planes) { return (K + kLinBK - 1) / kLinBK * planes; }
 
 // The workspace of a backward.  Every part has room of its own except the
 // splits' partial sums, which the two products use one after the other.
@@ -659,8 +763,8 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   p.pitch = round_up(N, 8);
   p.nb = (T + kDzRows - 1) / kDzRows;
   // the shapes of calls with one plane need no more
-  p.dx = linear_shape(T, K, contraction_steps(N, 1));
-  p.dw = linear_shape(N, K, contraction_steps(T, kMaxPlanes));
+  p.dx = linear_shape(kLinDx, T, K, N, 1);
+  p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);
   p.planes = 0;
   p.db = p.planes + round256(2 * kMaxPlanes * (size_t)T * (size_t)p.pitch);
   p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
@@ -675,14 +779,30 @@ static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipSt
   g.splits = s.splits;
   g.part = part;
   g.pn = round_up(g.N, 8);
+  if constexpr (KIND == kLinFwd) {
+    if (s.few) {
+      // narrower blocks fill more of the chip, wider ones read the inputs less often (7168 x 384: 6.7, 7.6
+      // and 9.9 us with 4, 8 and 16; 7168 x 2048: 13.7, 9.4, 11.6; 2048 x 7168: 14.5, 10.5, 8.2)
+      const int cols = g.N >= 4096 ? 16 : g.N >= 1024 ? 8 : 4;
+      const unsigned blocks = (unsigned)((g.N + cols - 1) / cols);
+      if (s.few == 1)
+        k_linear_few<1><<<blocks, 1024, 0, st>>>(g, cols);
+      else if (s.few == 2)
+        k_linear_few<2><<<blocks, 1024, 0, st>>>(g, cols);
+      else
+        k_linear_few<4><<<blocks, 1024, 0, st>>>(g, cols);
+      note_launch();
+      return;
+    }
+  }
   const dim3 grid((unsigned)s.tiles, (unsigned)s.splits);
-  if (s.big)
-    k_linear<KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
+  if (KIND != kLinFwd && s.big)
+    k_linear<KIND == kLinFwd ? kLinDx : KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
   else
     k_linear<KIND, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g);
   note_launch();
   if (s.splits > 1) {
-    k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 8) + 255) / 256), 256, 0, st>>>(g);
+    k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 8) + 63) / 64), 256, 0, st>>>(g);
     note_launch();
   }
 }
@@ -696,7 +816,7 @@ extern "C" {
 size_t kt_linear_workspace_bytes(const kt_linear* linear, int32_t tokens) {
   if (check_linear(linear, tokens)) return 0;
   (void)set_error(KT_RAWINT4_OK, "");  // 0 is a valid size: no message stays
-  return part_bytes(linear_shape(tokens, linear->out_features, contraction_steps(linear->in_features, 1)), tokens,
+  return part_bytes(linear_shape(kLinFwd, tokens, linear->out_features, linear->in_features, 1), tokens,
                     linear->out_features);
 }
 
@@ -711,7 +831,7 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   if (!is_aligned(inputs, 16) || !is_aligned(residual, 16) || !is_aligned(output, 16) || !is_aligned(preact, 16))
     return set_error(KT_RAWINT4_EINVAL, "inputs, residual, output and preact must be 16-byte aligned");
   const int64_t K = linear->in_features, N = linear->out_features;
-  const LinearShape s = linear_shape(tokens, N, contraction_steps(K, 1));
+  const LinearShape s = linear_shape(kLinFwd, tokens, N, K, 1);
   const size_t need = part_bytes(s, tokens, N);
   if (need) {
     rc = check_caller_workspace(workspace, workspace_bytes, need);
@@ -847,7 +967,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.out = d_weight;
     g.accumulate = accumulate;
     g.scale = grad_scale;
-    const LinearShape s = linear_shape(N, K, contraction_steps(T, planes));
+    const LinearShape s = linear_shape(kLinDw, N, K, T, planes);
     launch_linear<kLinDw>(g, s, ws_ptr<float>(workspace, p.part), st);
   }
   return finish_launches();
