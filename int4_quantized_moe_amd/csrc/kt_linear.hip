@@ -418,26 +418,29 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
     multiply(f1);
   }
   // An MFMA tile's lane holds m = lane % 16 and n = 4 (lane / 16) .. + 3.  Each
-  // wave turns 32 rows at a time in LDS of its own, so that a lane then holds 8
-  // neighbours of a row and rows are read and written in whole runs.  Rows lie a
-  // quad (4 values) more than their width apart.
-  constexpr int kCols = BN / WN, kEights = kCols / 8, kPitch = kCols / 4 + 1;
-  static_assert(kFm % 2 == 0 && kWaves * 32 * kPitch * 16 <= (int)sizeof(lds), "epilogue buffers");
-  floatx4* turn = reinterpret_cast<floatx4*>(&lds[0][0]) + wave * 32 * kPitch;
+  // wave turns 64 rows at a time in LDS of its own, so that a lane then holds 8
+  // neighbours of a row and rows are read and written in whole runs.  Quad q
+  // (4 values) of row r lies at position q ^ (r & 15).  (The loop over the rows
+  // must unroll: accumulators indexed at run time would live in scratch memory.)
+  constexpr int kCols = BN / WN, kEights = kCols / 8, kQuads = kCols / 4;
+  static_assert(kCols == 64 && kFm % 4 == 0 && kWaves * 64 * kCols * 4 <= (int)sizeof(lds), "epilogue buffers");
+  floatx4* turn = reinterpret_cast<floatx4*>(&lds[0][0]) + wave * 64 * kQuads;
   __syncthreads();  // every wave has read its last tiles
 #pragma unroll
-  for (int i0 = 0; i0 < kFm; i0 += 2) {
+  for (int i0 = 0; i0 < kFm; i0 += 4) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < kFn; ++j)
-        turn[(16 * i + (lane & 15)) * kPitch + 4 * j + (lane >> 4)] = acc[i0 + i][j];
+      for (int j = 0; j < kFn; ++j) {
+        const int r = 16 * i + (lane & 15), q = 4 * j + (lane >> 4);
+        turn[r * kQuads + (q ^ (r & 15))] = acc[i0 + i][j];
+      }
     wave_fence();
     with_act<KIND>(g.act, [&](auto act) {
 #pragma unroll 1
-      for (int at = lane; at < 32 * kEights; at += 64) {
-        const int r = at / kEights, c = at % kEights;
-        const floatx4 lo = turn[r * kPitch + 2 * c], hi = turn[r * kPitch + 2 * c + 1];
+      for (int r = lane / kEights; r < 64; r += 64 / kEights) {
+        const int c = lane % kEights;
+        const floatx4 lo = turn[r * kQuads + ((2 * c) ^ (r & 15))], hi = turn[r * kQuads + ((2 * c + 1) ^ (r & 15))];
         const int64_t m = m0 + wm + 16 * i0 + r, n = n0 + wn + 8 * c;
         if (m < g.M && n < g.N) {
           if (g.splits > 1) {
@@ -708,11 +711,10 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
 //   few      forward of few tokens: k_linear_few.  7168 x 384: 6.7 us for one token and 11.2 for 16 against
 //            12.2 and 13.4 us by tiles; 512 x 384: 4.4 us for 64 against 8.3.  It reads the inputs once per
 //            block, so it loses where tokens and K are large (7168 x 384, 64 tokens: 30 against 14.5 us).
-//   big      256 x 256 tiles, where they fill three quarters of the chip.  d_weight of 8192 x 7168 x 2048:
-//            1.24 against 1.06 PFLOP/s with 128 x 128 tiles; grad_input of 16384 x 2048 x 7168: 1.25 against
-//            1.01.  Not in the forward, whose operands both lie in rows of K: a copy's 1024 bytes then come
-//            from 8 rows instead of 2 (twice the requests to the address path), which two blocks of 128 x 128
-//            per unit hide better than one of 256 x 256 (8192 x 7168 x 2048: 1.15 against 0.95 PFLOP/s).
+//   big      256 x 256 tiles, where they fill three quarters of the chip (two rows of fragments then serve
+//            twice the MFMAs).  Forward of 8192 x 7168 x 2048: 1.27 against 1.11 PFLOP/s with 128 x 128
+//            tiles, d_weight 1.24 against 1.06, grad_input of 16384 x 2048 x 7168 1.25 against 1.01.  With
+//            fewer: 4096 x 2048 x 2048 (128 of them) 56 us against 38.
 //   splits   of the contraction, where 128 x 128 tiles alone leave units without the two blocks they can
 //            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 137 us with
 //            1, 93 with 2, 84 with 3 and 99 with 4), each with at least four steps.
@@ -734,7 +736,7 @@ static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K
   }
   const int64_t steps = (K + kLinBK - 1) / kLinBK * planes;
   const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
-  s.big = kind != kLinFwd && big >= 192;
+  s.big = big >= 192;
   s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
   int64_t splits = s.big || s.tiles == 0 ? 1 : kBlocksWanted / s.tiles;
   if (splits > steps / kMinSteps) splits = steps / kMinSteps;
@@ -796,8 +798,8 @@ static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipSt
     }
   }
   const dim3 grid((unsigned)s.tiles, (unsigned)s.splits);
-  if (KIND != kLinFwd && s.big)
-    k_linear<KIND == kLinFwd ? kLinDx : KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
+  if (s.big)
+    k_linear<KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
   else
     k_linear<KIND, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g);
   note_launch();
