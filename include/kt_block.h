@@ -64,8 +64,8 @@ typedef struct kt_router {
  *   largest c, in descending order,
  *   route_weights [tokens, k] fp32: scale * s / (renormalize ? sum of the k s
  *   + 1e-20 : 1).
- * Choices are made on c to 64 bits; equal values go to the lower index.  They
- * are what kt_rawint4_moe_fwd takes as expert_ids and route_weights.
+ * Choices are made on c to 64 bits (without a bias on the logits, which order
+ * as s does); equal values go to the lower index.  They are what kt_rawint4_moe_fwd takes as expert_ids and route_weights.
  *   - An expert whose logit or bias is -inf is never chosen; where fewer than
  *     k are left, the other slots hold id -1 (which the experts drop) and
  *     weight 0.  Its logit counts in the softmax as a probability of 0.

@@ -8,6 +8,8 @@
 // by less than an fp32 rounding.
 #include <math.h>
 
+#include <type_traits>
+
 #include "kt_common.hpp"
 #include "kt_internal.hpp"
 
@@ -39,12 +41,328 @@ __device__ __forceinline__ bool bad_logit(float l) {
   return is_nan(l) || (SCORE == KT_SCORE_SOFTMAX && l == INFINITY);
 }
 
-// ---------------------------------------------------------------- any size
+// ---------------------------------------------------------------- 16 lanes a token
 
-constexpr int kAnyThreads = 256;
+// Up to 512 experts and 16 choices: a block routes 16 tokens, 16 lanes each.
+// The block's logits, one run of memory, are staged in LDS; lane q of a token
+// then holds the v = ceil(E / 16) experts q v .. q v + v - 1.
+//
+// The choice.  With fp32 keys (the logit itself without a bias, which orders as
+// s does; else s + b to within tol / 2) let t be the k-th largest of the 16
+// lanes' largest keys.  At least k keys reach t, so no expert below t - tol is
+// among the k best.  The few above it (about 11 of 384 for k = 8) are listed,
+// valued in 64 bits, one per lane, and ranked against each other; equal values
+// rank by index.  Where over kList experts reach t - tol (rows of equal
+// scores, say), k rounds of the 16 lanes' best 64-bit value choose instead.
+//
+// Groups (whole lanes each) are kept by their fp32 scores, and by scores to 64
+// bits where the border between kept and dropped lies within the fp32 error.
+constexpr int kLanes = 16, kTokens = 16, kList = 48, kMaxVpl = 32;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true);
+}
+__device__ __forceinline__ int row16_or(int v) {
+  v |= dpp_i<0xB1>(v);
+  v |= dpp_i<0x4E>(v);
+  v |= dpp_i<0x141>(v);
+  return v | dpp_i<0x140>(v);
+}
+__device__ __forceinline__ float row16_min(float v) { return -row16_max(-v); }
+
+// lanes of the token whose v is above this lane's
+__device__ __forceinline__ int row16_above(float v) {
+  int n = 0;
+  // row_ror 1 .. 15
+#define KT_ABOVE(r) n += dpp_f<0x120 + r>(v) > v;
+  KT_ABOVE(1) KT_ABOVE(2) KT_ABOVE(3) KT_ABOVE(4) KT_ABOVE(5) KT_ABOVE(6) KT_ABOVE(7) KT_ABOVE(8)
+  KT_ABOVE(9) KT_ABOVE(10) KT_ABOVE(11) KT_ABOVE(12) KT_ABOVE(13) KT_ABOVE(14) KT_ABOVE(15)
+#undef KT_ABOVE
+  return n;
+}
+
+// sum of the lower lanes' v (whole numbers)
+__device__ __forceinline__ int row16_before(int v) {
+  int s = v;
+  s += dpp_i<0x111>(s);  // row_shr 1, 2, 4, 8 (zeros shift in)
+  s += dpp_i<0x112>(s);
+  s += dpp_i<0x114>(s);
+  s += dpp_i<0x118>(s);
+  return s - v;
+}
+
+// orders a wave's LDS writes before its later LDS reads of other lanes' values, and the other way round
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sigmoid and softmax terms in fp32 with the library's exponential (about one rounding).
+__device__ __forceinline__ float sigmoid32(float l) { return 1.f / (1.f + expf(-l)); }
 
 // (value, index) pairs in the order of choice: larger value, then lower index.
 __device__ __forceinline__ bool better(double a, int ia, double b, int ib) { return a > b || (a == b && ia < ib); }
+
+// The block's tokens' logits, widened to fp32.  A block's run starts at a
+// multiple of 16 E values, so at 16 bytes.
+template <bool BF16>
+__device__ __forceinline__ void stage_logits(const void* src, int64_t first, int n, float* dst) {
+  if (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(src) + first;
+    for (int i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
+      const u32x4 q = *reinterpret_cast<const u32x4*>(p + i);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        dst[i + 2 * h] = __uint_as_float(q[h] << 16);
+        dst[i + 2 * h + 1] = __uint_as_float(q[h] & 0xffff0000u);
+      }
+    }
+    const int i = (n & ~7) + threadIdx.x;
+    if (i < n) dst[i] = bf16_to_float(p[i]);
+  } else {
+    const float* p = static_cast<const float*>(src) + first;
+    for (int i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4)
+      *reinterpret_cast<floatx4*>(dst + i) = *reinterpret_cast<const floatx4*>(p + i);
+    const int i = (n & ~3) + threadIdx.x;
+    if (i < n) dst[i] = p[i];
+  }
+}
+
+template <int SCORE, bool BF16, int VPL>
+__global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int32_t* __restrict__ load) {
+  __shared__ __align__(16) float rows[kTokens * kLanes * VPL];
+  __shared__ float bias[kLanes * VPL];
+  __shared__ double val[kTokens][kList];  // before that, the groups' two best of each lane
+  __shared__ uint16_t list[kTokens][kList];
+  __shared__ int sel[kTokens][kLanes];
+  __shared__ int hist[kLanes * VPL];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int E = a.E, k = a.k, v = (E + kLanes - 1) / kLanes;
+  const int live = (int)(tokens - t0 < kTokens ? tokens - t0 : kTokens);
+  stage_logits<BF16>(a.logits, t0 * E, live * E, rows);
+  for (int e = threadIdx.x; e < E; e += 256) {
+    bias[e] = a.bias ? a.bias[e] : 0.f;
+    hist[e] = 0;
+  }
+  __syncthreads();
+  const int q = threadIdx.x & 15, tok = threadIdx.x >> 4, e0 = q * v;
+  const int64_t t = t0 + tok;
+  const float* row = rows + min(tok, live - 1) * E;  // (tokens past the end repeat the last one)
+  const bool exact = a.bias == nullptr;
+
+  float l[VPL];
+  float mx = -INFINITY;
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool in = i < v && e0 + i < E;
+    l[i] = in ? row[e0 + i] : -INFINITY;
+    bad |= bad_logit<SCORE>(l[i]);
+    if (!exact && in) bad |= is_nan(bias[e0 + i]) || bias[e0 + i] == INFINITY;
+    mx = fmaxf(mx, l[i]);
+  }
+  bad = row16_or(bad);
+  float m = 0.f, zinv = 1.f;
+  double m64 = 0.0, zinv64 = 1.0;
+  if (SCORE == KT_SCORE_SOFTMAX) {
+    m = row16_max(mx);
+    if (!(fabsf(m) < INFINITY)) m = 0.f;  // nobody left (s is 0), or an undefined row
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < v) z += expf(l[i] - m);
+    z = row16_sum(z);
+    zinv = z > 0.f ? 1.f / z : 0.f;
+    if (!exact) {  // s + b to 64 bits needs the sum to 64 bits
+      m64 = (double)m;
+      double z64 = 0.0;
+#pragma unroll 1
+      for (int i = 0; i < v; ++i)
+        if (e0 + i < E) z64 += exp((double)row[e0 + i] - m64);
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) z64 += __shfl_xor(z64, off);
+      zinv64 = z64 > 0.0 ? z64 : 1.0;
+    }
+  }
+  auto score32 = [&](float x) { return SCORE == KT_SCORE_SOFTMAX ? expf(x - m) * zinv : sigmoid32(x); };
+  // c to 64 bits (without a bias: of what orders alike)
+  auto value64 = [&](int e) {
+    if (exact) return (double)row[e];
+    const double s = SCORE == KT_SCORE_SOFTMAX ? exp((double)row[e] - m64) / zinv64 : sigmoid64((double)row[e]);
+    return s + (double)bias[e];
+  };
+
+  float key[VPL];
+  float big = 0.f;  // largest |key|
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    key[i] = l[i];
+    if (!exact && i < v && e0 + i < E) {
+      const float b = bias[e0 + i];
+      key[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : score32(l[i]) + b;
+      if (key[i] > -INFINITY) big = fmaxf(big, fabsf(key[i]));
+    }
+  }
+  // twice the error of a key: s within 2^-18 (softmax: some forty roundings of s and of s |l - m| <= 0.37;
+  // sigmoid: far less), and the rounding of the sum with b
+  const float tol = exact ? 0.f : 0x1p-17f + 0x1p-22f * row16_max(big);
+
+  if (a.G > 1) {
+    const int lg = a.per / v, g = q / lg;  // lanes per group, this lane's group
+    const bool used = g < a.G;
+    // keys whose sums the groups compare: c, or s where there is no bias
+    float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      b2 = fmaxf(b2, fminf(b1, key[i]));
+      b1 = fmaxf(b1, key[i]);
+    }
+    const bool sums = a.group_top == 2;
+    if (exact && sums) {
+      b1 = b1 == -INFINITY ? b1 : score32(b1);
+      b2 = b2 == -INFINITY ? b2 : score32(b2);
+    }
+    // one group's two best over its lanes, then the group's rank
+    auto group_rank = [&](double x1, double x2, double& mine) {
+      val[tok][2 * q] = x1;
+      val[tok][2 * q + 1] = x2;
+      wave_fence();
+      double y1 = -INFINITY, y2 = -INFINITY;
+      if (used)
+        for (int j = 0; j < lg; ++j) {
+          const double o1 = val[tok][2 * (g * lg + j)], o2 = val[tok][2 * (g * lg + j) + 1];
+          y2 = fmax(fmin(y1, o1), fmax(y2, o2));
+          y1 = fmax(y1, o1);
+        }
+      mine = sums ? y1 + y2 : y1;
+      wave_fence();
+      val[tok][2 * q] = mine;
+      wave_fence();
+      int rank = 0;
+      for (int j = 0; j < a.G; ++j) rank += better(val[tok][2 * j * lg], j, mine, g);
+      wave_fence();
+      return rank;
+    };
+    double mine;
+    bool keep = group_rank((double)b1, (double)b2, mine) < a.top_groups && used;
+    if (!exact || sums) {
+      const float lo = row16_min(keep ? (float)mine : INFINITY), hi = row16_max(keep || !used ? -INFINITY : (float)mine);
+      const float err = exact ? 0x1p-16f : 2.f * tol;  // twice the error of a sum of two
+      // (rows of the same wave may differ; all of them run the exact form where one needs it)
+      if (__any(hi > -INFINITY && !(lo - hi > err))) {
+        double c1 = -INFINITY, c2 = -INFINITY;
+#pragma unroll 1
+        for (int i = 0; i < v; ++i) {
+          const int e = e0 + i;
+          if (e >= E || row[e] == -INFINITY || bias[e] == -INFINITY) continue;
+          double c;
+          if (SCORE == KT_SCORE_SOFTMAX)  // without a bias the common divisor changes no order
+            c = exp((double)row[e] - (double)m) / zinv64 + (double)bias[e];
+          else
+            c = sigmoid64((double)row[e]) + (double)bias[e];
+          c2 = fmax(c2, fmin(c1, c));
+          c1 = fmax(c1, c);
+        }
+        keep = group_rank(c1, c2, mine) < a.top_groups && used;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : -INFINITY;
+  }
+
+  float best = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) best = fmaxf(best, key[i]);
+  const float t_k = row16_min(row16_above(best) < k ? best : INFINITY);
+  const float floor_key = t_k - tol;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) count += key[i] >= floor_key && key[i] > -INFINITY;
+  const int at = row16_before(count);
+  const int n = row16_max((float)(at + count));  // of the token: the last lane's end
+  const bool few = n <= kList;
+  if (few) {
+    int w = at;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (key[i] >= floor_key && key[i] > -INFINITY) list[tok][w++] = (uint16_t)(e0 + i);
+  }
+  if (q < k) sel[tok][q] = -1;
+  wave_fence();
+  if (few) {
+    for (int c = q; c < n; c += kLanes) val[tok][c] = value64(list[tok][c]);
+    wave_fence();
+    for (int c = q; c < n; c += kLanes) {
+      const double x = val[tok][c];
+      const int e = list[tok][c];
+      int rank = 0;
+      for (int o = 0; o < n; ++o) rank += better(val[tok][o], list[tok][o], x, e);
+      if (rank < k) sel[tok][rank] = e;
+    }
+  }
+  if (__any(!few)) {
+    // k rounds; a lane's experts leave its range in descending order, so it keeps the last one taken
+    double last = INFINITY;
+    int last_e = -1;
+    for (int j = 0; j < k; ++j) {
+      double x = -INFINITY;
+      int e = E;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (few || !(key[i] >= floor_key && key[i] > -INFINITY)) continue;
+        const double c = value64(e0 + i);
+        if (better(last, last_e, c, e0 + i) && better(c, e0 + i, x, e)) {
+          x = c;
+          e = e0 + i;
+        }
+      }
+      double y = x;
+      int f = e;
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) {
+        const double oy = __shfl_xor(y, off);
+        const int of = __shfl_xor(f, off);
+        if (better(oy, of, y, f)) {
+          y = oy;
+          f = of;
+        }
+      }
+      if (f == e && e < E) {
+        last = x;
+        last_e = e;
+      }
+      if (!few && q == j && f < E) sel[tok][j] = f;
+    }
+  }
+  wave_fence();
+  int id = q < k ? sel[tok][q] : -1;
+  float s = id >= 0 ? score32(row[id]) : 0.f;
+  const float total = row16_sum(s);
+  float w = id >= 0 ? (a.renorm ? s * (a.scale / (total + 1e-20f)) : s * a.scale) : 0.f;
+  if (bad) {
+    id = q;
+    w = __uint_as_float(0x7fc00000u);
+  }
+  if (t < tokens && q < k) {
+    if (a.mask && !a.mask[t]) {
+      id = -1;
+      w = 0.f;
+    }
+    a.ids[t * k + q] = id;
+    a.w[t * k + q] = w;
+    if (load && id >= 0) atomicAdd(&hist[id], 1);
+  }
+  if (load) {  // whole numbers: the order of the sums does not matter
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 256)
+      if (hist[e]) atomicAdd(&load[e], hist[e]);
+  }
+}
+
+// ---------------------------------------------------------------- any size
+
+constexpr int kAnyThreads = 256;
 
 __device__ __forceinline__ void wave_best(double& v, int& i) {
 #pragma unroll
@@ -117,7 +435,8 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_any(RouterArgs a) {
   for (int e = tid; e < a.E; e += kAnyThreads) {
     const float l = load_logit<BF16>(a.logits, base + e);
     const float b = a.bias ? a.bias[e] : 0.f;
-    c[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : score(l) + (double)b;
+    // without a bias the logit itself, which orders as s does
+    c[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : a.bias ? score(l) + (double)b : (double)l;
   }
   if (tid == 0) sum_s = 0.0;
   __syncthreads();
@@ -125,7 +444,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_any(RouterArgs a) {
     for (int g = wave; g < a.G; g += 4) {
       double v1 = -INFINITY, v2 = -INFINITY;
       for (int e = g * a.per + lane; e < (g + 1) * a.per; e += 64) {
-        const double v = c[e];
+        const double v = a.bias || a.group_top == 1 || c[e] == -INFINITY ? c[e] : score((float)c[e]);
         v2 = fmax(v2, fmin(v1, v));
         v1 = fmax(v1, v);
       }
@@ -221,9 +540,6 @@ __device__ __forceinline__ void store_grad(void* p, int64_t i, float v) {
     static_cast<float*>(p)[i] = v;
 }
 
-// Sigmoid and softmax in fp32 with the library's exponential (about one rounding).
-__device__ __forceinline__ float sigmoid32(float l) { return 1.f / (1.f + expf(-l)); }
-
 // With p = s / S the gradient of the chosen scores is ds = scale (g - d) / S,
 // and the softmax's sum ds s is scale d (1 - sum s / S) / S = scale d 1e-20 / S^2:
 // written so, the tiny term keeps its value instead of a difference of roundings.
@@ -241,6 +557,108 @@ __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off);
   return v;
+}
+
+// Up to 512 experts and 16 slots: 16 tokens a block, 16 lanes each.  The logits
+// are staged in LDS as one run, turned into s and then into -s (sum ds s) in
+// place, the chosen experts' values are put over those, and the run is written
+// back whole.
+template <int SCORE, bool BF16, int VPL>
+__global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t tokens) {
+  __shared__ __align__(16) float rows[kTokens * kLanes * VPL];
+  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  const int E = a.E, k = a.k, v = (E + kLanes - 1) / kLanes;
+  const int live = (int)(tokens - t0 < kTokens ? tokens - t0 : kTokens);
+  stage_logits<BF16>(a.logits, t0 * E, live * E, rows);
+  __syncthreads();
+  const int q = threadIdx.x & 15, tok = threadIdx.x >> 4;
+  const bool mine = tok < live;
+  float* row = rows + min(tok, live - 1) * E;
+  const int64_t slot = (t0 + min(tok, live - 1)) * k + q;
+  int id = -1;
+  float g = 0.f;
+  if (q < k) {
+    const int64_t given = a.ids[slot];
+    if (given >= 0 && given < E) {
+      id = (int)given;
+      g = a.g[slot];
+    }
+  }
+  // lane q: experts q, q + 16, ... (neighbouring lanes, neighbouring banks)
+  float s[VPL], mx = -INFINITY;
+  int bad = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = q + kLanes * i;
+    s[i] = i < v && e < E ? row[e] : -INFINITY;
+    bad |= bad_logit<SCORE>(s[i]);
+    mx = fmaxf(mx, s[i]);
+  }
+  bad = row16_or(bad);
+  const int used = row16_or(id >= 0);
+  RowGrad r{0.f, 1.f, 1.f, 0.f, 0.f};
+  if (SCORE == KT_SCORE_SOFTMAX) {
+    r.m = row16_max(mx);
+    if (!(fabsf(r.m) < INFINITY)) r.m = 0.f;
+    float z = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < v) {
+        s[i] = expf(s[i] - r.m);
+        z += s[i];
+      }
+    z = row16_sum(z);
+    r.zinv = z > 0.f ? 1.f / z : 0.f;
+  }
+  const float lc = id >= 0 ? row[id] : -INFINITY;
+  const float sc = id < 0 ? 0.f : SCORE == KT_SCORE_SOFTMAX ? expf(lc - r.m) * r.zinv : sigmoid32(lc);
+  const float ssum = row16_sum(sc), gsum = row16_sum(g * sc);
+  if (a.renorm) {
+    const float S = ssum + 1e-20f;
+    r.inv = 1.f / S;
+    r.d = gsum * r.inv;
+    r.dot = a.scale * r.d * (1e-20f * r.inv);
+  } else {
+    r.dot = a.scale * gsum;
+  }
+  // an expert in several slots: every one of its lanes has the sum, in slot order
+  float ds = 0.f;
+  const float own = id >= 0 ? chosen_ds(a, r, g) : 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int oi = __shfl(id, j, kLanes);
+    const float od = __shfl(own, j, kLanes);
+    if (oi == id) ds += od;
+  }
+  const float rest = bad && used ? __uint_as_float(0x7fc00000u) : SCORE == KT_SCORE_SOFTMAX && used ? -r.dot * r.zinv : 0.f;
+  if (mine) {
+    wave_fence();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = q + kLanes * i;
+      if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest;
+    }
+    wave_fence();
+    if (id >= 0 && !bad) row[id] = SCORE == KT_SCORE_SOFTMAX ? sc * (ds - r.dot) : ds * sc * (1.f - sc);
+  }
+  __syncthreads();
+  const int n = live * E;
+  if (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(a.out) + t0 * E;
+    for (int i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
+      u32x4 o;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) o[h] = pack2(float_to_bf16(rows[i + 2 * h]), float_to_bf16(rows[i + 2 * h + 1]));
+      *reinterpret_cast<u32x4*>(p + i) = o;
+    }
+    const int i = (n & ~7) + threadIdx.x;
+    if (i < n) p[i] = float_to_bf16(rows[i]);
+  } else {
+    float* p = static_cast<float*>(a.out) + t0 * E;
+    for (int i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4)
+      *reinterpret_cast<floatx4*>(p + i) = *reinterpret_cast<const floatx4*>(rows + i);
+    const int i = (n & ~3) + threadIdx.x;
+    if (i < n) p[i] = rows[i];
+  }
 }
 
 // One block per token; ds of every expert in LDS.  Each thread owns the experts
@@ -407,15 +825,8 @@ static int check_router(const kt_router* r, int32_t tokens) {
   return KT_RAWINT4_OK;
 }
 
-template <int SCORE, bool BF16>
-static void launch_route(const RouterArgs& a, int tokens, hipStream_t st) {
-  k_route_any<SCORE, BF16><<<(unsigned)tokens, kAnyThreads, 0, st>>>(a);
-  note_launch();
-}
-
-template <int SCORE, bool BF16>
-static void launch_route_bwd(const RouterBwdArgs& a, int tokens, hipStream_t st) {
-  k_route_bwd_any<SCORE, BF16><<<(unsigned)tokens, kAnyThreads, 0, st>>>(a);
+static void launch_zero_i32(int32_t* p, int n, hipStream_t st) {
+  k_zero_i32<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(p, n);
   note_launch();
 }
 
@@ -425,12 +836,56 @@ static void launch_load(const int64_t* ids, int64_t n, int E, int accumulate, in
     note_launch();
     return;
   }
-  if (!accumulate) {
-    k_zero_i32<<<(unsigned)((E + 255) / 256), 256, 0, st>>>(load, E);
-    note_launch();
-  }
+  if (!accumulate) launch_zero_i32(load, E, st);
   const int64_t blocks = (n + 4095) / 4096;
   k_route_load<<<(unsigned)(blocks < 256 ? blocks : 256), 256, 0, st>>>(ids, n, E, load);
+  note_launch();
+}
+
+// body(VPL as a constant) for the experts of a lane
+template <typename F>
+static void with_vpl(int E, F body) {
+  const int v = (E + kLanes - 1) / kLanes;
+  if (v <= 4)
+    body(std::integral_constant<int, 4>());
+  else if (v <= 8)
+    body(std::integral_constant<int, 8>());
+  else if (v <= 16)
+    body(std::integral_constant<int, 16>());
+  else if (v <= 24)
+    body(std::integral_constant<int, 24>());
+  else
+    body(std::integral_constant<int, kMaxVpl>());
+}
+
+// 16 lanes a token where they serve, else a block a token.
+template <int SCORE, bool BF16>
+static void launch_route(const RouterArgs& a, int64_t tokens, int32_t* load, int accumulate, hipStream_t st) {
+  const int v = (a.E + kLanes - 1) / kLanes;
+  if (v <= kMaxVpl && a.k <= kLanes && (a.G == 1 || a.per % v == 0)) {
+    if (load && !accumulate) launch_zero_i32(load, a.E, st);
+    with_vpl(a.E, [&](auto vpl) {
+      k_route<SCORE, BF16, decltype(vpl)::value>
+          <<<(unsigned)((tokens + kTokens - 1) / kTokens), 256, 0, st>>>(a, tokens, load);
+    });
+    note_launch();
+    return;
+  }
+  k_route_any<SCORE, BF16><<<(unsigned)tokens, kAnyThreads, 0, st>>>(a);
+  note_launch();
+  if (load) launch_load(a.ids, tokens * a.k, a.E, accumulate, load, st);
+}
+
+template <int SCORE, bool BF16>
+static void launch_route_bwd(const RouterBwdArgs& a, int64_t tokens, hipStream_t st) {
+  if (a.E <= kLanes * kMaxVpl && a.k <= kLanes) {
+    with_vpl(a.E, [&](auto vpl) {
+      k_route_bwd<SCORE, BF16, decltype(vpl)::value>
+          <<<(unsigned)((tokens + kTokens - 1) / kTokens), 256, 0, st>>>(a, tokens);
+    });
+  } else {
+    k_route_bwd_any<SCORE, BF16><<<(unsigned)tokens, kAnyThreads, 0, st>>>(a);
+  }
   note_launch();
 }
 
@@ -460,15 +915,15 @@ int kt_router_fwd(const kt_router* router, int32_t tokens, const void* logits, c
   if (tokens > 0) {
     const bool bf = router->logits_type == KT_TYPE_BF16, soft = router->score == KT_SCORE_SOFTMAX;
     if (soft && bf)
-      launch_route<KT_SCORE_SOFTMAX, true>(a, tokens, st);
+      launch_route<KT_SCORE_SOFTMAX, true>(a, tokens, load, accumulate, st);
     else if (soft)
-      launch_route<KT_SCORE_SOFTMAX, false>(a, tokens, st);
+      launch_route<KT_SCORE_SOFTMAX, false>(a, tokens, load, accumulate, st);
     else if (bf)
-      launch_route<KT_SCORE_SIGMOID, true>(a, tokens, st);
+      launch_route<KT_SCORE_SIGMOID, true>(a, tokens, load, accumulate, st);
     else
-      launch_route<KT_SCORE_SIGMOID, false>(a, tokens, st);
+      launch_route<KT_SCORE_SIGMOID, false>(a, tokens, load, accumulate, st);
   }
-  if (load) launch_load(expert_ids, (int64_t)tokens * a.k, a.E, accumulate, load, st);
+  if (tokens == 0 && load && !accumulate) launch_zero_i32(load, a.E, st);
   return finish_launches();
 }
 

@@ -82,9 +82,12 @@ def route(logits, top_k, score="softmax", num_groups=1, top_groups=1, group_top=
         b = np.zeros(e) if bias is None else np.asarray(bias, np.float64)
         c = np.where(np.isneginf(l[i]) | np.isneginf(b), -np.inf, s[i] + b)
         if num_groups > 1:
-            g = np.sort(c.reshape(num_groups, per), 1)[:, ::-1][:, :group_top].sum(1)
+            by = l[i] if bias is None and group_top == 1 else c
+            g = np.sort(by.reshape(num_groups, per), 1)[:, ::-1][:, :group_top].sum(1)
             kept = np.argsort(-g, kind="stable")[:top_groups]
             c = np.where(np.isin(np.arange(e) // per, kept), c, -np.inf)
+        if bias is None:  # s is monotone in the logit, also where it saturates in 64 bits
+            c = np.where(c > -np.inf, l[i], -np.inf)
         order = np.argsort(-c, kind="stable")[:top_k]
         order = order[c[order] > -np.inf]
         n = len(order)
