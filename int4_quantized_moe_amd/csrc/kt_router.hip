@@ -44,15 +44,17 @@ __device__ __forceinline__ bool bad_logit(float l) {
 // ---------------------------------------------------------------- 16 lanes a token
 
 // Up to 512 experts and 16 choices: a block routes 16 tokens, 16 lanes each.
-// The block's logits, one run of memory, are staged in LDS; lane q of a token
-// then holds the v = ceil(E / 16) experts q v .. q v + v - 1.
+// A token's logits are staged in LDS; a lane holds v = ceil(E / 16) of its
+// experts.  With groups, lg = per / v lanes share a group's experts in turn
+// (lane q: group q / lg, experts q % lg, q % lg + lg, ... of it); without, all
+// 16 lanes share all experts so (lg = 16).
 //
 // The choice.  With fp32 keys (the logit itself without a bias, which orders as
 // s does; else s + b to within tol / 2) let t be the k-th largest of the 16
-// lanes' largest keys.  At least k keys reach t, so no expert below t - tol is
-// among the k best.  The few above it (about 11 of 384 for k = 8) are listed,
-// valued in 64 bits, one per lane, and ranked against each other; equal values
-// rank by index.  Where over kList experts reach t - tol (rows of equal
+// lanes' two largest keys each.  At least k keys reach t, so no expert below
+// t - tol is among the k best.  The few above it (8 to 10 of 384 for k = 8) are
+// listed, valued in 64 bits, one per lane, and ranked against each other; equal
+// values rank by index.  Where over kList experts reach t - tol (rows of equal
 // scores, say), k rounds of the 16 lanes' best 64-bit value choose instead.
 //
 // Groups (whole lanes each) are kept by their fp32 scores, and by scores to 64
@@ -71,15 +73,18 @@ __device__ __forceinline__ int row16_or(int v) {
 }
 __device__ __forceinline__ float row16_min(float v) { return -row16_max(-v); }
 
-// lanes of the token whose v is above this lane's
-__device__ __forceinline__ int row16_above(float v) {
-  int n = 0;
+// counts the other lanes' b1 and b2 (b1 >= b2) above this lane's b1 and above its b2
+__device__ __forceinline__ void row16_above(float b1, float b2, int& n1, int& n2) {
   // row_ror 1 .. 15
-#define KT_ABOVE(r) n += dpp_f<0x120 + r>(v) > v;
+#define KT_ABOVE(r)                                                     \
+  {                                                                     \
+    const float o1 = dpp_f<0x120 + r>(b1), o2 = dpp_f<0x120 + r>(b2);   \
+    n1 += (o1 > b1) + (o2 > b1);                                        \
+    n2 += (o1 > b2) + (o2 > b2);                                        \
+  }
   KT_ABOVE(1) KT_ABOVE(2) KT_ABOVE(3) KT_ABOVE(4) KT_ABOVE(5) KT_ABOVE(6) KT_ABOVE(7) KT_ABOVE(8)
   KT_ABOVE(9) KT_ABOVE(10) KT_ABOVE(11) KT_ABOVE(12) KT_ABOVE(13) KT_ABOVE(14) KT_ABOVE(15)
 #undef KT_ABOVE
-  return n;
 }
 
 // sum of the lower lanes' v (whole numbers)
@@ -101,37 +106,42 @@ __device__ __forceinline__ void wave_fence() {
 // Sigmoid and softmax terms in fp32 with the library's exponential (about one rounding).
 __device__ __forceinline__ float sigmoid32(float l) { return 1.f / (1.f + expf(-l)); }
 
+// exp for arguments up to 0 from the hardware's exp2 (relative error below 2^-23 (2 + 1.5 |x|))
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
 // (value, index) pairs in the order of choice: larger value, then lower index.
 __device__ __forceinline__ bool better(double a, int ia, double b, int ib) { return a > b || (a == b && ia < ib); }
 
-// The block's tokens' logits, widened to fp32.  A block's run starts at a
-// multiple of 16 E values, so at 16 bytes.
+// A token's logits to LDS, widened to fp32, by its 16 lanes: 16-byte pieces
+// where rows start at 16 bytes.
 template <bool BF16>
-__device__ __forceinline__ void stage_logits(const void* src, int64_t first, int n, float* dst) {
-  if (BF16) {
-    const uint16_t* p = static_cast<const uint16_t*>(src) + first;
-    for (int i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(p + i);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        dst[i + 2 * h] = __uint_as_float(q[h] << 16);
-        dst[i + 2 * h + 1] = __uint_as_float(q[h] & 0xffff0000u);
+__device__ __forceinline__ void stage_row(const void* src, int64_t first, int E, int q, float* dst) {
+  constexpr int kPiece = BF16 ? 8 : 4;
+  if (E % kPiece == 0) {
+    for (int i = q * kPiece; i < E; i += kLanes * kPiece) {
+      const u32x4 p = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(src) + (first + i) * (16 / kPiece));
+      if (BF16) {
+        floatx4* d = reinterpret_cast<floatx4*>(dst + i);
+        d[0] = floatx4{__uint_as_float(p.x << 16), __uint_as_float(p.x & 0xffff0000u), __uint_as_float(p.y << 16),
+                       __uint_as_float(p.y & 0xffff0000u)};
+        d[1] = floatx4{__uint_as_float(p.z << 16), __uint_as_float(p.z & 0xffff0000u), __uint_as_float(p.w << 16),
+                       __uint_as_float(p.w & 0xffff0000u)};
+      } else {
+        *reinterpret_cast<u32x4*>(dst + i) = p;
       }
     }
-    const int i = (n & ~7) + threadIdx.x;
-    if (i < n) dst[i] = bf16_to_float(p[i]);
   } else {
-    const float* p = static_cast<const float*>(src) + first;
-    for (int i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4)
-      *reinterpret_cast<floatx4*>(dst + i) = *reinterpret_cast<const floatx4*>(p + i);
-    const int i = (n & ~3) + threadIdx.x;
-    if (i < n) dst[i] = p[i];
+    for (int i = q; i < E; i += kLanes) dst[i] = load_logit<BF16>(src, first + i);
   }
 }
 
+// Rows in LDS lie kRowPad values more than the largest row apart: the four
+// tokens of a wave start at different banks.
+constexpr int kRowPad = 16;
+
 template <int SCORE, bool BF16, int VPL>
 __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int32_t* __restrict__ load) {
-  __shared__ __align__(16) float rows[kTokens * kLanes * VPL];
+  __shared__ __align__(16) float rows[kTokens][kLanes * VPL + kRowPad];
   __shared__ float bias[kLanes * VPL];
   __shared__ double val[kTokens][kList];  // before that, the groups' two best of each lane
   __shared__ uint16_t list[kTokens][kList];
@@ -139,30 +149,37 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
   __shared__ int hist[kLanes * VPL];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
   const int E = a.E, k = a.k, v = (E + kLanes - 1) / kLanes;
-  const int live = (int)(tokens - t0 < kTokens ? tokens - t0 : kTokens);
-  stage_logits<BF16>(a.logits, t0 * E, live * E, rows);
+  const int q = threadIdx.x & 15, tok = threadIdx.x >> 4;
+  const int64_t t = t0 + tok;
+  float* row = rows[tok];
+  stage_row<BF16>(a.logits, min(t, tokens - 1) * E, E, q, row);  // (past the end: the last token again)
+  int bad_bias = 0;
   for (int e = threadIdx.x; e < E; e += 256) {
-    bias[e] = a.bias ? a.bias[e] : 0.f;
+    const float b = a.bias ? a.bias[e] : 0.f;
+    bad_bias |= is_nan(b) || b == INFINITY;
+    bias[e] = b;
     hist[e] = 0;
   }
-  __syncthreads();
-  const int q = threadIdx.x & 15, tok = threadIdx.x >> 4, e0 = q * v;
-  const int64_t t = t0 + tok;
-  const float* row = rows + min(tok, live - 1) * E;  // (tokens past the end repeat the last one)
+  bad_bias = __syncthreads_or(bad_bias);
+  const int lg = a.G > 1 ? a.per / v : kLanes, e0 = a.G > 1 ? q / lg * a.per + q % lg : q;
+  // this lane's experts are e0 + lg i, i < own
+  const int own = a.G > 1 ? (q < a.G * lg ? v : 0) : max(0, (E - q + kLanes - 1) / kLanes);
   const bool exact = a.bias == nullptr;
 
+  // (reads past a token's logits stay inside the array; the fp32 keys use the hardware's exponential and
+  // reciprocal, whose error tol covers; a few loops stay rolled to keep the code short: a single token's time
+  // is mostly that of fetching it)
   float l[VPL];
   float mx = -INFINITY;
-  int bad = 0;
+  bool odd = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const bool in = i < v && e0 + i < E;
-    l[i] = in ? row[e0 + i] : -INFINITY;
-    bad |= bad_logit<SCORE>(l[i]);
-    if (!exact && in) bad |= is_nan(bias[e0 + i]) || bias[e0 + i] == INFINITY;
+    const float x = row[min(e0 + lg * i, kLanes * VPL - 1)];
+    l[i] = i < own ? x : -INFINITY;
+    odd |= bad_logit<SCORE>(l[i]);
     mx = fmaxf(mx, l[i]);
   }
-  bad = row16_or(bad);
+  const int bad = row16_or(odd) | bad_bias;
   float m = 0.f, zinv = 1.f;
   double m64 = 0.0, zinv64 = 1.0;
   if (SCORE == KT_SCORE_SOFTMAX) {
@@ -170,22 +187,21 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
     if (!(fabsf(m) < INFINITY)) m = 0.f;  // nobody left (s is 0), or an undefined row
     float z = 0.f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < v) z += expf(l[i] - m);
+    for (int i = 0; i < VPL; ++i) z += fast_exp(l[i] - m);
     z = row16_sum(z);
     zinv = z > 0.f ? 1.f / z : 0.f;
     if (!exact) {  // s + b to 64 bits needs the sum to 64 bits
       m64 = (double)m;
       double z64 = 0.0;
 #pragma unroll 1
-      for (int i = 0; i < v; ++i)
-        if (e0 + i < E) z64 += exp((double)row[e0 + i] - m64);
+      for (int i = 0; i < own; ++i) z64 += exp((double)row[e0 + lg * i] - m64);
 #pragma unroll
       for (int off = 1; off < 16; off <<= 1) z64 += __shfl_xor(z64, off);
       zinv64 = z64 > 0.0 ? z64 : 1.0;
     }
   }
   auto score32 = [&](float x) { return SCORE == KT_SCORE_SOFTMAX ? expf(x - m) * zinv : sigmoid32(x); };
+  auto score_key = [&](float x) { return SCORE == KT_SCORE_SOFTMAX ? fast_exp(x - m) * zinv : sigmoid_f(x); };
   // c to 64 bits (without a bias: of what orders alike)
   auto value64 = [&](int e) {
     if (exact) return (double)row[e];
@@ -198,30 +214,32 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     key[i] = l[i];
-    if (!exact && i < v && e0 + i < E) {
-      const float b = bias[e0 + i];
-      key[i] = l[i] == -INFINITY || b == -INFINITY ? -INFINITY : score32(l[i]) + b;
-      if (key[i] > -INFINITY) big = fmaxf(big, fabsf(key[i]));
+    if (!exact) {
+      const float c = score_key(l[i]) + bias[min(e0 + lg * i, E - 1)];
+      key[i] = l[i] == -INFINITY ? -INFINITY : c;
+      big = fmaxf(big, fabsf(c) < INFINITY ? fabsf(c) : 0.f);
     }
   }
   // twice the error of a key: s within 2^-18 (softmax: some forty roundings of s and of s |l - m| <= 0.37;
   // sigmoid: far less), and the rounding of the sum with b
   const float tol = exact ? 0.f : 0x1p-17f + 0x1p-22f * row16_max(big);
 
+  float best = -INFINITY, second = -INFINITY;  // of this lane
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    second = fmaxf(second, fminf(best, key[i]));
+    best = fmaxf(best, key[i]);
+  }
   if (a.G > 1) {
-    const int lg = a.per / v, g = q / lg;  // lanes per group, this lane's group
+    const int g = q / lg;
     const bool used = g < a.G;
     // keys whose sums the groups compare: c, or s where there is no bias
-    float b1 = -INFINITY, b2 = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      b2 = fmaxf(b2, fminf(b1, key[i]));
-      b1 = fmaxf(b1, key[i]);
-    }
+    float b1 = best, b2 = second;
     const bool sums = a.group_top == 2;
+    const float reach2 = b2 - tol;  // a lane's two best to 64 bits are among its experts with such a key
     if (exact && sums) {
-      b1 = b1 == -INFINITY ? b1 : score32(b1);
-      b2 = b2 == -INFINITY ? b2 : score32(b2);
+      b1 = b1 == -INFINITY ? b1 : score_key(b1);
+      b2 = b2 == -INFINITY ? b2 : score_key(b2);
     }
     // one group's two best over its lanes, then the group's rank
     auto group_rank = [&](double x1, double x2, double& mine) {
@@ -251,11 +269,12 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
       const float err = exact ? 0x1p-16f : 2.f * tol;  // twice the error of a sum of two
       // (rows of the same wave may differ; all of them run the exact form where one needs it)
       if (__any(hi > -INFINITY && !(lo - hi > err))) {
+        uint32_t left = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) left |= key[i] >= reach2 && key[i] > -INFINITY ? 1u << i : 0u;
         double c1 = -INFINITY, c2 = -INFINITY;
-#pragma unroll 1
-        for (int i = 0; i < v; ++i) {
-          const int e = e0 + i;
-          if (e >= E || row[e] == -INFINITY || bias[e] == -INFINITY) continue;
+        for (; left; left &= left - 1) {
+          const int e = e0 + lg * (__ffs(left) - 1);
           double c;
           if (SCORE == KT_SCORE_SOFTMAX)  // without a bias the common divisor changes no order
             c = exp((double)row[e] - (double)m) / zinv64 + (double)bias[e];
@@ -269,24 +288,23 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) key[i] = keep ? key[i] : -INFINITY;
+    best = keep ? best : -INFINITY;
+    second = keep ? second : -INFINITY;
   }
 
-  float best = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) best = fmaxf(best, key[i]);
-  const float t_k = row16_min(row16_above(best) < k ? best : INFINITY);
+  int above1 = 0, above2 = second < best;
+  row16_above(best, second, above1, above2);
+  const float t_k = row16_min(above2 < k ? second : above1 < k ? best : INFINITY);
   const float floor_key = t_k - tol;
-  int count = 0;
+  uint32_t reach = 0;  // this lane's experts that reach it
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) count += key[i] >= floor_key && key[i] > -INFINITY;
-  const int at = row16_before(count);
-  const int n = row16_max((float)(at + count));  // of the token: the last lane's end
+  for (int i = 0; i < VPL; ++i) reach |= key[i] >= floor_key && key[i] > -INFINITY ? 1u << i : 0u;
+  const int count = __popc(reach), at = row16_before(count);
+  const int n = (int)row16_max((float)(at + count));  // of the token: the last lane's end
   const bool few = n <= kList;
   if (few) {
     int w = at;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (key[i] >= floor_key && key[i] > -INFINITY) list[tok][w++] = (uint16_t)(e0 + i);
+    for (uint32_t left = reach; left; left &= left - 1) list[tok][w++] = (uint16_t)(e0 + lg * (__ffs(left) - 1));
   }
   if (q < k) sel[tok][q] = -1;
   wave_fence();
@@ -297,24 +315,24 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
       const double x = val[tok][c];
       const int e = list[tok][c];
       int rank = 0;
+#pragma unroll 4
       for (int o = 0; o < n; ++o) rank += better(val[tok][o], list[tok][o], x, e);
       if (rank < k) sel[tok][rank] = e;
     }
   }
   if (__any(!few)) {
-    // k rounds; a lane's experts leave its range in descending order, so it keeps the last one taken
+    // k rounds; a lane's experts are taken in descending order, so it keeps the last one taken
     double last = INFINITY;
     int last_e = -1;
     for (int j = 0; j < k; ++j) {
       double x = -INFINITY;
       int e = E;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        if (few || !(key[i] >= floor_key && key[i] > -INFINITY)) continue;
-        const double c = value64(e0 + i);
-        if (better(last, last_e, c, e0 + i) && better(c, e0 + i, x, e)) {
+      for (uint32_t left = few ? 0u : reach; left; left &= left - 1) {
+        const int f = e0 + lg * (__ffs(left) - 1);
+        const double c = value64(f);
+        if (better(last, last_e, c, f) && better(c, f, x, e)) {
           x = c;
-          e = e0 + i;
+          e = f;
         }
       }
       double y = x;
@@ -559,22 +577,19 @@ __device__ __forceinline__ float wave_sum(float v) {
   return v;
 }
 
-// Up to 512 experts and 16 slots: 16 tokens a block, 16 lanes each.  The logits
-// are staged in LDS as one run, turned into s and then into -s (sum ds s) in
-// place, the chosen experts' values are put over those, and the run is written
-// back whole.
+// Up to 512 experts and 16 slots: 16 tokens a block, 16 lanes each.  A token's
+// logits are staged in LDS and turned into -s (sum ds s) in place, the chosen
+// experts' values are put over those, and the row is written back whole.
 template <int SCORE, bool BF16, int VPL>
 __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t tokens) {
-  __shared__ __align__(16) float rows[kTokens * kLanes * VPL];
-  const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+  __shared__ __align__(16) float rows[kTokens][kLanes * VPL + kRowPad];
   const int E = a.E, k = a.k, v = (E + kLanes - 1) / kLanes;
-  const int live = (int)(tokens - t0 < kTokens ? tokens - t0 : kTokens);
-  stage_logits<BF16>(a.logits, t0 * E, live * E, rows);
-  __syncthreads();
   const int q = threadIdx.x & 15, tok = threadIdx.x >> 4;
-  const bool mine = tok < live;
-  float* row = rows + min(tok, live - 1) * E;
-  const int64_t slot = (t0 + min(tok, live - 1)) * k + q;
+  const int64_t t = (int64_t)blockIdx.x * kTokens + tok, tc = min(t, tokens - 1);
+  float* row = rows[tok];
+  stage_row<BF16>(a.logits, tc * E, E, q, row);
+  wave_fence();
+  const int64_t slot = tc * k + q;
   int id = -1;
   float g = 0.f;
   if (q < k) {
@@ -604,7 +619,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t toke
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (i < v) {
-        s[i] = expf(s[i] - r.m);
+        s[i] = fast_exp(s[i] - r.m);
         z += s[i];
       }
     z = row16_sum(z);
@@ -630,34 +645,36 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t toke
     if (oi == id) ds += od;
   }
   const float rest = bad && used ? __uint_as_float(0x7fc00000u) : SCORE == KT_SCORE_SOFTMAX && used ? -r.dot * r.zinv : 0.f;
-  if (mine) {
-    wave_fence();
+  wave_fence();
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = q + kLanes * i;
-      if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest;
-    }
-    wave_fence();
-    if (id >= 0 && !bad) row[id] = SCORE == KT_SCORE_SOFTMAX ? sc * (ds - r.dot) : ds * sc * (1.f - sc);
+  for (int i = 0; i < VPL; ++i) {
+    const int e = q + kLanes * i;
+    if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest;
   }
-  __syncthreads();
-  const int n = live * E;
+  wave_fence();
+  if (id >= 0 && !bad) row[id] = SCORE == KT_SCORE_SOFTMAX ? sc * (ds - r.dot) : ds * sc * (1.f - sc);
+  wave_fence();
+  if (t >= tokens) return;
   if (BF16) {
-    uint16_t* p = static_cast<uint16_t*>(a.out) + t0 * E;
-    for (int i = threadIdx.x * 8; i + 8 <= n; i += 256 * 8) {
-      u32x4 o;
+    uint16_t* p = static_cast<uint16_t*>(a.out) + t * E;
+    if (E % 8 == 0) {
+      for (int i = q * 8; i < E; i += kLanes * 8) {
+        u32x4 o;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) o[h] = pack2(float_to_bf16(rows[i + 2 * h]), float_to_bf16(rows[i + 2 * h + 1]));
-      *reinterpret_cast<u32x4*>(p + i) = o;
+        for (int h = 0; h < 4; ++h) o[h] = pack2(float_to_bf16(row[i + 2 * h]), float_to_bf16(row[i + 2 * h + 1]));
+        *reinterpret_cast<u32x4*>(p + i) = o;
+      }
+    } else {
+      for (int i = q; i < E; i += kLanes) p[i] = float_to_bf16(row[i]);
     }
-    const int i = (n & ~7) + threadIdx.x;
-    if (i < n) p[i] = float_to_bf16(rows[i]);
   } else {
-    float* p = static_cast<float*>(a.out) + t0 * E;
-    for (int i = threadIdx.x * 4; i + 4 <= n; i += 256 * 4)
-      *reinterpret_cast<floatx4*>(p + i) = *reinterpret_cast<const floatx4*>(rows + i);
-    const int i = (n & ~3) + threadIdx.x;
-    if (i < n) p[i] = rows[i];
+    float* p = static_cast<float*>(a.out) + t * E;
+    if (E % 4 == 0) {
+      for (int i = q * 4; i < E; i += kLanes * 4)
+        *reinterpret_cast<floatx4*>(p + i) = *reinterpret_cast<const floatx4*>(row + i);
+    } else {
+      for (int i = q; i < E; i += kLanes) p[i] = row[i];
+    }
   }
 }
 
