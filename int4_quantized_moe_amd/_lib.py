@@ -167,11 +167,21 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _stream(stream) -> Optional[int]:
-    if stream is None:
-        import torch
+_current_stream = None
 
-        return torch.cuda.current_stream().cuda_stream
+
+def _stream(stream) -> Optional[int]:
+    global _current_stream
+    if stream is None:
+        if _current_stream is None:
+            import torch
+
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 0.1 us; a Stream object takes 2.5
+            if raw is None:
+                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+            else:
+                _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

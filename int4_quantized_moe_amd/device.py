@@ -96,6 +96,7 @@ class DeviceLayer:
         if isinstance(inputs, Checkpoint8):
             if inputs.shape[1] != self.cfg.hidden or inputs.codes.device != expert_ids.device:
                 raise ValueError(f"the checkpoint must be [tokens, {self.cfg.hidden}] on {expert_ids.device}")
+            _workspace(workspace, expert_ids.device)
             _lib.kt_moe_bwd_ckpt8(self.layer, qlen, inputs.fmt, inputs.codes, inputs.scales, expert_ids, route_weights,
                                   grad_output, grad_input, grad_route, *(grads[n] for n in LORA_NAMES), accumulate,
                                   grad_scale, workspace, stream)
@@ -133,7 +134,7 @@ def _checked(name, t, shape, dtype, device):
         return
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -161,22 +162,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-class _On:
-    """Makes the tensors' GPU the current one for a call, where it is not."""
+def _elsewhere(device) -> bool:
+    """Whether another GPU than the tensors' is the current one (a call then makes theirs current for its time)."""
+    return torch.cuda.current_device() != device.index
 
-    __slots__ = ("index", "before")
 
-    def __init__(self, device):
-        self.index = device.index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _workspace(workspace, device) -> None:
+    if workspace is not None and workspace.device != device:
+        raise ValueError(f"the workspace must be on {device}, not on {workspace.device}")
 
 
 _TYPES = {torch.bfloat16: _lib.KT_TYPE_BF16, torch.float32: _lib.KT_TYPE_F32}
@@ -220,8 +213,10 @@ def pack_checkpoint8(x: torch.Tensor, format: str = "int8", out: Optional[Checkp
                           _empty((rows, groups), torch.uint8, x.device, stream), format)
     elif out.format != format or out.shape != (rows, cols) or out.codes.device != x.device:
         raise ValueError(f"out must be a {format} checkpoint of {(rows, cols)} on {x.device}")
-    with _On(_gpu(x)):
-        _lib.kt_ckpt8_pack(x, rows, cols, out.fmt, out.codes, out.scales, stream)
+    if _elsewhere(_gpu(x)):
+        with torch.cuda.device(x.device):
+            return pack_checkpoint8(x, format, out, stream)
+    _lib.kt_ckpt8_pack(x, rows, cols, out.fmt, out.codes, out.scales, stream)
     return out
 
 
@@ -229,10 +224,12 @@ def unpack_checkpoint8(checkpoint: Checkpoint8, out: Optional[torch.Tensor] = No
     """The bf16 rows that a checkpoint stands for."""
     dev = checkpoint.codes.device
     _checked("out", out, checkpoint.shape, torch.bfloat16, dev)
-    with _On(_gpu(checkpoint.codes)):
-        if out is None:
-            out = _empty(checkpoint.shape, torch.bfloat16, dev, stream)
-        _lib.kt_ckpt8_unpack(checkpoint.codes, checkpoint.scales, *checkpoint.shape, checkpoint.fmt, out, stream)
+    if _elsewhere(_gpu(checkpoint.codes)):
+        with torch.cuda.device(dev):
+            return unpack_checkpoint8(checkpoint, out, stream)
+    if out is None:
+        out = _empty(checkpoint.shape, torch.bfloat16, dev, stream)
+    _lib.kt_ckpt8_unpack(checkpoint.codes, checkpoint.scales, *checkpoint.shape, checkpoint.fmt, out, stream)
     return out
 
 
@@ -275,13 +272,15 @@ class DeviceRouter:
         _checked("load", load, (self.num_experts,), torch.int32, dev)
         if self.bias is not None and self.bias.device != dev:
             raise ValueError(f"the bias is on {self.bias.device}, the logits are on {dev}")
-        with _On(_gpu(logits)):
-            if expert_ids is None:
-                expert_ids = _empty(shape, torch.int64, dev, stream)
-            if route_weights is None:
-                route_weights = _empty(shape, torch.float32, dev, stream)
-            _lib.kt_router_fwd(self._c[logits.dtype], tokens, logits, self.bias, token_mask, expert_ids, route_weights,
-                               load, accumulate, stream)
+        if _elsewhere(_gpu(logits)):
+            with torch.cuda.device(dev):
+                return self.forward(logits, token_mask, expert_ids, route_weights, load, accumulate, stream)
+        if expert_ids is None:
+            expert_ids = _empty(shape, torch.int64, dev, stream)
+        if route_weights is None:
+            route_weights = _empty(shape, torch.float32, dev, stream)
+        _lib.kt_router_fwd(self._c[logits.dtype], tokens, logits, self.bias, token_mask, expert_ids, route_weights, load,
+                           accumulate, stream)
         return expert_ids, route_weights
 
     def backward(self, logits, expert_ids, grad_route, grad_logits=None, stream=None):
@@ -291,10 +290,12 @@ class DeviceRouter:
         _checked("expert_ids", expert_ids, shape, torch.int64, dev)
         _checked("grad_route", grad_route, shape, torch.float32, dev)
         _checked("grad_logits", grad_logits, (tokens, self.num_experts), logits.dtype, dev)
-        with _On(_gpu(logits)):
-            if grad_logits is None:
-                grad_logits = _empty((tokens, self.num_experts), logits.dtype, dev, stream)
-            _lib.kt_router_bwd(self._c[logits.dtype], tokens, logits, expert_ids, grad_route, grad_logits, stream)
+        if _elsewhere(_gpu(logits)):
+            with torch.cuda.device(dev):
+                return self.backward(logits, expert_ids, grad_route, grad_logits, stream)
+        if grad_logits is None:
+            grad_logits = _empty((tokens, self.num_experts), logits.dtype, dev, stream)
+        _lib.kt_router_bwd(self._c[logits.dtype], tokens, logits, expert_ids, grad_route, grad_logits, stream)
         return grad_logits
 
     def update_bias(self, load, rate, stream=None) -> None:
@@ -302,7 +303,8 @@ class DeviceRouter:
         if self.bias is None:
             raise ValueError("this router has no bias")
         _checked("load", load, (self.num_experts,), torch.int32, self.bias.device)
-        with _On(_gpu(self.bias)):
+        _gpu(self.bias)
+        with torch.cuda.device(self.bias.device):
             _lib.kt_router_update_bias(self.bias, load, self.num_experts, rate, stream)
 
 
@@ -355,10 +357,13 @@ class DeviceLinear:
             raise ValueError("the output must be torch.bfloat16 or torch.float32")
         if output is not None:
             _checked("output", output, shape, output.dtype, dev)
-        with _On(_gpu(x)):
-            if output is None:
-                output = _empty(shape, dtype, dev, stream)
-            _lib.kt_linear_fwd(self.linear, tokens, x, residual, output, kind, preact, workspace, stream)
+        if _elsewhere(_gpu(x)):
+            with torch.cuda.device(dev):
+                return self.forward(x, workspace, residual, preact, output, dtype, stream)
+        _workspace(workspace, dev)
+        if output is None:
+            output = _empty(shape, dtype, dev, stream)
+        _lib.kt_linear_fwd(self.linear, tokens, x, residual, output, kind, preact, workspace, stream)
         return output
 
     def backward(self, x, grad_output, workspace, grads, preact=None, grad_input=None, grad_residual=None,
@@ -387,9 +392,13 @@ class DeviceLinear:
         d_weight, d_bias = grads.get("weight"), grads.get("bias")
         _checked("grads['weight']", d_weight, (self.out_features, self.in_features), torch.float32, dev)
         _checked("grads['bias']", d_bias, (self.out_features,), torch.float32, dev)
-        with _On(_gpu(grad_output)):
-            if grad_input is None and need_input:
-                grad_input = _empty(tuple(x.shape), torch.bfloat16, dev, stream)
-            _lib.kt_linear_bwd(self.linear, tokens, rows, ckpt, preact, grad_output, _TYPES[grad_output.dtype],
-                               grad_residual, grad_input, d_weight, d_bias, accumulate, grad_scale, workspace, stream)
+        if _elsewhere(_gpu(grad_output)):
+            with torch.cuda.device(dev):
+                return self.backward(x, grad_output, workspace, grads, preact, grad_input, grad_residual, accumulate,
+                                     grad_scale, stream, need_input)
+        _workspace(workspace, dev)
+        if grad_input is None and need_input:
+            grad_input = _empty(tuple(x.shape), torch.bfloat16, dev, stream)
+        _lib.kt_linear_bwd(self.linear, tokens, rows, ckpt, preact, grad_output, _TYPES[grad_output.dtype],
+                           grad_residual, grad_input, d_weight, d_bias, accumulate, grad_scale, workspace, stream)
         return grad_input
