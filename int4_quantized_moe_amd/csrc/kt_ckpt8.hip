@@ -284,6 +284,7 @@ int kt_ckpt8_pack(const uint16_t* x, int64_t rows, int64_t cols, int32_t format,
                   void* stream) {
   const int rc = check_ckpt8(x, rows, cols, format, codes, scales);
   if (rc) return rc;
+  if (rows * cols == 0) return set_error(KT_RAWINT4_OK, "");
   begin_launches();
   launch_ckpt8_pack(x, rows, cols, format, codes, scales, static_cast<hipStream_t>(stream));
   return finish_launches();
@@ -293,6 +294,7 @@ int kt_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, i
                     uint16_t* x, void* stream) {
   const int rc = check_ckpt8(x, rows, cols, format, codes, scales);
   if (rc) return rc;
+  if (rows * cols == 0) return set_error(KT_RAWINT4_OK, "");
   begin_launches();
   launch_ckpt8_unpack(codes, scales, rows, cols, format, x, static_cast<hipStream_t>(stream));
   return finish_launches();

@@ -839,25 +839,24 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     rc = check_caller_workspace(workspace, workspace_bytes, need);
     if (rc) return rc;
   }
+  if (tokens == 0) return set_error(KT_RAWINT4_OK, "");
   begin_launches();
-  if (tokens > 0) {
-    LinearGemm g{};
-    g.a = inputs;
-    g.lda = K;
-    g.b = linear->weight;
-    g.ldb = K;
-    g.M = tokens;
-    g.N = N;
-    g.K = K;
-    g.planes = 1;
-    g.bias = linear->bias;
-    g.residual = residual;
-    g.out = output;
-    g.out_f32 = output_type == KT_TYPE_F32;
-    g.preact = preact;
-    g.act = linear->activation;
-    launch_linear<kLinFwd>(g, s, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
-  }
+  LinearGemm g{};
+  g.a = inputs;
+  g.lda = K;
+  g.b = linear->weight;
+  g.ldb = K;
+  g.M = tokens;
+  g.N = N;
+  g.K = K;
+  g.planes = 1;
+  g.bias = linear->bias;
+  g.residual = residual;
+  g.out = output;
+  g.out_f32 = output_type == KT_TYPE_F32;
+  g.preact = preact;
+  g.act = linear->activation;
+  launch_linear<kLinFwd>(g, s, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
   return finish_launches();
 }
 

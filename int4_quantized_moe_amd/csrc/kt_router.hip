@@ -928,6 +928,7 @@ int kt_router_fwd(const kt_router* router, int32_t tokens, const void* logits, c
                logits,              bias,              token_mask,         expert_ids,
                route_weights};
   if (a.top_groups == a.G) a.G = 1;  // every group stays
+  if (tokens == 0 && (!load || accumulate)) return set_error(KT_RAWINT4_OK, "");
   begin_launches();
   if (tokens > 0) {
     const bool bf = router->logits_type == KT_TYPE_BF16, soft = router->score == KT_SCORE_SOFTMAX;
@@ -953,21 +954,20 @@ int kt_router_bwd(const kt_router* router, int32_t tokens, const void* logits, c
   if (!is_aligned(logits, 16) || !is_aligned(grad_logits, 16) || !is_aligned(expert_ids, 8) ||
       !is_aligned(grad_route, 4))
     return set_error(KT_RAWINT4_EINVAL, "logits and grad_logits must be 16-byte aligned, expert_ids 8-byte aligned");
+  if (tokens == 0) return set_error(KT_RAWINT4_OK, "");
   hipStream_t st = static_cast<hipStream_t>(stream);
   const RouterBwdArgs a{router->num_experts, router->top_k, router->renormalize != 0, router->scale,
                         logits,              expert_ids,    grad_route,               grad_logits};
   begin_launches();
-  if (tokens > 0) {
-    const bool bf = router->logits_type == KT_TYPE_BF16, soft = router->score == KT_SCORE_SOFTMAX;
-    if (soft && bf)
-      launch_route_bwd<KT_SCORE_SOFTMAX, true>(a, tokens, st);
-    else if (soft)
-      launch_route_bwd<KT_SCORE_SOFTMAX, false>(a, tokens, st);
-    else if (bf)
-      launch_route_bwd<KT_SCORE_SIGMOID, true>(a, tokens, st);
-    else
-      launch_route_bwd<KT_SCORE_SIGMOID, false>(a, tokens, st);
-  }
+  const bool bf = router->logits_type == KT_TYPE_BF16, soft = router->score == KT_SCORE_SOFTMAX;
+  if (soft && bf)
+    launch_route_bwd<KT_SCORE_SOFTMAX, true>(a, tokens, st);
+  else if (soft)
+    launch_route_bwd<KT_SCORE_SOFTMAX, false>(a, tokens, st);
+  else if (bf)
+    launch_route_bwd<KT_SCORE_SIGMOID, true>(a, tokens, st);
+  else
+    launch_route_bwd<KT_SCORE_SIGMOID, false>(a, tokens, st);
   return finish_launches();
 }
 

@@ -62,6 +62,14 @@ def test_forward_shapes(dev, t, k, n, dtype):
     _forward(dev, t, k, n, "silu", True, True, True, dtype, seed=10)
 
 
+@pytest.mark.parametrize("t,k,n", [(3471, 136, 3613), (6200, 8, 2056), (3471, 200, 3656)])
+def test_forward_large_tiles(dev, t, k, n):
+    """Shapes that the 256 x 256 tiles take, ragged in every direction."""
+    _say("large", t, k, n)
+    _forward(dev, t, k, n, "none", False, False, False, F32)
+    _forward(dev, t, k, n, "gelu", True, True, True, BF16, seed=10)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("bias,residual,preact", [(0, 0, 0), (1, 0, 1), (0, 1, 0), (1, 1, 1)])
 @pytest.mark.parametrize("t,k,n", [(5, 512, 40), (130, 136, 129), (300, 256, 260)])
@@ -181,6 +189,15 @@ def test_backward_shapes(dev, t, k, n, dtype):
     _say("backward", t, k, n, dtype)
     _backward(dev, t, k, n, "none", dtype, bias=False)
     _backward(dev, t, k, n, "silu", dtype, residual=True, seed=20)
+
+
+@pytest.mark.parametrize("t,k,n", [(3471, 3656, 75), (75, 3656, 3471), (130, 3656, 3472)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_backward_large_tiles(dev, t, k, n, dtype):
+    """Shapes whose grad_input or weight gradient the 256 x 256 tiles take."""
+    _say("large backward", t, k, n, dtype)
+    _backward(dev, t, k, n, "none", dtype, accumulate=True, scale=0.5)
+    _backward(dev, t, k, n, "silu", dtype, residual=True, ckpt="int8", seed=20)
 
 
 @pytest.mark.parametrize("act", ACTS)
