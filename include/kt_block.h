@@ -10,7 +10,8 @@
  * patterns, caller-owned workspaces (256-byte aligned), work enqueued on
  * `stream` of the current device and nothing else, no allocation of device
  * memory, no synchronisation, nothing that a stream capture refuses, the same
- * return codes, and kt_rawint4_last_error for the message.  Results depend on
+ * return codes, and kt_rawint4_last_error for the message.  Outputs overlap no
+ * other argument unless an entry point allows it.  Results depend on
  * the inputs alone, bit for bit: no kernel accumulates floating-point numbers
  * with atomics.  A workspace holds nothing between calls; calls that may run
  * at the same time, replays of captured graphs among them, need workspaces of

@@ -56,7 +56,9 @@ __device__ __forceinline__ float ckpt8_mult(int byte) {
 // one 16-byte store a lane.  FLAT: rows are whole groups, so the tensor is one
 // run of groups.  Otherwise rows start at any 2-byte (codes: 1-byte) address, for
 // which the hardware's unaligned accesses serve as well, and the last group
-// of a row, if it is shorter, goes value by value.
+// of a row, if it is shorter, goes value by value.  Bound by memory: 16384 x 7168
+// packs in 80 us (4.4 TB/s) and unpacks in 71 us (5.0), where a plain copy of 1
+// GiB reaches 5.1; half a wave a group, one value a lane, took 457 us for both.
 struct Ckpt8Args {
   int64_t rows, cols, ng;  // ng: groups per row
   const uint16_t* x;
@@ -226,7 +228,7 @@ static void launch_ckpt8_as(const Ckpt8Args& a, bool pack, hipStream_t st) {
 
 template <int FMT, bool FLAT>
 static void launch_ckpt8_units(const Ckpt8Args& a, bool pack, hipStream_t st) {
-  // four units a thread keep more loads in flight once the chip is full without them
+  // four units a thread keep more loads in flight once the chip is full without them (2^21 half groups: 8 waves a SIMD)
   if (a.rows * a.ng * 2 >= (int64_t)8 * 256 * 1024)
     launch_ckpt8_as<FMT, FLAT, 4>(a, pack, st);
   else

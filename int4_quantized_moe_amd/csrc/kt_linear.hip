@@ -71,8 +71,7 @@ struct LinearGemm {
   int64_t lda, ldb;      // row pitch (elements, a multiple of 8)
   int64_t a_width;       // columns of A's rows that exist (a multiple of 8), for a contraction across them
   int64_t M, N, K;
-  int planes;            // A is the sum of so many bf16 planes ...
-  int64_t a_plane;       // ... so many elements apart
+  int64_t a_plane;       // elements from one of A's planes to the next, where A is the sum of kMaxPlanes bf16 planes
   int splits;            // the steps of the contraction are dealt to so many blocks; over 1: part
   float* part;           // [splits][M][pn] partial sums
   int64_t pn;            // N rounded up to a multiple of 8
@@ -178,6 +177,9 @@ __device__ __forceinline__ void with_act(int act, F body) {
   }
 }
 
+// contraction values per step of the tiles
+constexpr int linear_step(int planes) { return planes == 1 ? 64 : 32; }
+
 // 16 zero bytes that copies past the end of a contraction read
 __device__ const uint32_t kZero16[4] = {0, 0, 0, 0};
 
@@ -209,10 +211,7 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-constexpr int kLinBK = 64;  // contraction values per step
-
-// One operand's tile of R rows (or columns) x kLinBK contraction values in LDS,
-// R * 128 bytes, filled by 16-byte copies straight from memory: a wave's copy
+// One operand's tile of R rows (or columns) x BK contraction values in LDS, filled by 16-byte copies straight from memory: a wave's copy
 // fills 1024 consecutive bytes, so the arrangement is made on the source side.
 //
 // Contiguous contraction: row r at r * 128, its 16-byte chunk c (8 values) at
@@ -225,9 +224,10 @@ constexpr int kLinBK = 64;  // contraction values per step
 // lane) is two transposing reads, each of 4 values k for 16 columns per 16
 // lanes; h(k) = (k & 3) | (k >> 3 & 1) << 2 spreads the 8 rows that two 16-lane
 // groups read together over all banks.
-template <int R, bool ACROSS>
+template <int R, bool ACROSS, int BK>
 struct LinTile {
-  static constexpr int kBytes = R * 2 * kLinBK;
+  static_assert(ACROSS || BK == 64, "rows of 128 bytes");
+  static constexpr int kBytes = R * 2 * BK;
   static constexpr int kCopies = kBytes / 1024;
 
   // the pair swizzle of contraction value k
@@ -264,15 +264,28 @@ struct LinTile {
 
 // A block of WM x WN waves computes BM x BN outputs, each wave BM / WM x BN / WN
 // of them as 16 x 16 MFMA tiles.  Two LDS buffers: while one step's tiles are
-// multiplied, the next step's are copied into the other.
-template <int KIND, int BM, int BN, int WM, int WN>
+// multiplied, the next step's are copied into the other.  A step is 64
+// contraction values, or 32 of PLANES = 3 planes of A, which share B's tile (the
+// planes one after another would copy and read B three times: d_weight of 4096 x
+// 7168 x 384 from fp32 gradients 84 us so against 77, of 8192 x 7168 x 2048 602
+// against 588).
+//
+// Bound by the MFMAs and, as near, by LDS: a 256 x 256 step takes 2048 cycles of
+// MFMAs per SIMD and 256 KB of LDS traffic per unit, also 2048 cycles (a wave's
+// 128 x 64 outputs reuse a fragment 4 to 8 times); 128 x 128 tiles take 768 LDS
+// cycles for 512 of MFMAs.  Reached: 1.27 PFLOP/s forward at 8192 x 7168 x 2048
+// and 1.23 in d_weight with three planes, where a library's plain product runs at
+// 1.31; the chip's power holds the clock below 2 GHz there.
+template <int KIND, int BM, int BN, int WM, int WN, int PLANES>
 __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(LinearGemm g) {
   constexpr bool kAcrossA = KIND == kLinDw, kAcrossB = KIND != kLinFwd;
-  typedef LinTile<BM, kAcrossA> TA;
-  typedef LinTile<BN, kAcrossB> TB;
+  constexpr int BK = linear_step(PLANES);
+  typedef LinTile<BM, kAcrossA, BK> TA;
+  typedef LinTile<BN, kAcrossB, BK> TB;
   constexpr int kWaves = WM * WN, kFm = BM / WM / 16, kFn = BN / WN / 16;
-  constexpr int kCa = TA::kCopies / kWaves, kCb = TB::kCopies / kWaves;
-  __shared__ __align__(1024) uint8_t lds[2][TA::kBytes + TB::kBytes];
+  constexpr int kCa = TA::kCopies / kWaves, kCb = TB::kCopies / kWaves, kOffB = PLANES * TA::kBytes;
+  static_assert(PLANES == 1 || (PLANES == kMaxPlanes && KIND == kLinDw), "planes");
+  __shared__ __align__(1024) uint8_t lds[2][kOffB + TB::kBytes];
 
   // tiles: each XCD (blocks reach them in turn) takes a contiguous run of the
   // order below, in which kGroup rows of tiles are walked column by column, so
@@ -287,8 +300,8 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
   const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(in / rows) * BN;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // the steps of this split: planes one after another, each of ceil(K / 64)
-  const int per_plane = (int)((g.K + kLinBK - 1) / kLinBK), total = per_plane * g.planes;
+  // the steps of this split
+  const int total = (int)((g.K + BK - 1) / BK);
   const int s0 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * blockIdx.y / g.splits));
   const int s1 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * (blockIdx.y + 1) / g.splits));
 
@@ -311,27 +324,34 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
   }
   const uint8_t* base_a = reinterpret_cast<const uint8_t*>(g.a + (kAcrossA ? m0 : m0 * g.lda));
   const uint8_t* base_b = reinterpret_cast<const uint8_t*>(g.b + (kAcrossB ? n0 : n0 * g.ldb));
-  const int64_t step_a = kAcrossA ? 2 * kLinBK * g.lda : 2 * kLinBK, step_b = kAcrossB ? 2 * kLinBK * g.ldb : 2 * kLinBK;
+  const int64_t step_a = kAcrossA ? 2 * BK * g.lda : 2 * BK, step_b = kAcrossB ? 2 * BK * g.ldb : 2 * BK;
 
-  int p = __builtin_amdgcn_readfirstlane(s0 / per_plane), ks = s0 - p * per_plane;  // plane and step of the next copy
+  int ks = s0;  // the next copy's step
   auto copy = [&](int buf) {
-    const uint8_t* pa = base_a + 2 * p * g.a_plane + ks * step_a;
     const uint8_t* pb = base_b + ks * step_b;
     const uint32_t la = lds_addr(&lds[buf][0]) + wave * kCa * 1024;
-    const uint32_t lb = lds_addr(&lds[buf][TA::kBytes]) + wave * kCb * 1024;
-    if ((int64_t)(ks + 1) * kLinBK <= g.K) {
+    const uint32_t lb = lds_addr(&lds[buf][kOffB]) + wave * kCb * 1024;
+    const bool whole = (int64_t)(ks + 1) * BK <= g.K;
+    const int left = (int)(g.K - (int64_t)ks * BK);  // values that exist
 #pragma unroll
-      for (int c = 0; c < kCa; ++c) dma16_off(pa, off_a[c], la + c * 1024);
+    for (int p = 0; p < PLANES; ++p) {
+      const uint8_t* pa = base_a + 2 * p * g.a_plane + ks * step_a;
+      if (whole) {
+#pragma unroll
+        for (int c = 0; c < kCa; ++c) dma16_off(pa, off_a[c], la + p * TA::kBytes + c * 1024);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCa; ++c) {
+          int row, col;
+          TA::place(wave * kCa + c, lane, row, col);
+          dma16((kAcrossA ? row : col) < left ? (const void*)(pa + off_a[c]) : kZero16, la + p * TA::kBytes + c * 1024);
+        }
+      }
+    }
+    if (whole) {
 #pragma unroll
       for (int c = 0; c < kCb; ++c) dma16_off(pb, off_b[c], lb + c * 1024);
     } else {
-      const int left = (int)(g.K - (int64_t)ks * kLinBK);  // values that exist
-#pragma unroll
-      for (int c = 0; c < kCa; ++c) {
-        int row, col;
-        TA::place(wave * kCa + c, lane, row, col);
-        dma16((kAcrossA ? row : col) < left ? (const void*)(pa + off_a[c]) : kZero16, la + c * 1024);
-      }
 #pragma unroll
       for (int c = 0; c < kCb; ++c) {
         int row, col;
@@ -339,34 +359,36 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
         dma16((kAcrossB ? row : col) < left ? (const void*)(pb + off_b[c]) : kZero16, lb + c * 1024);
       }
     }
-    if (++ks == per_plane) {
-      ks = 0;
-      ++p;
-    }
+    ++ks;
   };
 
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
   floatx4 acc[kFm][kFn] = {};
-  struct Frags {
-    u32x4 a[kFm], b[kFn];
+  struct FragsA {
+    u32x4 v[kFm];
   };
-  auto load = [&](Frags& f, int buf, int h) {
-    const uint8_t* ta = &lds[buf][0];
-    const uint8_t* tb = &lds[buf][TA::kBytes];
-#pragma unroll
-    for (int j = 0; j < kFn; ++j) f.b[j] = TB::fragment(tb, wn + 16 * j, h, lane);
-#pragma unroll
-    for (int i = 0; i < kFm; ++i) f.a[i] = TA::fragment(ta, wm + 16 * i, h, lane);
+  struct FragsB {
+    u32x4 v[kFn];
   };
-  auto multiply = [&](const Frags& f) {
+  // the fragments of half h of the step in buffer buf
+  auto load_a = [&](FragsA& f, int buf, int h) {
+#pragma unroll
+    for (int i = 0; i < kFm; ++i) f.v[i] = TA::fragment(&lds[buf][0], wm + 16 * i, h, lane);
+  };
+  auto load_b = [&](FragsB& f, int buf, int h) {
+#pragma unroll
+    for (int j = 0; j < kFn; ++j) f.v[j] = TB::fragment(&lds[buf][kOffB], wn + 16 * j, h, lane);
+  };
+  auto multiply = [&](const FragsA& a, const FragsB& b) {
 #pragma unroll
     for (int i = 0; i < kFm; ++i)
 #pragma unroll
-      for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(f.b[j], f.a[i], acc[i][j]);
+      for (int j = 0; j < kFn; ++j) acc[i][j] = mfma_bf16(b.v[j], a.v[i], acc[i][j]);
   };
+  constexpr int kReadsA = kFm * (kAcrossA ? 2 : 1), kReadsB = kFn * (kAcrossB ? 2 : 1);
   // spreads a phase's LDS reads over its MFMAs
-  auto spread = [] {
-    constexpr int kReads = kFm * (kAcrossA ? 2 : 1) + kFn * (kAcrossB ? 2 : 1), kMfma = kFm * kFn;
+  auto spread = [](auto reads, auto products) {
+    constexpr int kReads = decltype(reads)::value, kMfma = decltype(products)::value;
     constexpr int kPer = kMfma / kReads > 0 ? kMfma / kReads : 1;
 #pragma unroll
     for (int r = 0; r < kReads; ++r) {
@@ -375,47 +397,115 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
     }
     __builtin_amdgcn_sched_barrier(0);
   };
+  std::integral_constant<int, kReadsA + kReadsB> reads;
+  std::integral_constant<int, kReadsA / 2> reads_half;
+  std::integral_constant<int, kReadsA / 2 + kReadsB> reads_half_b;
+  std::integral_constant<int, kFm * kFn> products;
+  std::integral_constant<int, kFm * kFn / 2> products_half;
   auto fence = [] {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  // A step is two halves of 32 contraction values.  While one half is
-  // multiplied, the other half's (or the next step's first half's) fragments are
-  // read.  In the middle of a step every wave holds all of its tile in
-  // registers, so the copies of the step after next may overwrite it, and the
-  // next step's copies, issued a step ago, must have landed.
+  // every wave holds the rest of its tile in registers: the next step's copies, issued a step ago, must have
+  // landed, and the copies of the step after it may overwrite this step's buffer
+  auto turn_over = [&](int s, int buf) {
+    wait_vm_lgkm<0>();
+    fence();
+    __builtin_amdgcn_s_barrier();
+    fence();
+    if (s + 2 < s1) copy(buf);
+  };
+  // A step is two halves of 32 contraction values, or three planes of 32.  While
+  // one is multiplied, the next one's fragments are read (the next step's first
+  // ones during the last).
   if (s0 < s1) {
     copy(0);
     if (s0 + 1 < s1) {
       copy(1);
-      wait_vm_lgkm<kCa + kCb>();
+      wait_vm_lgkm<PLANES * kCa + kCb>();
     } else {
       wait_vm_lgkm<0>();
     }
     fence();
     __builtin_amdgcn_s_barrier();
     fence();
-    Frags f0, f1;
-    load(f0, 0, 0);
-    int buf = 0;
-    for (int s = s0; s + 1 < s1; ++s) {
-      load(f1, buf, 1);
-      multiply(f0);
-      spread();
-      fence();
-      wait_vm_lgkm<0>();
-      fence();
-      __builtin_amdgcn_s_barrier();
-      fence();
-      if (s + 2 < s1) copy(buf);
-      buf ^= 1;
-      load(f0, buf, 0);
-      multiply(f1);
-      spread();
+    FragsB b0, b1;
+    load_b(b0, 0, 0);
+    if constexpr (PLANES == 1) {
+      FragsA a0, a1;
+      load_a(a0, 0, 0);
+      int buf = 0;
+      for (int s = s0; s + 1 < s1; ++s) {
+        load_b(b1, buf, 1);
+        load_a(a1, buf, 1);
+        multiply(a0, b0);
+        spread(reads, products);
+        fence();
+        turn_over(s, buf);
+        buf ^= 1;
+        load_b(b0, buf, 0);
+        load_a(a0, buf, 0);
+        multiply(a1, b1);
+        spread(reads, products);
+      }
+      load_b(b1, buf, 1);
+      load_a(a1, buf, 1);
+      multiply(a0, b0);
+      multiply(a1, b1);
+    } else {
+      // by halves of A's rows: six half planes a step, each read while the one before is multiplied
+      constexpr int kHalf = kFm / 2;
+      u32x4 x[kHalf], y[kHalf];
+      auto load_half = [&](u32x4(&f)[kHalf], int buf, int p, int part) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+          f[i] = TA::fragment(&lds[buf][p * TA::kBytes], wm + 16 * (part * kHalf + i), 0, lane);
+      };
+      auto multiply_half = [&](const u32x4(&f)[kHalf], auto part) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i)
+#pragma unroll
+          for (int j = 0; j < kFn; ++j) {
+            constexpr int first = decltype(part)::value * kHalf;
+            acc[first + i][j] = mfma_bf16(b0.v[j], f[i], acc[first + i][j]);
+          }
+      };
+      std::integral_constant<int, 0> lower;
+      std::integral_constant<int, 1> upper;
+      // everything but the last half plane; y holds that one at the end
+      auto five = [&](int buf) __attribute__((always_inline)) {
+        load_half(y, buf, 0, 1);
+        multiply_half(x, lower);
+        spread(reads_half, products_half);
+        load_half(x, buf, 1, 0);
+        multiply_half(y, upper);
+        spread(reads_half, products_half);
+        load_half(y, buf, 1, 1);
+        multiply_half(x, lower);
+        spread(reads_half, products_half);
+        load_half(x, buf, 2, 0);
+        multiply_half(y, upper);
+        spread(reads_half, products_half);
+        load_half(y, buf, 2, 1);
+        multiply_half(x, lower);
+        spread(reads_half, products_half);
+      };
+      load_half(x, 0, 0, 0);
+      int buf = 0;
+      for (int s = s0; s + 1 < s1; ++s) {
+        five(buf);
+        fence();
+        turn_over(s, buf);
+        buf ^= 1;
+        load_b(b1, buf, 0);
+        load_half(x, buf, 0, 0);
+        multiply_half(y, upper);
+        spread(reads_half_b, products_half);
+        b0 = b1;
+      }
+      five(buf);
+      multiply_half(y, upper);
     }
-    load(f1, buf, 1);
-    multiply(f0);
-    multiply(f1);
   }
   // An MFMA tile's lane holds m = lane % 16 and n = 4 (lane / 16) .. + 3.  Each
   // wave turns 64 rows at a time in LDS of its own, so that a lane then holds 8
@@ -460,7 +550,8 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
 
 // The splits' partial sums and the epilogue: 64 outputs of 8 columns per block,
 // each wave sums every fourth split (so that their loads are in flight
-// together), wave 0 joins the four in order.
+// together), wave 0 joins the four in order.  Bound by reading the partial sums
+// (three of 384 x 7168: 8 us for 44 MB in and out, 5.4 TB/s from the caches).
 template <int KIND>
 __global__ __launch_bounds__(256) void k_linear_join(LinearGemm g) {
   __shared__ floatx4 red[3][2][64];
@@ -500,6 +591,8 @@ __global__ __launch_bounds__(256) void k_linear_join(LinearGemm g) {
 // inputs straight into fragments (32 bytes of a row per lane: a wave reads whole
 // 128-byte lines of 16 rows; lanes past the last column or token repeat it), and
 // their sums are joined through LDS in the waves' order.  One launch, no workspace.
+// One token through 7168 x 384 takes 6.7 us, six of them latency (launch, two
+// rounds of loads, the join): the weight's 5.5 MB alone are 1.1 us.
 template <int MT>
 __global__ __launch_bounds__(1024) void k_linear_few(LinearGemm g, int cols) {
   constexpr int kWaves = 16, kUnroll = MT == 1 ? 4 : MT == 2 ? 2 : 1;
@@ -598,7 +691,8 @@ __device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes])
 constexpr int kDzRows = 32, kDzCols = 256;
 
 // kDzCols columns x kDzRows rows per block, 8 columns a thread.  WIDE: N is a
-// multiple of 8, so that a thread's values are 16-byte pieces.
+// multiple of 8, so that a thread's values are 16-byte pieces.  Bound by memory:
+// 8192 x 2048 with an activation and three planes moves 168 MB in 41 us (4.1 TB/s).
 template <bool WIDE>
 __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
   __shared__ float red[8][kDzCols + 4];
@@ -716,8 +810,8 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
 //            tiles, d_weight 1.24 against 1.06, grad_input of 16384 x 2048 x 7168 1.25 against 1.01.  With
 //            fewer: 4096 x 2048 x 2048 (128 of them) 56 us against 38.
 //   splits   of the contraction, where 128 x 128 tiles alone leave units without the two blocks they can
-//            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 137 us with
-//            1, 93 with 2, 84 with 3 and 99 with 4), each with at least four steps.
+//            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 114 us with
+//            1, 89 with 2, 77 with 3 and 89 with 4), each with at least four steps.
 constexpr int kBlocksWanted = 512, kMinSteps = 4, kMaxSplits = 64;
 
 struct LinearShape {
@@ -734,7 +828,7 @@ static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K
     s.few = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     return s;
   }
-  const int64_t steps = (K + kLinBK - 1) / kLinBK * planes;
+  const int64_t steps = (K + linear_step(planes) - 1) / linear_step(planes);
   const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
   s.big = big >= 192;
   s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
@@ -764,9 +858,8 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   const int64_t N = L->out_features, K = L->in_features;
   p.pitch = round_up(N, 8);
   p.nb = (T + kDzRows - 1) / kDzRows;
-  // the shapes of calls with one plane need no more
   p.dx = linear_shape(kLinDx, T, K, N, 1);
-  p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);
+  p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);  // (with one plane no more splits)
   p.planes = 0;
   p.db = p.planes + round256(2 * kMaxPlanes * (size_t)T * (size_t)p.pitch);
   p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
@@ -776,7 +869,7 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   return p;
 }
 
-template <int KIND>
+template <int KIND, int PLANES = 1>
 static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipStream_t st) {
   g.splits = s.splits;
   g.part = part;
@@ -799,9 +892,9 @@ static void launch_linear(LinearGemm g, const LinearShape& s, float* part, hipSt
   }
   const dim3 grid((unsigned)s.tiles, (unsigned)s.splits);
   if (s.big)
-    k_linear<KIND, 256, 256, 2, 4><<<grid, 512, 0, st>>>(g);
+    k_linear<KIND, 256, 256, 2, 4, PLANES><<<grid, 512, 0, st>>>(g);
   else
-    k_linear<KIND, 128, 128, 2, 2><<<grid, 256, 0, st>>>(g);
+    k_linear<KIND, 128, 128, 2, 2, PLANES><<<grid, 256, 0, st>>>(g);
   note_launch();
   if (s.splits > 1) {
     k_linear_join<KIND><<<(unsigned)((g.M * (g.pn / 8) + 63) / 64), 256, 0, st>>>(g);
@@ -849,7 +942,6 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   g.M = tokens;
   g.N = N;
   g.K = K;
-  g.planes = 1;
   g.bias = linear->bias;
   g.residual = residual;
   g.out = output;
@@ -904,7 +996,8 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   if (rc) return rc;
   begin_launches();
   // a bf16 grad_output without activation is dz itself (its rows must start at 16 bytes)
-  const bool exact = !act && grad_output_type == KT_TYPE_BF16, direct = exact && N % 8 == 0;
+  const bool exact = !act && grad_output_type == KT_TYPE_BF16, products = grad_input || d_weight;
+  const bool direct = (exact && N % 8 == 0) || !products;
   const uint16_t* dz = static_cast<const uint16_t*>(grad_output);
   const int64_t pitch = direct ? N : p.pitch;
   const int planes = exact || !d_weight ? 1 : kMaxPlanes;
@@ -942,8 +1035,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.M = T;
     g.N = K;
     g.K = N;
-    g.planes = 1;
-    g.residual = grad_residual;
+      g.residual = grad_residual;
     g.out = grad_input;
     launch_linear<kLinDx>(g, p.dx, ws_ptr<float>(workspace, p.part), st);
   }
@@ -963,13 +1055,15 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.M = N;
     g.N = K;
     g.K = T;
-    g.planes = planes;
     g.a_plane = T * p.pitch;
     g.out = d_weight;
     g.accumulate = accumulate;
     g.scale = grad_scale;
     const LinearShape s = linear_shape(kLinDw, N, K, T, planes);
-    launch_linear<kLinDw>(g, s, ws_ptr<float>(workspace, p.part), st);
+    if (planes == 1)
+      launch_linear<kLinDw>(g, s, ws_ptr<float>(workspace, p.part), st);
+    else
+      launch_linear<kLinDw, kMaxPlanes>(g, s, ws_ptr<float>(workspace, p.part), st);
   }
   return finish_launches();
 }

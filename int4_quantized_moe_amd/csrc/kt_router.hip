@@ -59,6 +59,11 @@ __device__ __forceinline__ bool bad_logit(float l) {
 //
 // Groups (whole lanes each) are kept by their fp32 scores, and by scores to 64
 // bits where the border between kept and dropped lies within the fp32 error.
+//
+// Bound by instructions (about 1900 a wave of four tokens), then by latency where
+// one block a unit is all there is: 16384 tokens of 384 experts in 8 groups 18 us
+// (reading the logits alone: 5), 4096 tokens 11 us, one token 8 us.  Choosing
+// by k rounds of a block's best instead took 434 us.
 constexpr int kLanes = 16, kTokens = 16, kList = 48, kMaxVpl = 32;
 
 template <int CTRL>
@@ -394,8 +399,8 @@ __device__ __forceinline__ void wave_best(double& v, int& i) {
   }
 }
 
-// One block per token, c of every expert in LDS, top_k rounds of the block's
-// best.  Takes any E, k and group shape.
+// One block per token, c of every expert in LDS to 64 bits, top_k rounds of the
+// block's best.  Takes any E, k and group shape; 384 experts by top 8: 26 ns a token.
 template <int SCORE, bool BF16>
 __global__ __launch_bounds__(kAnyThreads) void k_route_any(RouterArgs a) {
   __shared__ double c[KT_RAWINT4_MAX_EXPERTS];
@@ -579,7 +584,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // Up to 512 experts and 16 slots: 16 tokens a block, 16 lanes each.  A token's
 // logits are staged in LDS and turned into -s (sum ds s) in place, the chosen
-// experts' values are put over those, and the row is written back whole.
+// experts' values are put over those, and the row is written back whole.  16384
+// tokens of 384 experts in bf16 by softmax take 11 us (25 MB; a plain copy of them:
+// 5), 4096 in fp32 6.6 us, of which launch and latency are most.
 template <int SCORE, bool BF16, int VPL>
 __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t tokens) {
   __shared__ __align__(16) float rows[kTokens][kLanes * VPL + kRowPad];
