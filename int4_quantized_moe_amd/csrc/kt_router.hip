@@ -16,7 +16,7 @@
 namespace kt {
 
 struct RouterArgs {
-  int E, k, G, per, top_groups, group_top;
+  int E, k, G, per, top_groups, group_top;  // G = 1 (per = E) where every group stays
   int renorm;
   float scale;
   const void* logits;
@@ -44,10 +44,9 @@ __device__ __forceinline__ bool bad_logit(float l) {
 // ---------------------------------------------------------------- 16 lanes a token
 
 // Up to 512 experts and 16 choices: a block routes 16 tokens, 16 lanes each.
-// A token's logits are staged in LDS; a lane holds v = ceil(E / 16) of its
-// experts.  With groups, lg = per / v lanes share a group's experts in turn
-// (lane q: group q / lg, experts q % lg, q % lg + lg, ... of it); without, all
-// 16 lanes share all experts so (lg = 16).
+// A token's logits are staged in LDS.  Of G groups of `per` experts, lg = 16 / G
+// (rounded down) lanes share one: lane q has group q / lg and its experts q %
+// lg, q % lg + lg, ..., at most VPL of them (without groups: G = 1, lg = 16).
 //
 // The choice.  With fp32 keys (the logit itself without a bias, which orders as
 // s does; else s + b to within tol / 2) let t be the k-th largest of the 16
@@ -153,7 +152,7 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
   __shared__ int sel[kTokens][kLanes];
   __shared__ int hist[kLanes * VPL];
   const int64_t t0 = (int64_t)blockIdx.x * kTokens;
-  const int E = a.E, k = a.k, v = (E + kLanes - 1) / kLanes;
+  const int E = a.E, k = a.k;
   const int q = threadIdx.x & 15, tok = threadIdx.x >> 4;
   const int64_t t = t0 + tok;
   float* row = rows[tok];
@@ -166,9 +165,9 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
     hist[e] = 0;
   }
   bad_bias = __syncthreads_or(bad_bias);
-  const int lg = a.G > 1 ? a.per / v : kLanes, e0 = a.G > 1 ? q / lg * a.per + q % lg : q;
-  // this lane's experts are e0 + lg i, i < own
-  const int own = a.G > 1 ? (q < a.G * lg ? v : 0) : max(0, (E - q + kLanes - 1) / kLanes);
+  const int lg = kLanes / a.G, g = q / lg;  // lanes per group, this lane's group (from G on: none)
+  // this lane's experts are e0 + lg i, i < own.  With per <= lg VPL, e0 + lg i stays below 16 VPL for every i < VPL.
+  const int e0 = g < a.G ? g * a.per + q % lg : 0, own = g < a.G ? max(0, (a.per - q % lg + lg - 1) / lg) : 0;
   const bool exact = a.bias == nullptr;
 
   // (reads past a token's logits stay inside the array; the fp32 keys use the hardware's exponential and
@@ -179,7 +178,7 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
   bool odd = false;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const float x = row[min(e0 + lg * i, kLanes * VPL - 1)];
+    const float x = row[e0 + lg * i];
     l[i] = i < own ? x : -INFINITY;
     odd |= bad_logit<SCORE>(l[i]);
     mx = fmaxf(mx, l[i]);
@@ -220,9 +219,9 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
   for (int i = 0; i < VPL; ++i) {
     key[i] = l[i];
     if (!exact) {
-      const float c = score_key(l[i]) + bias[min(e0 + lg * i, E - 1)];
+      const float c = score_key(l[i]) + bias[e0 + lg * i];
       key[i] = l[i] == -INFINITY ? -INFINITY : c;
-      big = fmaxf(big, fabsf(c) < INFINITY ? fabsf(c) : 0.f);
+      big = fmaxf(big, key[i] > -INFINITY ? fabsf(c) : 0.f);
     }
   }
   // twice the error of a key: s within 2^-18 (softmax: some forty roundings of s and of s |l - m| <= 0.37;
@@ -236,7 +235,6 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
     best = fmaxf(best, key[i]);
   }
   if (a.G > 1) {
-    const int g = q / lg;
     const bool used = g < a.G;
     // keys whose sums the groups compare: c, or s where there is no bias
     float b1 = best, b2 = second;
@@ -868,8 +866,7 @@ static void launch_load(const int64_t* ids, int64_t n, int E, int accumulate, in
 
 // body(VPL as a constant) for the experts of a lane
 template <typename F>
-static void with_vpl(int E, F body) {
-  const int v = (E + kLanes - 1) / kLanes;
+static void with_vpl(int v, F body) {
   if (v <= 4)
     body(std::integral_constant<int, 4>());
   else if (v <= 8)
@@ -885,10 +882,10 @@ static void with_vpl(int E, F body) {
 // 16 lanes a token where they serve, else a block a token.
 template <int SCORE, bool BF16>
 static void launch_route(const RouterArgs& a, int64_t tokens, int32_t* load, int accumulate, hipStream_t st) {
-  const int v = (a.E + kLanes - 1) / kLanes;
-  if (v <= kMaxVpl && a.k <= kLanes && (a.G == 1 || a.per % v == 0)) {
+  const int lg = a.G <= kLanes ? kLanes / a.G : 0, v = lg ? (a.per + lg - 1) / lg : kMaxVpl + 1;
+  if (v <= kMaxVpl && a.k <= kLanes) {
     if (load && !accumulate) launch_zero_i32(load, a.E, st);
-    with_vpl(a.E, [&](auto vpl) {
+    with_vpl(v, [&](auto vpl) {
       k_route<SCORE, BF16, decltype(vpl)::value>
           <<<(unsigned)((tokens + kTokens - 1) / kTokens), 256, 0, st>>>(a, tokens, load);
     });
@@ -903,7 +900,7 @@ static void launch_route(const RouterArgs& a, int64_t tokens, int32_t* load, int
 template <int SCORE, bool BF16>
 static void launch_route_bwd(const RouterBwdArgs& a, int64_t tokens, hipStream_t st) {
   if (a.E <= kLanes * kMaxVpl && a.k <= kLanes) {
-    with_vpl(a.E, [&](auto vpl) {
+    with_vpl((a.E + kLanes - 1) / kLanes, [&](auto vpl) {
       k_route_bwd<SCORE, BF16, decltype(vpl)::value>
           <<<(unsigned)((tokens + kTokens - 1) / kTokens), 256, 0, st>>>(a, tokens);
     });
@@ -934,7 +931,10 @@ int kt_router_fwd(const kt_router* router, int32_t tokens, const void* logits, c
                router->top_groups,  router->group_top, router->renormalize != 0, router->scale,
                logits,              bias,              token_mask,         expert_ids,
                route_weights};
-  if (a.top_groups == a.G) a.G = 1;  // every group stays
+  if (a.top_groups == a.G) {  // every group stays
+    a.G = 1;
+    a.per = a.E;
+  }
   if (tokens == 0 && (!load || accumulate)) return set_error(KT_RAWINT4_OK, "");
   begin_launches();
   if (tokens > 0) {

@@ -74,7 +74,8 @@ def test_choice_and_weights(dev, t, e, k, score, bf16, biased):
 @pytest.mark.parametrize("e,groups,top_groups,group_top,k", [
     (384, 8, 4, 2, 8), (384, 8, 4, 1, 8), (256, 8, 4, 2, 8), (256, 8, 1, 2, 8), (160, 8, 3, 1, 6), (64, 4, 2, 2, 6),
     (60, 4, 2, 2, 6), (24, 8, 3, 2, 8), (16, 16, 5, 1, 5), (128, 64, 40, 2, 12), (8, 2, 2, 2, 3), (1024, 16, 4, 2, 10),
-    (512, 2, 1, 2, 16), (32, 2, 1, 2, 16),
+    (512, 2, 1, 2, 16), (32, 2, 1, 2, 16), (104, 8, 5, 2, 12), (96, 3, 2, 2, 7), (85, 5, 2, 1, 11), (117, 9, 4, 2, 9),
+    (320, 10, 3, 2, 8), (480, 15, 7, 2, 16), (26, 13, 6, 2, 4), (512, 16, 4, 2, 8), (136, 17, 4, 2, 8), (528, 16, 4, 2, 8),
 ])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
