@@ -811,8 +811,10 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
 //            fewer: 4096 x 2048 x 2048 (128 of them) 56 us against 38.
 //   splits   of the contraction, where 128 x 128 tiles alone leave units without the two blocks they can
 //            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 114 us with
-//            1, 89 with 2, 77 with 3 and 89 with 4), each with at least four steps.
-constexpr int kBlocksWanted = 512, kMinSteps = 4, kMaxSplits = 64;
+//            1, 89 with 2, 77 with 3 and 89 with 4), each with at least four steps, or eight above 64 rows,
+//            where the partial sums cost more (2048 x 2048, 512 tokens: 21 us with 4 splits of 8 steps, 25 with
+//            8 of 4; 7168 x 384, 32 tokens: 11 us with 28 splits of 4 steps, 13 with 14 of 8).
+constexpr int kBlocksWanted = 512, kMaxSplits = 64;
 
 struct LinearShape {
   int few;   // 16-row tiles of k_linear_few (0: not used)
@@ -833,7 +835,8 @@ static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K
   s.big = big >= 192;
   s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
   int64_t splits = s.big || s.tiles == 0 ? 1 : kBlocksWanted / s.tiles;
-  if (splits > steps / kMinSteps) splits = steps / kMinSteps;
+  const int64_t least = M <= 64 ? 4 : 8;
+  if (splits > steps / least) splits = steps / least;
   if (splits > kMaxSplits) splits = kMaxSplits;
   if (splits > 1) s.splits = (int)splits;
   return s;
