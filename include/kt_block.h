@@ -66,7 +66,8 @@ typedef struct kt_router {
  *   route_weights [tokens, k] fp32: scale * s / (renormalize ? sum of the k s
  *   + 1e-20 : 1).
  * Choices are made on c to 64 bits (without a bias on the logits, which order
- * as s does); equal values go to the lower index.  They are what kt_rawint4_moe_fwd takes as expert_ids and route_weights.
+ * as s does); equal values go to the lower index.  The outputs are what
+ * kt_rawint4_moe_fwd takes as expert_ids and route_weights.
  *   - An expert whose logit or bias is -inf is never chosen; where fewer than
  *     k are left, the other slots hold id -1 (which the experts drop) and
  *     weight 0.  Its logit counts in the softmax as a probability of 0.
@@ -211,7 +212,8 @@ typedef struct kt_ckpt8 {
  * product.  grad_input, d_weight and d_bias may each be NULL: not
  * computed.  d_bias needs no bias in the layer.
  * d_weight and d_bias come from dz to fp32's precision (a dz that bf16 does
- * not hold takes part as the sum of two bf16 numbers), grad_input from dz in bf16.
+ * not hold takes part as the sum of three bf16 numbers, so an infinite input
+ * may give a NaN where dz times it is infinite), grad_input from dz in bf16.
  * tokens == 0: only the window rule runs.  The workspace is larger for calls
  * with a checkpoint (from_checkpoint nonzero); such a one serves both.
  */

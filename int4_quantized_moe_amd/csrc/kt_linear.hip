@@ -27,7 +27,8 @@ __device__ __forceinline__ float act_value(int act, float z) {
   switch (act) {
     case KT_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
     case KT_ACT_SILU: return fmaxf(z, -128.f) * sigmoid_lin(z);  // the sigmoid ends at 2^-127, not at 0
-    case KT_ACT_GELU: return 0.5f * z * (1.f + erff(z * kInvSqrt2));
+    // (erfc keeps the digits of a small Phi, where 1 + erf has none left; -infinity gives -0)
+    case KT_ACT_GELU: return 0.5f * fmaxf(z, -16.f) * erfcf(-z * kInvSqrt2);
     case KT_ACT_GELU_TANH: return fmaxf(z, -16.f) * sigmoid_lin(z != z ? z : gelu_tanh_arg(z));
     default: return z;
   }
@@ -42,7 +43,7 @@ __device__ __forceinline__ float act_slope(int act, float z) {
     }
     case KT_ACT_GELU: {
       const float c = fminf(fmaxf(z, -16.f), 16.f);
-      return 0.5f * (1.f + erff(z * kInvSqrt2)) + c * expf(-0.5f * c * c) * kInvSqrt2Pi;
+      return 0.5f * erfcf(-z * kInvSqrt2) + c * expf(-0.5f * c * c) * kInvSqrt2Pi;
     }
     case KT_ACT_GELU_TANH: {
       if (z != z) return z;
@@ -802,9 +803,10 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
 }
 
 // How a product runs.
-//   few      forward of few tokens: k_linear_few.  7168 x 384: 6.7 us for one token and 11.2 for 16 against
-//            12.2 and 13.4 us by tiles; 512 x 384: 4.4 us for 64 against 8.3.  It reads the inputs once per
-//            block, so it loses where tokens and K are large (7168 x 384, 64 tokens: 30 against 14.5 us).
+//   few      forward of few tokens: k_linear_few.  7168 x 384: 6.7 us for one token, 11.2 for 16, where tiles
+//            with their splits and joining launch take 11.1 us for 32 and no less for fewer; 2048 x 7168:
+//            10.1 us for 16 tokens against 15; 512 x 384: 4.4 us for 64 against 8.3.  It reads the inputs once
+//            per block, so it loses where tokens and K are large (7168 x 384, 64 tokens: 30 against 11.7 us).
 //   big      256 x 256 tiles, where they fill three quarters of the chip (two rows of fragments then serve
 //            twice the MFMAs).  Forward of 8192 x 7168 x 2048: 1.27 against 1.11 PFLOP/s with 128 x 128
 //            tiles, d_weight 1.24 against 1.06, grad_input of 16384 x 2048 x 7168 1.25 against 1.01.  With
@@ -990,7 +992,11 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (T == 0) {
     begin_launches();
-    if (!accumulate && d_weight) launch_fill_zero_f32(d_weight, N * K, st);
+    if (!accumulate && d_weight) {
+      const int64_t most = (int64_t)1 << 31;  // N K may be 2^32, more threads than a launch takes
+      for (int64_t i = 0; i < N * K; i += most)
+        launch_fill_zero_f32(d_weight + i, N * K - i < most ? N * K - i : most, st);
+    }
     if (!accumulate && d_bias) launch_fill_zero_f32(d_bias, N, st);
     return finish_launches();
   }
@@ -1038,7 +1044,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.M = T;
     g.N = K;
     g.K = N;
-      g.residual = grad_residual;
+    g.residual = grad_residual;
     g.out = grad_input;
     launch_linear<kLinDx>(g, p.dx, ws_ptr<float>(workspace, p.part), st);
   }

@@ -2,6 +2,8 @@
 products within the bounds derived in block_reference.  Each case prints its
 name first."""
 
+import math
+
 import pytest
 
 from tests import block_reference as R
@@ -152,6 +154,46 @@ def test_extreme_preactivations(dev, act):
     dx = lin.backward(x, torch.ones(16, 8, dtype=BF16, device="cuda"), lin.backward_workspace(16), grads, preact=z)
     slope = torch.where(zd < -40, 0.0, torch.where(zd > 40, 1.0, R.act_grad(lim, act)))
     R.within("slope", dx[:, 0], 8 * slope, 2 * R.UB * (8 * slope).abs() + 1e-5)
+
+
+def test_gelu_keeps_the_digits_of_its_tail(dev):
+    """z Phi(z) and its slope for z far below 0, relative to their own size.  erfc is within 16 units of
+    its last place (2^-23), and its argument u = z / sqrt(2) within two roundings, which it magnifies by 2 u^2 + 1;
+    the slope's exponential magnifies z^2 / 2's three roundings by z^2 / 2."""
+    _say("gelu's tail")
+    v = torch.tensor([-0.5, -1, -2, -3, -4, -5, -6, -7, -8, -9, -10, -10.5, -11, -11.5, -11.75, -12], dtype=F32)
+    x = torch.zeros(16, 16, dtype=BF16, device="cuda")
+    x[:, 0] = v.to(BF16).cuda()
+    w = torch.zeros(8, 16, dtype=BF16, device="cuda")
+    w[:, 0] = 1
+    lin = dev.DeviceLinear(w, None, "gelu")
+    z = torch.empty(16, 8, dtype=BF16, device="cuda")
+    y = lin.forward(x, lin.workspace(16), preact=z, dtype=F32)
+    zd = v.double()
+    want = R.act(zd, "gelu")
+    rel = 16 * 2.0**-23 + (zd * zd + 1) * 2.0**-23 + 4 * R.U
+    R.within("value", y[:, 3], want, rel * want.abs())
+    dx = lin.backward(x, torch.ones(16, 8, dtype=BF16, device="cuda"), lin.backward_workspace(16), {}, preact=z)
+    slope = R.act_grad(zd, "gelu")
+    parts = R.act(zd, "gelu").abs() / zd.abs() + zd.abs() * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    R.within("slope", dx[:, 0], 8 * slope, 8 * (2.01 * R.UB * slope.abs() + (rel + 3 * zd * zd * R.U) * parts))
+
+
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_activations_of_minus_infinity(dev, act):
+    """Their limit there is 0, and so is their slope's."""
+    _say("minus infinity", act)
+    for t in (3, 200):
+        x = torch.zeros(t, 16, dtype=BF16, device="cuda")
+        x[:, 0] = -float("inf")
+        w = torch.zeros(8, 16, dtype=BF16, device="cuda")
+        w[:, 0] = 1
+        lin = dev.DeviceLinear(w, None, act)
+        z = torch.empty(t, 8, dtype=BF16, device="cuda")
+        y = lin.forward(x, lin.workspace(t), preact=z, dtype=F32)
+        assert torch.isneginf(z).all() and (y == 0).all()
+        dx = lin.backward(x, torch.ones(t, 8, dtype=BF16, device="cuda"), lin.backward_workspace(t), {}, preact=z)
+        assert (dx == 0).all()
 
 
 # ---------------------------------------------------------------- gradients
