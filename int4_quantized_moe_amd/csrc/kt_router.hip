@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256) void k_route(RouterArgs a, int64_t tokens, int
   int id = q < k ? sel[tok][q] : -1;
   float s = id >= 0 ? score32(row[id]) : 0.f;
   const float total = row16_sum(s);
-  float w = id >= 0 ? (a.renorm ? s * (a.scale / (total + 1e-20f)) : s * a.scale) : 0.f;
+  float w = id >= 0 ? (a.renorm ? s / (total + 1e-20f) : s) * a.scale : 0.f;
   if (bad) {
     id = q;
     w = __uint_as_float(0x7fc00000u);
@@ -530,10 +530,10 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_any(RouterArgs a) {
     }
     __syncthreads();  // before the next round's owner adds to sum_s
   }
-  const float mul = a.renorm ? (float)((double)a.scale / (sum_s + 1e-20)) : a.scale;
+  const double mul = a.renorm ? (double)a.scale / (sum_s + 1e-20) : (double)a.scale;
   for (int q = tid; q < a.k; q += kAnyThreads) {
     if (q < j) {
-      w[q] *= mul;
+      w[q] = (float)(w[q] * mul);
     } else {
       ids[q] = -1;
       w[q] = 0.f;

@@ -149,6 +149,13 @@ def test_masks_infinities_and_nans(dev, e, k, score, groups):
         _check(dev, l, k, bias=b, mask=mask, **cfg)
 
 
+@pytest.mark.parametrize("e,k", [(384, 8), (600, 20)])
+def test_scores_that_vanish_under_a_large_scale(dev, e, k):
+    """Every s is 0 in fp32: the weights are 0 however large scale / 1e-20 is."""
+    _say("large scale", e, k)
+    _check(dev, _logits(9, 37, e) - 300, k, score="sigmoid", scale=1e25)
+
+
 def test_no_tokens_and_load_window(dev):
     _say("load")
     router = dev.DeviceRouter(48, 4, score="sigmoid")
