@@ -91,16 +91,24 @@ class DeviceLayer:
         ``inputs`` may be a Checkpoint8 of the forward's inputs: the backward then always reruns the
         forward, in a checkpoint_workspace()."""
         qlen = inputs.shape[0]
-        if grad_input is None:
-            grad_input = torch.empty((qlen, self.cfg.hidden), dtype=torch.bfloat16, device=self.device)
         if isinstance(inputs, Checkpoint8):
-            if inputs.shape[1] != self.cfg.hidden or inputs.codes.device != expert_ids.device:
-                raise ValueError(f"the checkpoint must be [tokens, {self.cfg.hidden}] on {expert_ids.device}")
-            _workspace(workspace, expert_ids.device)
+            dev, rows, slots = inputs.codes.device, (qlen, self.cfg.hidden), (qlen, self.cfg.top_k)
+            if inputs.shape != rows:
+                raise ValueError(f"the checkpoint must be [tokens, {self.cfg.hidden}], not {inputs.shape}")
+            for name, t, shape, dtype in (
+                    ("expert_ids", expert_ids, slots, torch.int64), ("route_weights", route_weights, slots, torch.float32),
+                    ("grad_output", grad_output, rows, torch.bfloat16), ("grad_input", grad_input, rows, torch.bfloat16),
+                    ("grad_route", grad_route, slots, torch.float32)):
+                _checked(name, t, shape, dtype, dev)
+            _workspace(workspace, _gpu(inputs.codes))
+            if grad_input is None:
+                grad_input = _empty(rows, torch.bfloat16, dev, stream)
             _lib.kt_moe_bwd_ckpt8(self.layer, qlen, inputs.fmt, inputs.codes, inputs.scales, expert_ids, route_weights,
                                   grad_output, grad_input, grad_route, *(grads[n] for n in LORA_NAMES), accumulate,
                                   grad_scale, workspace, stream)
             return grad_input, grad_route
+        if grad_input is None:
+            grad_input = torch.empty((qlen, self.cfg.hidden), dtype=torch.bfloat16, device=self.device)
         fn = _lib.kt_rawint4_moe_bwd_recompute if recompute else _lib.kt_rawint4_moe_bwd
         fn(self.layer, qlen, inputs, expert_ids, route_weights, grad_output, grad_input, grad_route,
            *(grads[n] for n in LORA_NAMES), accumulate, grad_scale, workspace, stream)

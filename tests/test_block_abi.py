@@ -9,7 +9,7 @@ import re
 import pytest
 
 import int4_quantized_moe_amd as kt
-from int4_quantized_moe_amd import _lib
+from int4_quantized_moe_amd import _lib, workloads
 
 from .conftest import ROOT
 
@@ -182,6 +182,23 @@ def test_experts_backward_from_a_checkpoint_refuses():
     _fails(call(ws=None), "workspace")
     _fails(call(ws=FAKE + 8), "aligned")
     _fails(call(nbytes=need - 256), "smaller", kt.KT_RAWINT4_EWORKSPACE)
+
+
+def test_layer_class_refuses_a_checkpoint_of_other_sizes():
+    layer = object.__new__(device.DeviceLayer)
+    layer.cfg = workloads.LayerConfig("small", 8, 2, 64, 32, 4, 8.0, 5, 2.0)
+    t = 5
+    ck = device.Checkpoint8(torch.zeros(t, 64, dtype=torch.int8), torch.zeros(t, 2, dtype=torch.uint8), "int8")
+    narrow = device.Checkpoint8(torch.zeros(t, 32, dtype=torch.int8), torch.zeros(t, 1, dtype=torch.uint8), "int8")
+    ids, rw, dy = torch.zeros(t, 2, dtype=torch.int64), torch.zeros(t, 2), torch.zeros(t, 64, dtype=torch.bfloat16)
+    for args, kw, word in (((narrow, ids, rw, dy), {}, "checkpoint must be"), ((ck, ids[:4], rw, dy), {}, "expert_ids"),
+                           ((ck, ids.int(), rw, dy), {}, "expert_ids"), ((ck, ids, rw[:, :1], dy), {}, "route_weights"),
+                           ((ck, ids, rw, dy.float()), {}, "grad_output"), ((ck, ids, rw, dy[:4]), {}, "grad_output"),
+                           ((ck, ids, rw, dy), dict(grad_input=dy[:4]), "grad_input"),
+                           ((ck, ids, rw, dy), dict(grad_route=rw.double()), "grad_route"),
+                           ((ck, ids, rw, dy), {}, "GPU")):
+        with pytest.raises(ValueError, match=word):
+            layer.backward(*args, None, {}, **kw)
 
 
 # ---------------------------------------------------------------- dense products
