@@ -167,21 +167,26 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_current_stream = None
+_raw_stream = None
+
+
+def device_stream(index: int) -> int:
+    """The handle of torch's current stream on GPU ``index``."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        # 0.1 us; a Stream object takes 2.5
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
 
 
 def _stream(stream) -> Optional[int]:
-    global _current_stream
     if stream is None:
-        if _current_stream is None:
-            import torch
+        import torch
 
-            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 0.1 us; a Stream object takes 2.5
-            if raw is None:
-                _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
-            else:
-                _current_stream = lambda: raw(torch.cuda.current_device())  # noqa: E731
-        return _current_stream()
+        return device_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

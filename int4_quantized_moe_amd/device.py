@@ -143,7 +143,7 @@ def _checked(name, t, shape, dtype, device):
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {shape}, not {tuple(t.shape)}")
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if t.device != device:
@@ -151,7 +151,7 @@ def _checked(name, t, shape, dtype, device):
 
 
 def _gpu(t):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"tensors must be on a GPU, not on {t.device}")
     return t.device
 
@@ -170,9 +170,18 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+# (current_device() asks first whether the GPUs are in use; a tensor on one answers that)
+_current_index = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _elsewhere(device) -> bool:
     """Whether another GPU than the tensors' is the current one (a call then makes theirs current for its time)."""
-    return torch.cuda.current_device() != device.index
+    return _current_index() != device.index
+
+
+def _handle(stream, device):
+    """``stream``, or the device's current one."""
+    return _lib.device_stream(device.index) if stream is None else stream
 
 
 def _workspace(workspace, device) -> None:
@@ -224,7 +233,7 @@ def pack_checkpoint8(x: torch.Tensor, format: str = "int8", out: Optional[Checkp
     if _elsewhere(_gpu(x)):
         with torch.cuda.device(x.device):
             return pack_checkpoint8(x, format, out, stream)
-    _lib.kt_ckpt8_pack(x, rows, cols, out.fmt, out.codes, out.scales, stream)
+    _lib.kt_ckpt8_pack(x, rows, cols, out.fmt, out.codes, out.scales, _handle(stream, x.device))
     return out
 
 
@@ -237,7 +246,8 @@ def unpack_checkpoint8(checkpoint: Checkpoint8, out: Optional[torch.Tensor] = No
             return unpack_checkpoint8(checkpoint, out, stream)
     if out is None:
         out = _empty(checkpoint.shape, torch.bfloat16, dev, stream)
-    _lib.kt_ckpt8_unpack(checkpoint.codes, checkpoint.scales, *checkpoint.shape, checkpoint.fmt, out, stream)
+    _lib.kt_ckpt8_unpack(checkpoint.codes, checkpoint.scales, *checkpoint.shape, checkpoint.fmt, out,
+                         _handle(stream, dev))
     return out
 
 
@@ -288,7 +298,7 @@ class DeviceRouter:
         if route_weights is None:
             route_weights = _empty(shape, torch.float32, dev, stream)
         _lib.kt_router_fwd(self._c[logits.dtype], tokens, logits, self.bias, token_mask, expert_ids, route_weights, load,
-                           accumulate, stream)
+                           accumulate, _handle(stream, dev))
         return expert_ids, route_weights
 
     def backward(self, logits, expert_ids, grad_route, grad_logits=None, stream=None):
@@ -303,7 +313,8 @@ class DeviceRouter:
                 return self.backward(logits, expert_ids, grad_route, grad_logits, stream)
         if grad_logits is None:
             grad_logits = _empty((tokens, self.num_experts), logits.dtype, dev, stream)
-        _lib.kt_router_bwd(self._c[logits.dtype], tokens, logits, expert_ids, grad_route, grad_logits, stream)
+        _lib.kt_router_bwd(self._c[logits.dtype], tokens, logits, expert_ids, grad_route, grad_logits,
+                           _handle(stream, dev))
         return grad_logits
 
     def update_bias(self, load, rate, stream=None) -> None:
@@ -371,7 +382,8 @@ class DeviceLinear:
         _workspace(workspace, dev)
         if output is None:
             output = _empty(shape, dtype, dev, stream)
-        _lib.kt_linear_fwd(self.linear, tokens, x, residual, output, kind, preact, workspace, stream)
+        _lib.kt_linear_fwd(self.linear, tokens, x, residual, output, kind, preact, workspace,
+                           _handle(stream, dev))
         return output
 
     def backward(self, x, grad_output, workspace, grads, preact=None, grad_input=None, grad_residual=None,
@@ -408,5 +420,6 @@ class DeviceLinear:
         if grad_input is None and need_input:
             grad_input = _empty(tuple(x.shape), torch.bfloat16, dev, stream)
         _lib.kt_linear_bwd(self.linear, tokens, rows, ckpt, preact, grad_output, _TYPES[grad_output.dtype],
-                           grad_residual, grad_input, d_weight, d_bias, accumulate, grad_scale, workspace, stream)
+                           grad_residual, grad_input, d_weight, d_bias, accumulate, grad_scale, workspace,
+                           _handle(stream, dev))
         return grad_input
