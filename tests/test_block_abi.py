@@ -5,6 +5,8 @@ every entry point and class refuses wrong arguments before any GPU work."""
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -309,3 +311,18 @@ def test_linear_class_refuses():
                            ((x, y, None, g), dict(grad_residual=x[:1]), "grad_residual"), ((x, y, None, g), {}, "GPU")):
         with pytest.raises(ValueError, match=word):
             lin.backward(*args, **kw)
+
+
+# ---------------------------------------------------------------- plain C
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs gcc")
+def test_plain_c_consumer(tmp_path):
+    lib_dir = os.path.dirname(_lib.LIBRARY_PATH)
+    exe = tmp_path / "block_consumer"
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"),
+                    os.path.join(ROOT, "tests", "c", "block_consumer.c"), "-o", str(exe), "-L", lib_dir,
+                    "-l:libkt_rawint4.so", f"-Wl,-rpath,{lib_dir}", "-lm"], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert run.returncode == 0, run.stdout + run.stderr
+    assert "FAIL" not in run.stdout and run.stdout.count("ok   ") == 17
