@@ -213,7 +213,8 @@ typedef struct kt_ckpt8 {
  * computed.  d_bias needs no bias in the layer.
  * d_weight and d_bias come from dz to fp32's precision (a dz that bf16 does
  * not hold takes part as the sum of three bf16 numbers, so an infinite input
- * may give a NaN where dz times it is infinite), grad_input from dz in bf16.
+ * may give a NaN where dz times it is infinite), grad_input from dz to 16 bits
+ * (two of them), far below its own rounding to bf16.
  * tokens == 0: only the window rule runs.  The workspace is larger for calls
  * with a checkpoint (from_checkpoint nonzero); such a one serves both.
  */

@@ -66,13 +66,15 @@ __device__ __forceinline__ float act_slope(int act, float z) {
 enum LinearKind { kLinFwd, kLinDx, kLinDw };
 
 constexpr int kMaxPlanes = 3;
+constexpr int kDxPlanes = 2;  // of them for grad_input (see split_planes)
 
 struct LinearGemm {
   const uint16_t *a, *b;
   int64_t lda, ldb;      // row pitch (elements, a multiple of 8)
   int64_t a_width;       // columns of A's rows that exist (a multiple of 8), for a contraction across them
   int64_t M, N, K;
-  int64_t a_plane;       // elements from one of A's planes to the next, where A is the sum of kMaxPlanes bf16 planes
+  int64_t a_plane;       // elements from one of A's planes to the next, where A is the sum of bf16 planes
+  int planes;            // grad_input: how many (1 or kDxPlanes; d_weight's are a constant of the kernel)
   int splits;            // the steps of the contraction are dealt to so many blocks; over 1: part
   float* part;           // [splits][M][pn] partial sums
   int64_t pn;            // N rounded up to a multiple of 8
@@ -302,7 +304,8 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the steps of this split
-  const int total = (int)((g.K + BK - 1) / BK);
+  const int dx_planes = KIND == kLinDx ? g.planes : 1;
+  const int total = (int)((g.K + BK - 1) / BK) * dx_planes;
   const int s0 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * blockIdx.y / g.splits));
   const int s1 = __builtin_amdgcn_readfirstlane((int)((int64_t)total * (blockIdx.y + 1) / g.splits));
 
@@ -333,15 +336,18 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
   // few memory channels (16384 x 7168 x 384: 110 us so, 115 without; 32768 rows: 192
   // against 201; K of 2048: no change).  The other products walk whole rows.
   int ks = s0 + (KIND == kLinFwd ? (s1 - s0) * xcd / 8 : 0);
+  // grad_input's planes take turns at each piece of the contraction, so that B's tile comes from L2 the second time.
   auto copy = [&](int buf) {
-    const uint8_t* pb = base_b + ks * step_b;
+    const bool two = KIND == kLinDx && dx_planes == kDxPlanes;
+    const int kc = two ? ks >> 1 : ks, second = two ? ks & 1 : 0;
+    const uint8_t* pb = base_b + kc * step_b;
     const uint32_t la = lds_addr(&lds[buf][0]) + wave * kCa * 1024;
     const uint32_t lb = lds_addr(&lds[buf][kOffB]) + wave * kCb * 1024;
-    const bool whole = (int64_t)(ks + 1) * BK <= g.K;
-    const int left = (int)(g.K - (int64_t)ks * BK);  // values that exist
+    const bool whole = (int64_t)(kc + 1) * BK <= g.K;
+    const int left = (int)(g.K - (int64_t)kc * BK);  // values that exist
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
-      const uint8_t* pa = base_a + 2 * p * g.a_plane + ks * step_a;
+      const uint8_t* pa = base_a + 2 * (p + second) * g.a_plane + kc * step_a;
       if (whole) {
 #pragma unroll
         for (int c = 0; c < kCa; ++c) dma16_off(pa, off_a[c], la + p * TA::kBytes + c * 1024);
@@ -660,8 +666,10 @@ __global__ __launch_bounds__(1024) void k_linear_few(LinearGemm g, int cols) {
 
 // ---------------------------------------------------------------- dz and its column sums
 
-// dz = grad_output * act'(preact) as bf16 planes that sum to it: one for
-// grad_input, three (24 bits: dz itself, but for the smallest parts) for d_weight.
+// dz = grad_output * act'(preact) as bf16 planes that sum to it: three (24 bits:
+// dz itself, but for the smallest parts) for d_weight, the first two (16 bits,
+// 2^-17 of dz: far below the rounding of the bf16 result) for grad_input, whose
+// rounding to bf16 would else not be its only one.
 struct DzArgs {
   const void* dy;
   int dy_f32;
@@ -830,6 +838,7 @@ struct LinearShape {
   int splits;
 };
 
+// planes: of A
 static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K, int planes) {
   LinearShape s{};
   s.splits = 1;
@@ -837,7 +846,8 @@ static LinearShape linear_shape(LinearKind kind, int64_t M, int64_t N, int64_t K
     s.few = M <= 16 ? 1 : M <= 32 ? 2 : 4;
     return s;
   }
-  const int64_t steps = (K + linear_step(planes) - 1) / linear_step(planes);
+  const int step = linear_step(kind == kLinDw ? planes : 1);
+  const int64_t steps = (K + step - 1) / step * (kind == kLinDx ? planes : 1);
   const int64_t big = (M + 255) / 256 * ((N + 255) / 256);
   s.big = big >= 192;
   s.tiles = s.big ? big : (M + 127) / 128 * ((N + 127) / 128);
@@ -868,8 +878,9 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   const int64_t N = L->out_features, K = L->in_features;
   p.pitch = round_up(N, 8);
   p.nb = (T + kDzRows - 1) / kDzRows;
-  p.dx = linear_shape(kLinDx, T, K, N, 1);
-  p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);  // (with one plane no more splits)
+  // (with one plane no more splits)
+  p.dx = linear_shape(kLinDx, T, K, N, kDxPlanes);
+  p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);
   p.planes = 0;
   p.db = p.planes + round256(2 * kMaxPlanes * (size_t)T * (size_t)p.pitch);
   p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
@@ -1014,7 +1025,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   const bool direct = (exact && N % 8 == 0) || !products;
   const uint16_t* dz = static_cast<const uint16_t*>(grad_output);
   const int64_t pitch = direct ? N : p.pitch;
-  const int planes = exact || !d_weight ? 1 : kMaxPlanes;
+  const int planes = exact ? 1 : d_weight ? kMaxPlanes : kDxPlanes;
   if (!direct || d_bias) {
     DzArgs a{};
     a.dy = grad_output;
@@ -1049,9 +1060,11 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.M = T;
     g.N = K;
     g.K = N;
+    g.a_plane = T * p.pitch;
+    g.planes = exact ? 1 : kDxPlanes;
     g.residual = grad_residual;
     g.out = grad_input;
-    launch_linear<kLinDx>(g, p.dx, ws_ptr<float>(workspace, p.part), st);
+    launch_linear<kLinDx>(g, linear_shape(kLinDx, T, K, N, g.planes), ws_ptr<float>(workspace, p.part), st);
   }
   if (d_weight) {
     const uint16_t* x = inputs;

@@ -1,0 +1,102 @@
+"""Gradients of dense products from a dz that bf16 does not hold (an fp32
+grad_output, or one times an activation's slope), which enters the products as
+bf16 numbers that sum to it, against 64-bit products.  Each case prints its name first.
+
+dz = p0 + p1 + p2, each the nearest bf16 number to what the ones before leave:
+24 bits (for |dz| above 2^-100), so d_weight takes no error from the planes.
+grad_input takes p0 + p1: what p0 leaves is at most 2^-8 of dz's binade, and half a
+step of that at most 2^-16 |dz|.
+"""
+
+import math
+
+import pytest
+
+from tests import block_reference as R
+
+torch = pytest.importorskip("torch")
+
+gpu = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+REST = 2.0**-16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from int4_quantized_moe_amd import device
+
+    return device
+
+
+def _say(*a):
+    print("[planes]", *a, flush=True)
+
+
+def _rand(seed, *shape, std=1.0, dtype=BF16, where="cuda"):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype).to(where)
+
+
+def _dz(dy, z, act):
+    """dz in 64 bits and the error of an fp32 evaluation of it (block_reference's)."""
+    d = dy.double().cpu()
+    if act == "none":
+        return d, torch.zeros_like(d)
+    return d * R.act_grad(z.double().cpu(), act), 32 * R.U * d.abs() * 1.2
+
+
+FORMS = [("none", F32), ("silu", BF16), ("gelu", F32)]
+
+
+# ---------------------------------------------------------------- grad_input
+
+
+@gpu
+@pytest.mark.parametrize("t,k,n", [(5, 8, 8), (33, 64, 40), (200, 264, 136), (64, 512, 72), (3471, 3656, 75)])
+@pytest.mark.parametrize("act,dtype", FORMS)
+def test_grad_input_takes_more_than_bf16_of_dz(dev, t, k, n, act, dtype):
+    """Each column of W holds a single 1, and the residual takes dz's bf16 value away: what is left is what
+    bf16 does not hold of dz."""
+    _say("what is left", t, k, n, act, dtype)
+    w = torch.zeros(n, k, dtype=BF16)
+    w[torch.arange(k) % n, torch.arange(k)] = 1
+    dy = _rand(1, t, n, dtype=dtype)
+    z = _rand(2, t, n) if act != "none" else None
+    dz, err = _dz(dy, z, act)
+    picked, err = dz[:, torch.arange(k) % n], err[:, torch.arange(k) % n]
+    res = (-picked).float().to(BF16)
+    lin = dev.DeviceLinear(w.cuda(), None, act)
+    dx = lin.backward(_rand(3, t, k), dy, lin.backward_workspace(t), {}, preact=z, grad_residual=res.cuda())
+    want = picked + res.double()
+    # two terms and the residual are added in fp32
+    R.within("dx", dx, want, err + (REST + 3 * R.U) * picked.abs() + R.UB * want.abs())
+
+
+@gpu
+@pytest.mark.parametrize("t,k,n", [(1, 8, 1), (15, 136, 33), (31, 1024, 384), (65, 264, 130), (127, 96, 250),
+                                   (300, 512, 384), (513, 1000, 257), (1025, 128, 520), (3471, 3656, 75),
+                                   (75, 3656, 3471), (130, 3656, 3472)])
+@pytest.mark.parametrize("act,dtype", FORMS)
+def test_gradients_of_shapes(dev, t, k, n, act, dtype):
+    """Both gradients with the planes' own errors, at every tile and split; alone they are the same bits."""
+    _say("shapes", t, k, n, act, dtype)
+    x, w, dy = _rand(1, t, k), _rand(2, n, k, std=n**-0.5), _rand(3, t, n, dtype=dtype)
+    z = _rand(4, t, n) if act != "none" else None
+    lin = dev.DeviceLinear(w, None, act)
+    ws = lin.backward_workspace(t)
+    ws.fill_(0xFF)
+    grads = lin.grad_buffers(fill=0.5)
+    dx = lin.backward(x, dy, ws, grads, preact=z)
+    ws.fill_(0xFF)
+    assert torch.equal(lin.backward(x, dy, ws, {}, preact=z), dx)
+    alone = lin.grad_buffers(fill=0.5)
+    ws.fill_(0xFF)
+    lin.backward(x, dy, ws, alone, preact=z, need_input=False)
+    assert torch.equal(alone["weight"], grads["weight"])
+    dz, err = _dz(dy, z, act)
+    xd, wd = x.double().cpu(), w.double().cpu()
+    want, mag = dz @ wd, dz.abs() @ wd.abs()
+    R.within("dx", dx, want, err @ wd.abs() + (REST + 8 * math.sqrt(2 * n) * R.U) * mag + R.UB * want.abs())
+    want, mag = dz.t() @ xd, dz.abs().t() @ xd.abs()
+    R.within("dw", grads["weight"], want, err.t() @ xd.abs() + (8 * math.sqrt(3 * t) + 1) * R.U * mag)
