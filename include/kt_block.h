@@ -211,10 +211,11 @@ typedef struct kt_ckpt8 {
  * grad_input itself, such as the experts' grad_input when this is the router's
  * product.  grad_input, d_weight and d_bias may each be NULL: not
  * computed.  d_bias needs no bias in the layer.
- * d_weight and d_bias come from dz to fp32's precision (a dz that bf16 does
- * not hold takes part as the sum of three bf16 numbers, so an infinite input
- * may give a NaN where dz times it is infinite), grad_input from dz to 16 bits
- * (two of them), far below its own rounding to bf16.
+ * d_weight and d_bias come from dz to fp32's precision, grad_input from dz to
+ * 2^-16 of it, far below its own rounding to bf16: a dz that bf16 may not hold
+ * (of an fp32 gradient, or behind an activation) takes part as a sum of bf16 numbers of
+ * its sign.  Its product with an infinite input or weight is infinite for
+ * |dz| above 2^-100 and may be NaN below.
  * tokens == 0: only the window rule runs.  The workspace is larger for calls
  * with a checkpoint (from_checkpoint nonzero); such a one serves both.
  */

@@ -66,7 +66,7 @@ __device__ __forceinline__ float act_slope(int act, float z) {
 enum LinearKind { kLinFwd, kLinDx, kLinDw };
 
 constexpr int kMaxPlanes = 3;
-constexpr int kDxPlanes = 2;  // of them for grad_input (see split_planes)
+constexpr int kDxPlanes = 2;  // for grad_input
 
 struct LinearGemm {
   const uint16_t *a, *b;
@@ -666,19 +666,25 @@ __global__ __launch_bounds__(1024) void k_linear_few(LinearGemm g, int cols) {
 
 // ---------------------------------------------------------------- dz and its column sums
 
-// dz = grad_output * act'(preact) as bf16 planes that sum to it: three (24 bits:
-// dz itself, but for the smallest parts) for d_weight, the first two (16 bits,
-// 2^-17 of dz: far below the rounding of the bf16 result) for grad_input, whose
-// rounding to bf16 would else not be its only one.
+// dz = grad_output * act'(preact) as bf16 planes that sum to it: p0 + p1 + p2 (24
+// bits: dz itself, for |dz| above 2^-100) for d_weight, p0 + rest (2^-16 of dz: far
+// below the rounding of the bf16 result) for grad_input, whose rounding to bf16
+// would else not be its only one.
+//
+// The parts of a nonzero dz all have its sign and none is 0, so that they
+// times an infinity give what dz times it is: with parts of both signs, or
+// zeros, its product would be NaN.  So p0 and p1 are cut off, not rounded, and go
+// a step towards 0 where they would leave nothing; the next part is then that step.
 struct DzArgs {
   const void* dy;
   int dy_f32;
   const uint16_t* z;
   int act;
   int64_t T, N, pitch;  // planes are [T][pitch], zeros from N on
-  uint16_t* plane;
+  uint16_t* plane;      // p0
   int64_t plane_size;   // elements from one plane to the next
-  int planes;
+  int planes;           // p0 alone (1), or with p1 and p2 (kMaxPlanes)
+  int rest;             // which plane is p0's rest (0: none)
   float* part;          // [row blocks][N] column sums
 };
 
@@ -688,18 +694,27 @@ __device__ __forceinline__ float dz_of(int act, float dy, float z) {
   return dy * act_slope(act, z);
 }
 
-// The planes of v: each the nearest bf16 number to what the ones before leave.
-// An infinite v is one infinite plane; a finite v above bf16's largest number
-// starts with that number, so that the sum stays finite.
-__device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes]) {
-  float rest = v;
-#pragma unroll
-  for (int q = 0; q < kMaxPlanes; ++q) {
-    uint16_t h = float_to_bf16(rest);
-    if ((h & 0x7fff) == 0x7f80 && fabsf(rest) < INFINITY) h -= 1;
-    p[q] = h;
-    rest = (h & 0x7f80) == 0x7f80 ? 0.f : rest - bf16_to_float(h);
-  }
+// v's leading 8 bits, less a step where that is all of v.
+__device__ __forceinline__ uint16_t cut_part(float v) {
+  const uint32_t b = __float_as_uint(v);
+  uint32_t h = b >> 16;
+  if ((b & 0x7fffffffu) > 0x7f800000u) return (uint16_t)(h | 0x40u);  // NaN
+  if ((b & 0xffffu) == 0 && (h & 0x7fffu) != 0 && (h & 0x7fffu) != 0x7f80u) h -= 1;
+  return (uint16_t)h;
+}
+
+// What v's part h leaves; an infinity or a NaN stays whole.
+__device__ __forceinline__ float left_by(float v, uint16_t h) {
+  return (h & 0x7f80) == 0x7f80 ? v : v - bf16_to_float(h);
+}
+
+// p0, p1, p2 and the rest of p0 rounded to bf16.
+__device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes + 1]) {
+  p[0] = cut_part(v);
+  const float r0 = left_by(v, p[0]);
+  p[1] = cut_part(r0);
+  p[2] = float_to_bf16(left_by(r0, p[1]));
+  p[3] = float_to_bf16(r0);
 }
 
 constexpr int kDzRows = 32, kDzCols = 256;
@@ -753,15 +768,25 @@ __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum[k] += v[k];
       if (a.plane) {
-        uint16_t p[8][kMaxPlanes];
+        uint16_t p[8][kMaxPlanes + 1];
+        const bool whole = a.planes == 1 && !a.rest;  // bf16 holds every v: p0 is v
 #pragma unroll
-        for (int k = 0; k < 8; ++k) split_planes(v[k], p[k]);
-#pragma unroll
-        for (int w = 0; w < kMaxPlanes; ++w)
-          if (w < a.planes)
-            *reinterpret_cast<u32x4*>(a.plane + w * a.plane_size + t * a.pitch + n) =
-                u32x4{pack2(p[0][w], p[1][w]), pack2(p[2][w], p[3][w]), pack2(p[4][w], p[5][w]),
-                      pack2(p[6][w], p[7][w])};
+        for (int k = 0; k < 8; ++k) {
+          if (whole)
+            p[k][0] = float_to_bf16(v[k]);
+          else
+            split_planes(v[k], p[k]);
+        }
+        auto put = [&](int w, int to) {
+          *reinterpret_cast<u32x4*>(a.plane + to * a.plane_size + t * a.pitch + n) =
+              u32x4{pack2(p[0][w], p[1][w]), pack2(p[2][w], p[3][w]), pack2(p[4][w], p[5][w]), pack2(p[6][w], p[7][w])};
+        };
+        put(0, 0);
+        if (a.planes > 1) {
+          put(1, 1);
+          put(2, 2);
+        }
+        if (a.rest) put(3, a.rest);
       }
     }
   }
@@ -882,7 +907,7 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   p.dx = linear_shape(kLinDx, T, K, N, kDxPlanes);
   p.dw = linear_shape(kLinDw, N, K, T, kMaxPlanes);
   p.planes = 0;
-  p.db = p.planes + round256(2 * kMaxPlanes * (size_t)T * (size_t)p.pitch);
+  p.db = p.planes + round256(2 * (kMaxPlanes + 1) * (size_t)T * (size_t)p.pitch);
   p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
   const size_t a = part_bytes(p.dx, T, K), b = part_bytes(p.dw, N, K);
   p.x = p.part + (a > b ? a : b);
@@ -1025,7 +1050,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
   const bool direct = (exact && N % 8 == 0) || !products;
   const uint16_t* dz = static_cast<const uint16_t*>(grad_output);
   const int64_t pitch = direct ? N : p.pitch;
-  const int planes = exact ? 1 : d_weight ? kMaxPlanes : kDxPlanes;
+  const int planes = exact || !d_weight ? 1 : kMaxPlanes, rest = exact || !grad_input ? 0 : planes;
   if (!direct || d_bias) {
     DzArgs a{};
     a.dy = grad_output;
@@ -1038,6 +1063,7 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     a.plane = direct ? nullptr : ws_ptr<uint16_t>(workspace, p.planes);
     a.plane_size = T * p.pitch;
     a.planes = planes;
+    a.rest = rest;
     a.part = d_bias ? ws_ptr<float>(workspace, p.db) : nullptr;
     const dim3 grid((unsigned)((p.pitch + kDzCols - 1) / kDzCols), (unsigned)p.nb);
     if (N % 8 == 0)
@@ -1060,8 +1086,8 @@ int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
     g.M = T;
     g.N = K;
     g.K = N;
-    g.a_plane = T * p.pitch;
-    g.planes = exact ? 1 : kDxPlanes;
+    g.a_plane = rest * T * p.pitch;
+    g.planes = rest ? kDxPlanes : 1;
     g.residual = grad_residual;
     g.out = grad_input;
     launch_linear<kLinDx>(g, linear_shape(kLinDx, T, K, N, g.planes), ws_ptr<float>(workspace, p.part), st);

@@ -2,10 +2,11 @@
 grad_output, or one times an activation's slope), which enters the products as
 bf16 numbers that sum to it, against 64-bit products.  Each case prints its name first.
 
-dz = p0 + p1 + p2, each the nearest bf16 number to what the ones before leave:
-24 bits (for |dz| above 2^-100), so d_weight takes no error from the planes.
-grad_input takes p0 + p1: what p0 leaves is at most 2^-8 of dz's binade, and half a
-step of that at most 2^-16 |dz|.
+dz = p0 + p1 + p2: p0 and p1 are cut off after their 8 significant bits, so p2
+holds the rest of the 24 exactly (for |dz| above 2^-100): d_weight takes no
+error from the planes.  grad_input takes p0 and the rest rounded to bf16: the
+rest is at most a step of p0, 2^-7 |dz|, and below that step in the binades
+under it, so half a step of the rest is at most 2^-16 |dz|.
 """
 
 import math
@@ -100,3 +101,44 @@ def test_gradients_of_shapes(dev, t, k, n, act, dtype):
     R.within("dx", dx, want, err @ wd.abs() + (REST + 8 * math.sqrt(2 * n) * R.U) * mag + R.UB * want.abs())
     want, mag = dz.t() @ xd, dz.abs().t() @ xd.abs()
     R.within("dw", grads["weight"], want, err.t() @ xd.abs() + (8 * math.sqrt(3 * t) + 1) * R.U * mag)
+
+
+# ---------------------------------------------------------------- infinities
+
+
+@gpu
+@pytest.mark.parametrize("t,k,n", [(9, 64, 40), (200, 264, 130), (130, 3656, 3472)])
+@pytest.mark.parametrize("act,dtype", FORMS + [("none", BF16)])
+def test_infinite_operands(dev, t, k, n, act, dtype):
+    """A nonzero dz times an infinite input or weight is infinite, whether bf16 holds the dz or not; zeros, NaNs
+    and infinities of both signs give what the products in 64 bits give."""
+    _say("infinite operands", t, k, n, act, dtype)
+    inf = float("inf")
+    x, w, dy = _rand(1, t, k), _rand(2, n, k), _rand(3, t, n, dtype=dtype)
+    x[3, 5], x[4, 7], x[5, 7] = inf, -inf, inf
+    w[11, 9], w[12, 20] = inf, -inf
+    dy[:, 1] = 1.0  # held by bf16
+    dy[:, 2] = -2.5
+    dy[:, 3] = 2.0**-99
+    dy[3, 4] = 0.0
+    dy[5, 6] = -inf
+    if dtype is F32:
+        dy[:, 14] = 1 + 2.0**-8  # held by two planes
+        dy[:, 15] = 1e30
+    z = _rand(4, t, n) if act != "none" else None
+    lin = dev.DeviceLinear(w, None, act)
+    grads = lin.grad_buffers()
+    dx = lin.backward(x, dy, lin.backward_workspace(t), grads, preact=z)
+    dz, _ = _dz(dy, z, act)
+    xd, wd = x.double().cpu(), w.double().cpu()
+
+    def check(tag, actual, want):
+        """The same NaNs, the same infinities, and no others."""
+        a = actual.double().cpu()
+        assert torch.equal(torch.isnan(a), torch.isnan(want)), f"{tag}: NaNs at other places"
+        at = torch.isinf(want)
+        assert torch.equal(a[at], want[at]), f"{tag}: infinities"
+        assert torch.isfinite(a[torch.isfinite(want)]).all(), f"{tag}: infinities at other places"
+
+    check("dw", grads["weight"], dz.t() @ xd)
+    check("dx", dx, dz @ wd)
