@@ -180,7 +180,8 @@ typedef struct kt_linear {
  * inputs [tokens, K] bf16; residual [tokens, N] bf16 or NULL (it may be the
  * output itself where that is bf16); output [tokens, N] of output_type; preact
  * [tokens, N] bf16 or NULL receives z, which the backward of an activation
- * reads.  Sums are fp32, each output is rounded once.  All tensors 16-byte
+ * reads.  Sums are fp32, each output is rounded once.  Within a call, equal rows
+ * of inputs (and residual) give equal rows of outputs, wherever they stand.  All tensors 16-byte
  * aligned.  The router's logits are a call of this with a weight of [E, H]
  * and KT_TYPE_F32.  tokens == 0 is a valid no-op.  The workspace size may be
  * 0; the workspace may then be NULL.

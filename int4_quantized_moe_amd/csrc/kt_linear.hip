@@ -330,12 +330,12 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
   const uint8_t* base_b = reinterpret_cast<const uint8_t*>(g.b + (kAcrossB ? n0 : n0 * g.ldb));
   const int64_t step_a = kAcrossA ? 2 * BK * g.lda : 2 * BK, step_b = kAcrossB ? 2 * BK * g.ldb : 2 * BK;
 
-  // The next copy's step.  In the forward, each XCD starts its walk of the
-  // contraction at another eighth and comes round: with all of them at the same
-  // columns of rows a power of two (times an odd number) apart, their reads gather on
-  // few memory channels (16384 x 7168 x 384: 110 us so, 115 without; 32768 rows: 192
-  // against 201; K of 2048: no change).  The other products walk whole rows.
-  int ks = s0 + (KIND == kLinFwd ? (s1 - s0) * xcd / 8 : 0);
+  // The next copy's step.  Every tile walks the contraction in the same order, so
+  // that equal rows of A give equal outputs wherever they stand: a token's logits,
+  // and the choice made on them, do not depend on its place in the batch.  (Each XCD
+  // starting at another eighth spreads the reads over the memory channels: 16384 x
+  // 7168 x 384 in 113 us instead of 116, but with sums in another order per XCD.)
+  int ks = s0;
   // grad_input's planes take turns at each piece of the contraction, so that B's tile comes from L2 the second time.
   auto copy = [&](int buf) {
     const bool two = KIND == kLinDx && dx_planes == kDxPlanes;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
         dma16((kAcrossB ? row : col) < left ? (const void*)(pb + off_b[c]) : kZero16, lb + c * 1024);
       }
     }
-    if (++ks == s1) ks = s0;
+    ++ks;
   };
 
   const int wm = wave / WN * (BM / WM), wn = wave % WN * (BN / WN);
