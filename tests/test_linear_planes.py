@@ -1,6 +1,7 @@
 """Gradients of dense products from a dz that bf16 does not hold (an fp32
 grad_output, or one times an activation's slope), which enters the products as
-bf16 numbers that sum to it, against 64-bit products.  Each case prints its name first.
+bf16 numbers that sum to it.  GPU tests against 64-bit products, and CPU tests
+that the bounds tell fewer planes from enough.  Each case prints its name first.
 
 dz = p0 + p1 + p2: p0 and p1 are cut off after their 8 significant bits, so p2
 holds the rest of the 24 exactly (for |dz| above 2^-100): d_weight takes no
@@ -101,6 +102,49 @@ def test_gradients_of_shapes(dev, t, k, n, act, dtype):
     R.within("dx", dx, want, err @ wd.abs() + (REST + 8 * math.sqrt(2 * n) * R.U) * mag + R.UB * want.abs())
     want, mag = dz.t() @ xd, dz.abs().t() @ xd.abs()
     R.within("dw", grads["weight"], want, err.t() @ xd.abs() + (8 * math.sqrt(3 * t) + 1) * R.U * mag)
+
+
+# ---------------------------------------------------------------- d_weight
+
+
+def _few_planes(dy, planes, nearest):
+    """dy from its first bf16 planes, on the CPU."""
+    rest, total = dy.clone(), torch.zeros_like(dy, dtype=torch.float64)
+    for _ in range(planes):
+        h = rest.to(BF16).float() if nearest else (rest.view(torch.int32) & ~0xFFFF).view(F32)
+        total += h.double()
+        rest = rest - h
+    return total
+
+
+def _one_token(t, n, k):
+    """A gradient with all 24 bits in use and inputs that are powers of two: one product (or, with two tokens
+    of the same sign, two) whose planes' products are exact, so three roundings of sums are all there is."""
+    dy = _rand(5, t, n, dtype=F32, where="cpu").abs() + 0.25
+    dy = (dy.view(torch.int32) | 1).view(F32)
+    x = torch.exp2(torch.randint(-6, 7, (t, k), generator=torch.Generator().manual_seed(6)).float()).to(BF16)
+    want = dy.double().t() @ x.double()
+    return dy, x, want, 4 * t * R.U * want
+
+
+@pytest.mark.parametrize("t", [1, 2])
+@pytest.mark.parametrize("nearest", [False, True])
+def test_two_planes_are_told_from_three(t, nearest):
+    dy, x, want, bound = _one_token(t, 40, 64)
+    off = (_few_planes(dy, 2, nearest).t() @ x.double() - want).abs()
+    assert (off > bound).float().mean() > 0.2
+    assert ((_few_planes(dy, 3, nearest).t() @ x.double() - want).abs() <= bound).all()
+
+
+@gpu
+@pytest.mark.parametrize("t,k,n", [(1, 64, 40), (2, 64, 40), (1, 3656, 3471), (2, 264, 130)])
+def test_weight_gradient_holds_all_of_dz(dev, t, k, n):
+    _say("24 bits", t, k, n)
+    dy, x, want, bound = _one_token(t, n, k)
+    lin = dev.DeviceLinear(_rand(1, n, k))
+    grads = lin.grad_buffers()
+    lin.backward(x.cuda(), dy.cuda(), lin.backward_workspace(t), grads, need_input=False)
+    R.within("dw", grads["weight"], want, bound)
 
 
 # ---------------------------------------------------------------- infinities
