@@ -561,17 +561,32 @@ __device__ __forceinline__ void store_grad(void* p, int64_t i, float v) {
     static_cast<float*>(p)[i] = v;
 }
 
-// With p = s / S the gradient of the chosen scores is ds = scale (g - d) / S,
-// and the softmax's sum ds s is scale d (1 - sum s / S) / S = scale d 1e-20 / S^2:
-// written so, the tiny term keeps its value instead of a difference of roundings.
+// Of the chosen scores the gradient is scale (g - d) / S (scale g without
+// renormalisation), and the softmax's sum ds s is scale d (1 - sum s / S) / S =
+// scale d 1e-20 / S^2: written so, the tiny term keeps its value instead of a
+// difference of roundings.  Scores are multiplied with 1 / S (up to 1e20) first
+// and with the scale last, so that nothing overflows on the way to a result that does not.
 struct RowGrad {
-  float m, zinv;       // softmax: maximum and 1 / sum of exponentials
-  float inv, d, dot;   // 1 / S (1 without renormalisation), d, sum ds s
+  float m, zinv;     // softmax: maximum and 1 / sum of exponentials
+  float inv, d;      // 1 / S (1 without renormalisation), d (0 without)
+  float c;           // sum ds s / scale: 1e-20 / S d (renormalised), sum g s
 };
 
-// ds of a chosen expert with score gradient g
-__device__ __forceinline__ float chosen_ds(const RouterBwdArgs& a, const RowGrad& r, float g) {
-  return a.renorm ? a.scale * (g - r.d) * r.inv : a.scale * g;
+// d, c and 1 / S from the sums of the chosen s and of their g s
+__device__ __forceinline__ void finish_row(const RouterBwdArgs& a, RowGrad& r, float ssum, float gsum) {
+  r.c = gsum;
+  if (a.renorm) {
+    r.inv = 1.f / (ssum + 1e-20f);
+    r.d = gsum * r.inv;
+    r.c = 1e-20f * r.inv * r.d;
+  }
+}
+
+// dl of an expert with score s whose slots' g - d add up to gd
+template <int SCORE>
+__device__ __forceinline__ float chosen_grad(const RouterBwdArgs& a, const RowGrad& r, float s, float gd) {
+  if (SCORE == KT_SCORE_SIGMOID) return s * r.inv * (1.f - s) * gd * a.scale;
+  return (a.renorm ? s * r.inv * gd - s * r.c : s * (gd - r.c)) * a.scale;
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -581,7 +596,7 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // Up to 512 experts and 16 slots: 16 tokens a block, 16 lanes each.  A token's
-// logits are staged in LDS and turned into -s (sum ds s) in place, the chosen
+// logits are staged in LDS and turned into -s sum ds s in place, the chosen
 // experts' values are put over those, and the row is written back whole.  16384
 // tokens of 384 experts in bf16 by softmax take 11 us (25 MB; a plain copy of them:
 // 5), 4096 in fp32 6.6 us, of which launch and latency are most.
@@ -633,31 +648,24 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t toke
   const float lc = id >= 0 ? row[id] : -INFINITY;
   const float sc = id < 0 ? 0.f : SCORE == KT_SCORE_SOFTMAX ? expf(lc - r.m) * r.zinv : sigmoid32(lc);
   const float ssum = row16_sum(sc), gsum = row16_sum(g * sc);
-  if (a.renorm) {
-    const float S = ssum + 1e-20f;
-    r.inv = 1.f / S;
-    r.d = gsum * r.inv;
-    r.dot = a.scale * r.d * (1e-20f * r.inv);
-  } else {
-    r.dot = a.scale * gsum;
-  }
+  finish_row(a, r, ssum, gsum);
   // an expert in several slots: every one of its lanes has the sum, in slot order
-  float ds = 0.f;
-  const float own = id >= 0 ? chosen_ds(a, r, g) : 0.f;
+  float gd = 0.f;
+  const float own = id >= 0 ? g - r.d : 0.f;
   for (int j = 0; j < k; ++j) {
     const int oi = __shfl(id, j, kLanes);
     const float od = __shfl(own, j, kLanes);
-    if (oi == id) ds += od;
+    if (oi == id) gd += od;
   }
-  const float rest = bad && used ? __uint_as_float(0x7fc00000u) : SCORE == KT_SCORE_SOFTMAX && used ? -r.dot * r.zinv : 0.f;
+  const float rest = bad && used ? __uint_as_float(0x7fc00000u) : SCORE == KT_SCORE_SOFTMAX && used ? -r.c * r.zinv : 0.f;
   wave_fence();
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = q + kLanes * i;
-    if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest;
+    if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest * a.scale;
   }
   wave_fence();
-  if (id >= 0 && !bad) row[id] = SCORE == KT_SCORE_SOFTMAX ? sc * (ds - r.dot) : ds * sc * (1.f - sc);
+  if (id >= 0 && !bad) row[id] = chosen_grad<SCORE>(a, r, sc, gd);
   wave_fence();
   if (t >= tokens) return;
   if (BF16) {
@@ -683,11 +691,11 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t toke
   }
 }
 
-// One block per token; ds of every expert in LDS.  Each thread owns the experts
-// tid, tid + 256, ... and adds their slots in slot order.
+// One block per token; the slots' g - d by expert in LDS.  Each thread owns the
+// experts tid, tid + 256, ... and adds their slots in slot order.
 template <int SCORE, bool BF16>
 __global__ __launch_bounds__(kAnyThreads) void k_route_bwd_any(RouterBwdArgs a) {
-  __shared__ float ds[KT_RAWINT4_MAX_EXPERTS];
+  __shared__ float gd[KT_RAWINT4_MAX_EXPERTS];
   __shared__ float red[4], red2[4], red3[4];
   __shared__ int sid[kAnyThreads];
   __shared__ float sg[kAnyThreads];
@@ -701,7 +709,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_bwd_any(RouterBwdArgs a) 
     const float l = load_logit<BF16>(a.logits, base + e);
     bad |= bad_logit<SCORE>(l);
     mx = fmaxf(mx, l);
-    ds[e] = 0.f;
+    gd[e] = 0.f;
   }
   bad = __syncthreads_or(bad);
   auto block_sum = [&](float v, float* buf) {
@@ -739,14 +747,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_bwd_any(RouterBwdArgs a) 
   gsum = block_sum(gsum, red2);
   used = block_sum(used, red3);
   if (used == 0.f) bad = 0;
-  if (a.renorm) {
-    const float S = ssum + 1e-20f;
-    r.inv = 1.f / S;
-    r.d = gsum * r.inv;
-    r.dot = a.scale * r.d * (1e-20f * r.inv);
-  } else {
-    r.dot = a.scale * gsum;
-  }
+  finish_row(a, r, ssum, gsum);
   for (int j0 = 0; j0 < a.k; j0 += kAnyThreads) {
     __syncthreads();
     const int64_t id = j0 + tid < a.k ? ids[j0 + tid] : -1;
@@ -755,12 +756,11 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_bwd_any(RouterBwdArgs a) 
     __syncthreads();
     const int n = min(kAnyThreads, a.k - j0);
     for (int j = 0; j < n; ++j)
-      if (sid[j] >= 0 && (sid[j] & (kAnyThreads - 1)) == tid) ds[sid[j]] += chosen_ds(a, r, sg[j]);
+      if (sid[j] >= 0 && (sid[j] & (kAnyThreads - 1)) == tid) gd[sid[j]] += sg[j] - r.d;
   }
   for (int e = tid; e < a.E; e += kAnyThreads) {
     const float s = score(load_logit<BF16>(a.logits, base + e));
-    float v = SCORE == KT_SCORE_SOFTMAX ? s * (ds[e] - (used == 0.f ? 0.f : r.dot)) : ds[e] * s * (1.f - s);
-    if (used == 0.f) v = 0.f;
+    float v = used == 0.f ? 0.f : chosen_grad<SCORE>(a, r, s, gd[e]);
     if (bad) v = __uint_as_float(0x7fc00000u);
     store_grad<BF16>(a.out, base + e, v);
   }
