@@ -107,8 +107,13 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Sigmoid and softmax terms in fp32 with the library's exponential (about one rounding).
-__device__ __forceinline__ float sigmoid32(float l) { return 1.f / (1.f + expf(-l)); }
+// The sigmoid in fp32 with the library's exponential (about one rounding), from
+// the exponential of -|l|: it keeps a small score's digits down to fp32's
+// lowest numbers.
+__device__ __forceinline__ float sigmoid32(float l) {
+  const float e = expf(-fabsf(l));
+  return (l < 0.f ? e : 1.f) / (1.f + e);
+}
 
 // exp for arguments up to 0 from the hardware's exp2 (relative error below 2^-23 (2 + 1.5 |x|))
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }

@@ -57,3 +57,32 @@ def test_gradient_of_scores_that_vanish_under_a_large_scale(dev, e, k, score, re
                         scale=scale)
         # |dl| <= scale * |g| * e^-294 / 1e-20 < 1e-60
         assert (out == 0).all()
+
+
+@pytest.mark.parametrize("e,k", [(384, 8), (600, 20)])
+def test_sigmoid_scores_below_the_normal_range(dev, e, k):
+    """Scores of logits between -103 and -60 are fp32 numbers, the lowest in steps of 2^-149, and a large scale
+    brings their weights and gradients back into sight."""
+    _say("below the normal range", e, k)
+    t, scale = 31, 1e22
+    rng = np.random.default_rng(e)
+    l = rng.uniform(-101, -88, (t, e)).astype(np.float32)
+    router = dev.DeviceRouter(e, k, score="sigmoid", scale=scale)
+    ids, w = router.forward(torch.from_numpy(l).cuda())
+    want_ids, want, _ = R.route(l, k, score="sigmoid", scale=scale)
+    assert np.array_equal(ids.cpu().numpy(), want_ids) and want.max() > 1
+    R.within("weights", w, want, 2 * R.route_precision(l)[:, None] * np.abs(want) + scale / 1e-20 * 2 * STEP)
+    l = rng.uniform(-101, -60, (t, e)).astype(np.float32)
+    prec = R.route_precision(l)[:, None]
+    low = np.argsort(l, 1)[:, :k].copy()  # the smallest scores, most of them below 2^-126
+    _, g = _slots(e, t, e, k)
+    out = _gradient(dev, torch.from_numpy(l), low, g, score="sigmoid", scale=scale)
+    want, _ = R.route_bwd(l, low, g, score="sigmoid", scale=scale)
+    s = R.scores(l, "sigmoid")
+    si, g64 = np.take_along_axis(s, low, 1), np.abs(g.astype(np.float64))
+    total = si.sum(1, keepdims=True) + 1e-20
+    mag = np.zeros((t, e))
+    np.put_along_axis(mag, low, scale * (g64 + (g64 * si).sum(1, keepdims=True) / total) / total, 1)
+    bound = mag * (4 * prec * s + 4 * STEP) + 2.0**-126
+    assert (np.abs(want) > 4 * bound).any()  # values that a gradient of 0 would miss
+    R.within("dlogits", out, want, bound)
