@@ -109,7 +109,7 @@ __device__ __forceinline__ void wave_fence() {
 
 // The sigmoid in fp32 with the library's exponential (about one rounding), from
 // the exponential of -|l|: it keeps a small score's digits down to fp32's
-// lowest numbers.
+// lowest numbers, and 1 - s is sigmoid32(-l).
 __device__ __forceinline__ float sigmoid32(float l) {
   const float e = expf(-fabsf(l));
   return (l < 0.f ? e : 1.f) / (1.f + e);
@@ -587,10 +587,11 @@ __device__ __forceinline__ void finish_row(const RouterBwdArgs& a, RowGrad& r, f
   }
 }
 
-// dl of an expert with score s whose slots' g - d add up to gd
+// dl of an expert with logit l and score s whose slots' g - d add up to gd
+// (1 - s from the logit: the difference would lose its digits where s is close to 1)
 template <int SCORE>
-__device__ __forceinline__ float chosen_grad(const RouterBwdArgs& a, const RowGrad& r, float s, float gd) {
-  if (SCORE == KT_SCORE_SIGMOID) return s * r.inv * (1.f - s) * gd * a.scale;
+__device__ __forceinline__ float chosen_grad(const RouterBwdArgs& a, const RowGrad& r, float l, float s, float gd) {
+  if (SCORE == KT_SCORE_SIGMOID) return s * r.inv * sigmoid32(-l) * gd * a.scale;
   return (a.renorm ? s * r.inv * gd - s * r.c : s * (gd - r.c)) * a.scale;
 }
 
@@ -670,7 +671,7 @@ __global__ __launch_bounds__(256) void k_route_bwd(RouterBwdArgs a, int64_t toke
     if (i < v && e < E) row[e] = bad || !used || SCORE == KT_SCORE_SIGMOID ? rest : s[i] * rest * a.scale;
   }
   wave_fence();
-  if (id >= 0 && !bad) row[id] = chosen_grad<SCORE>(a, r, sc, gd);
+  if (id >= 0 && !bad) row[id] = chosen_grad<SCORE>(a, r, lc, sc, gd);
   wave_fence();
   if (t >= tokens) return;
   if (BF16) {
@@ -764,8 +765,8 @@ __global__ __launch_bounds__(kAnyThreads) void k_route_bwd_any(RouterBwdArgs a) 
       if (sid[j] >= 0 && (sid[j] & (kAnyThreads - 1)) == tid) gd[sid[j]] += sg[j] - r.d;
   }
   for (int e = tid; e < a.E; e += kAnyThreads) {
-    const float s = score(load_logit<BF16>(a.logits, base + e));
-    float v = used == 0.f ? 0.f : chosen_grad<SCORE>(a, r, s, gd[e]);
+    const float l = load_logit<BF16>(a.logits, base + e);
+    float v = used == 0.f ? 0.f : chosen_grad<SCORE>(a, r, l, score(l), gd[e]);
     if (bad) v = __uint_as_float(0x7fc00000u);
     store_grad<BF16>(a.out, base + e, v);
   }

@@ -59,6 +59,29 @@ def test_gradient_of_scores_that_vanish_under_a_large_scale(dev, e, k, score, re
         assert (out == 0).all()
 
 
+@pytest.mark.parametrize("e,k", [(384, 8), (40, 6), (700, 8), (384, 20)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_gradient_of_large_logits(dev, e, k, renorm):
+    """s (1 - s) keeps its digits where s is close to 1: each of the factors is within `prec` of its own size."""
+    _say("large logits", e, k, renorm)
+    t = 29
+    rng = np.random.default_rng(e)
+    l = np.where(rng.random((t, e)) < 0.7, rng.uniform(8, 80, (t, e)), rng.uniform(-20, 8, (t, e))).astype(np.float32)
+    ids, g = _slots(e + 1, t, e, k)
+    out = _gradient(dev, torch.from_numpy(l), ids, g, score="sigmoid", renormalize=renorm, scale=1.5)
+    s = R.scores(l, "sigmoid")
+    comp = 1.0 / (1.0 + np.exp(l.astype(np.float64)))  # 1 - s, which as a difference ends at l = 37 in 64 bits too
+    si, g64 = np.take_along_axis(s, ids, 1), g.astype(np.float64)
+    total = si.sum(1, keepdims=True) + 1e-20 if renorm else 1.0
+    d = (g64 * si).sum(1, keepdims=True) / total if renorm else 0.0
+    dmag = (np.abs(g64) * si).sum(1, keepdims=True) / total if renorm else 0.0
+    want, mag = np.zeros((t, e)), np.zeros((t, e))
+    np.put_along_axis(want, ids, 1.5 * (g64 - d) / total, 1)
+    np.put_along_axis(mag, ids, 1.5 * (np.abs(g64) + dmag) / total, 1)
+    want *= s * comp
+    R.within("dlogits", out, want, 4 * R.route_precision(l)[:, None] * mag * s * comp + 2.0**-126)
+
+
 @pytest.mark.parametrize("e,k", [(384, 8), (600, 20)])
 def test_sigmoid_scores_below_the_normal_range(dev, e, k):
     """Scores of logits between -103 and -60 are fp32 numbers, the lowest in steps of 2^-149, and a large scale
