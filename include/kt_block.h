@@ -145,7 +145,8 @@ int kt_ckpt8_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, i
  * the inputs are unpacked into the workspace and the rest is that call, with
  * the same results, bit for bit, as on unpacked inputs.  The gradients are
  * those at the unpacked inputs.  The workspace
- * (kt_moe_bwd_ckpt8_workspace_bytes) holds those rows behind the recompute's.
+ * (kt_moe_bwd_ckpt8_workspace_bytes) holds those rows behind the recompute's; its
+ * size is for that qlen, as the recompute's is (a smaller one may need more).
  */
 size_t kt_moe_bwd_ckpt8_workspace_bytes(const kt_rawint4_moe_layer* layer, int32_t qlen);
 int kt_moe_bwd_ckpt8(const kt_rawint4_moe_layer* layer, int32_t qlen, int32_t format, const uint8_t* codes,
@@ -183,8 +184,9 @@ typedef struct kt_linear {
  * reads.  Sums are fp32, each output is rounded once.  Within a call, equal rows
  * of inputs (and residual) give equal rows of outputs, wherever they stand.  All tensors 16-byte
  * aligned.  The router's logits are a call of this with a weight of [E, H]
- * and KT_TYPE_F32.  tokens == 0 is a valid no-op.  The workspace size may be
- * 0; the workspace may then be NULL.
+ * and KT_TYPE_F32.  tokens == 0 is a valid no-op.  A workspace of the size for
+ * some number of tokens serves every smaller number too.  The size may be 0; the
+ * workspace may then be NULL.
  */
 size_t kt_linear_workspace_bytes(const kt_linear* linear, int32_t tokens);
 int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* inputs, const uint16_t* residual,
@@ -217,8 +219,9 @@ typedef struct kt_ckpt8 {
  * (of an fp32 gradient, or behind an activation) takes part as a sum of bf16 numbers of
  * its sign.  Its product with an infinite input or weight is infinite for
  * |dz| above 2^-100 and may be NaN below.
- * tokens == 0: only the window rule runs.  The workspace is larger for calls
- * with a checkpoint (from_checkpoint nonzero); such a one serves both.
+ * tokens == 0: only the window rule runs.  A workspace of the size for some
+ * number of tokens serves every smaller number too.  It is larger for calls with a
+ * checkpoint (from_checkpoint nonzero); such a one serves both.
  */
 size_t kt_linear_bwd_workspace_bytes(const kt_linear* linear, int32_t tokens, int32_t from_checkpoint);
 int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* inputs, const kt_ckpt8* checkpoint,

@@ -2,6 +2,7 @@
 // their gradients.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kt_common.hpp"
@@ -890,6 +891,17 @@ static size_t part_bytes(const LinearShape& s, int64_t M, int64_t N) {
   return s.splits > 1 ? round256(4 * (size_t)s.splits * (size_t)M * (size_t)round_up(N, 8)) : 0;
 }
 
+// The most that part_bytes is for 1 .. T rows: fewer rows may take more splits.
+// Between multiples of 128 rows, and above and below 64, the splits stay.
+static size_t most_part_bytes(LinearKind kind, int64_t T, int64_t N, int64_t K, int planes) {
+  auto bytes = [&](int64_t M) { return part_bytes(linear_shape(kind, M, N, K, planes), M, N); };
+  size_t most = bytes(T);
+  if (T > 64) most = std::max(most, bytes(64));
+  // over kBlocksWanted / 2 tiles nothing is split
+  for (int64_t M = 128; M < T && M / 128 * ((N + 127) / 128) <= kBlocksWanted / 2; M += 128) most = std::max(most, bytes(M));
+  return most;
+}
+
 // The workspace of a backward.  Every part has room of its own except the
 // splits' partial sums, which the two products use one after the other.
 struct LinearBwdPlan {
@@ -898,7 +910,8 @@ struct LinearBwdPlan {
   int64_t pitch, nb;
 };
 
-static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
+// most: at its largest for 1 .. T tokens
+static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt, bool most = false) {
   LinearBwdPlan p{};
   const int64_t N = L->out_features, K = L->in_features;
   p.pitch = round_up(N, 8);
@@ -909,8 +922,8 @@ static LinearBwdPlan plan_linear_bwd(const kt_linear* L, int64_t T, bool ckpt) {
   p.planes = 0;
   p.db = p.planes + round256(2 * (kMaxPlanes + 1) * (size_t)T * (size_t)p.pitch);
   p.part = p.db + round256(4 * (size_t)p.nb * (size_t)N);
-  const size_t a = part_bytes(p.dx, T, K), b = part_bytes(p.dw, N, K);
-  p.x = p.part + (a > b ? a : b);
+  const size_t a = most ? most_part_bytes(kLinDx, T, K, N, kDxPlanes) : part_bytes(p.dx, T, K);
+  p.x = p.part + std::max(a, part_bytes(p.dw, N, K));  // (d_weight's splits grow with T)
   p.total = p.x + (ckpt ? round256(2 * (size_t)T * (size_t)K) : 0);
   return p;
 }
@@ -957,8 +970,7 @@ extern "C" {
 size_t kt_linear_workspace_bytes(const kt_linear* linear, int32_t tokens) {
   if (check_linear(linear, tokens)) return 0;
   (void)set_error(KT_RAWINT4_OK, "");  // 0 is a valid size: no message stays
-  return part_bytes(linear_shape(kLinFwd, tokens, linear->out_features, linear->in_features, 1), tokens,
-                    linear->out_features);
+  return most_part_bytes(kLinFwd, tokens, linear->out_features, linear->in_features, 1);
 }
 
 int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* inputs, const uint16_t* residual,
@@ -1001,7 +1013,7 @@ int kt_linear_fwd(const kt_linear* linear, int32_t tokens, const uint16_t* input
 size_t kt_linear_bwd_workspace_bytes(const kt_linear* linear, int32_t tokens, int32_t from_checkpoint) {
   if (check_linear(linear, tokens)) return 0;
   (void)set_error(KT_RAWINT4_OK, "");
-  return plan_linear_bwd(linear, tokens, from_checkpoint != 0).total;
+  return plan_linear_bwd(linear, tokens, from_checkpoint != 0, true).total;
 }
 
 int kt_linear_bwd(const kt_linear* linear, int32_t tokens, const uint16_t* inputs, const kt_ckpt8* checkpoint,

@@ -60,7 +60,7 @@ class DeviceLayer:
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def checkpoint_workspace(self, qlen: int) -> torch.Tensor:
-        """Workspace of a backward whose inputs are a Checkpoint8."""
+        """Workspace of a backward whose inputs are a Checkpoint8, for that qlen."""
         n = _lib.kt_moe_bwd_ckpt8_workspace_bytes(self.layer, qlen)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
@@ -344,11 +344,12 @@ class DeviceLinear:
         self.linear = _lib.make_linear(weight, bias, activation)
 
     def workspace(self, tokens: int) -> torch.Tensor:
+        """Of forward() for up to so many tokens."""
         n = _lib.kt_linear_workspace_bytes(self.linear, tokens)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def backward_workspace(self, tokens: int, checkpoint: bool = True) -> torch.Tensor:
-        """checkpoint=False: for inputs given as rows only (smaller)."""
+        """Of backward() for up to so many tokens.  checkpoint=False: for inputs given as rows only (smaller)."""
         n = _lib.kt_linear_bwd_workspace_bytes(self.linear, tokens, checkpoint)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
