@@ -101,6 +101,16 @@ class DeviceLayer:
                     ("grad_route", grad_route, slots, torch.float32)):
                 _checked(name, t, shape, dtype, dev)
             _workspace(workspace, _gpu(inputs.codes))
+            if dev != self.gate_packed.device:
+                raise ValueError(f"the checkpoint must be on {self.gate_packed.device}, not on {dev}")
+            for name, shape in self.cfg.lora_shapes().items():
+                if grads.get(name) is None:
+                    raise ValueError(f"grads has no {name!r}")
+                _checked(f"grads[{name!r}]", grads[name], shape, torch.float32, dev)
+            if _elsewhere(dev):
+                with torch.cuda.device(dev):
+                    return self.backward(inputs, expert_ids, route_weights, grad_output, workspace, grads, accumulate,
+                                         grad_scale, grad_input, grad_route, stream)
             if grad_input is None:
                 grad_input = _empty(rows, torch.bfloat16, dev, stream)
             _lib.kt_moe_bwd_ckpt8(self.layer, qlen, inputs.fmt, inputs.codes, inputs.scales, expert_ids, route_weights,
