@@ -30,7 +30,7 @@ extern "C" {
 #define KT_TYPE_BF16 0
 #define KT_TYPE_F32 1
 
-/* ------------------------------------------------------------------ routing */
+/* ------------------------------------------------------------------ routing (at most 2^23 tokens a call) */
 
 #define KT_SCORE_SOFTMAX 0
 #define KT_SCORE_SIGMOID 1
@@ -77,6 +77,9 @@ typedef struct kt_router {
  *     is NaN or +inf, gets ids 0 .. k-1 and weights NaN.
  *   - load [E] int32, or NULL: load = (accumulate ? load : 0) + how many slots
  *     chose each expert.
+ *   - Weights, like the gradient below, are computed in fp32 whatever the choice
+ *     takes: a score below 2^-149 is 0, and the terms of a softmax's sum are within
+ *     2^-23 (2 + 1.5 |l - max|) of their size.
  * tokens == 0 is valid (load is still cleared where accumulate is 0).
  * logits must be 16-byte aligned, expert_ids 8-byte, the rest by their type.
  */
@@ -155,7 +158,7 @@ int kt_moe_bwd_ckpt8(const kt_rawint4_moe_layer* layer, int32_t qlen, int32_t fo
                      float* d_gate_b, float* d_up_a, float* d_up_b, float* d_down_a, float* d_down_b,
                      int32_t accumulate, float grad_scale, void* workspace, size_t workspace_bytes, void* stream);
 
-/* ---------------------------------------------------------- dense products */
+/* ---------------------------------------------------------- dense products (at most 2^20 tokens a call) */
 
 #define KT_ACT_NONE 0
 #define KT_ACT_RELU 1

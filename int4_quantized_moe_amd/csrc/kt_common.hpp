@@ -249,6 +249,12 @@ __device__ __forceinline__ float row16_sum(float v) {
   return v + dpp_f<0x140>(v);
 }
 
+// orders a wave's LDS writes before its later LDS reads of other lanes' values, and the other way round
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------- activation
 
 // Sigmoid from the hardware exp2 and reciprocal (about 1 ulp each), with the

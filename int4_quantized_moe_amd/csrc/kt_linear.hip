@@ -27,7 +27,7 @@ __device__ __forceinline__ float sigmoid_lin(float u) { return u != u ? u : sigm
 __device__ __forceinline__ float act_value(int act, float z) {
   switch (act) {
     case KT_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays
-    case KT_ACT_SILU: return fmaxf(z, -128.f) * sigmoid_lin(z);  // the sigmoid ends at 2^-127, not at 0
+    case KT_ACT_SILU: return fmaxf(z, -128.f) * sigmoid_lin(z);  // (the sigmoid is 0 there: -infinity gives -0, not NaN)
     // (erfc keeps the digits of a small Phi, where 1 + erf has none left; -infinity gives -0)
     case KT_ACT_GELU: return 0.5f * fmaxf(z, -16.f) * erfcf(-z * kInvSqrt2);
     case KT_ACT_GELU_TANH: return fmaxf(z, -16.f) * sigmoid_lin(z != z ? z : gelu_tanh_arg(z));
@@ -209,12 +209,6 @@ __device__ __forceinline__ void dma16_off(const void* base, uint32_t off, uint32
 }
 #pragma clang diagnostic pop
 
-// orders a wave's LDS writes before its later LDS reads of other lanes' values, and the other way round
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // One operand's tile of R rows (or columns) x BK contraction values in LDS, filled by 16-byte copies straight from memory: a wave's copy
 // fills 1024 consecutive bytes, so the arrangement is made on the source side.
 //
@@ -292,15 +286,15 @@ __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(Line
   __shared__ __align__(1024) uint8_t lds[2][kOffB + TB::kBytes];
 
   // tiles: each XCD (blocks reach them in turn) takes a contiguous run of the
-  // order below, in which kGroup rows of tiles are walked column by column, so
+  // order below, in which kRows rows of tiles are walked column by column, so
   // that the operand rows a run shares stay in that XCD's L2
-  constexpr int kGroup = 4;
+  constexpr int kRows = 4;
   const int mt = (int)((g.M + BM - 1) / BM), nt = (int)((g.N + BN - 1) / BN), tiles = mt * nt;
   const int xcd = blockIdx.x & 7, q8 = tiles >> 3, r8 = tiles & 7;
   const int tile = __builtin_amdgcn_readfirstlane(xcd * q8 + min(xcd, r8) + (int)(blockIdx.x >> 3));
-  const int span = kGroup * nt, grp = tile / span, in = tile - grp * span;
-  const int rows = min(kGroup, mt - grp * kGroup);
-  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(grp * kGroup + in % rows) * BM;
+  const int span = kRows * nt, grp = tile / span, in = tile - grp * span;
+  const int rows = min(kRows, mt - grp * kRows);
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(grp * kRows + in % rows) * BM;
   const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(in / rows) * BN;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

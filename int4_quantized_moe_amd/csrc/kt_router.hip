@@ -101,12 +101,6 @@ __device__ __forceinline__ int row16_before(int v) {
   return s - v;
 }
 
-// orders a wave's LDS writes before its later LDS reads of other lanes' values, and the other way round
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // The sigmoid in fp32 with the library's exponential (about one rounding), from
 // the exponential of -|l|: it keeps a small score's digits down to fp32's
 // lowest numbers, and 1 - s is sigmoid32(-l).
