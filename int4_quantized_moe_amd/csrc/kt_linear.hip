@@ -689,27 +689,29 @@ __device__ __forceinline__ float dz_of(int act, float dy, float z) {
   return dy * act_slope(act, z);
 }
 
-// v's leading 8 bits, less a step where that is all of v.
-__device__ __forceinline__ uint16_t cut_part(float v) {
-  const uint32_t b = __float_as_uint(v);
-  uint32_t h = b >> 16;
-  if ((b & 0x7fffffffu) > 0x7f800000u) return (uint16_t)(h | 0x40u);  // NaN
-  if ((b & 0xffffu) == 0 && (h & 0x7fffu) != 0 && (h & 0x7fffu) != 0x7f80u) h -= 1;
-  return (uint16_t)h;
+// v's leading 8 bits, less a step where that is all of v.  (Selects, not branches: values of all kinds share a wave.)
+__device__ __forceinline__ uint32_t cut_part(float v) {
+  const uint32_t b = __float_as_uint(v), h = b >> 16, mag = b & 0x7fffffffu;
+  const uint32_t step = (b & 0xffffu) == 0 && mag - 1 < 0x7f7fffffu;  // nonzero, finite
+  return mag > 0x7f800000u ? h | 0x40u : h - step;                   // (a NaN stays one)
 }
 
 // What v's part h leaves; an infinity or a NaN stays whole.
-__device__ __forceinline__ float left_by(float v, uint16_t h) {
-  return (h & 0x7f80) == 0x7f80 ? v : v - bf16_to_float(h);
+__device__ __forceinline__ float left_by(float v, uint32_t h) {
+  return (h & 0x7f80u) == 0x7f80u ? v : v - __uint_as_float(h << 16);
 }
 
-// p0, p1, p2 and the rest of p0 rounded to bf16.
+// p0, p1, p2 and the rest of p0 rounded to bf16.  p2 holds all that is left, so
+// its cut loses nothing; a NaN's later parts may be anything beside p0.
 __device__ __forceinline__ void split_planes(float v, uint16_t (&p)[kMaxPlanes + 1]) {
-  p[0] = cut_part(v);
-  const float r0 = left_by(v, p[0]);
-  p[1] = cut_part(r0);
-  p[2] = float_to_bf16(left_by(r0, p[1]));
-  p[3] = float_to_bf16(r0);
+  const uint32_t h0 = cut_part(v);
+  const float r0 = left_by(v, h0);
+  const uint32_t h1 = cut_part(r0);
+  p[0] = (uint16_t)h0;
+  p[1] = (uint16_t)h1;
+  p[2] = (uint16_t)(__float_as_uint(left_by(r0, h1)) >> 16);
+  const uint32_t r = __float_as_uint(r0);
+  p[3] = (uint16_t)((r + 0x7fffu + (r >> 16 & 1u)) >> 16);
 }
 
 constexpr int kDzRows = 32, kDzCols = 256;
