@@ -268,12 +268,12 @@ struct LinTile {
 // 7168 x 384 from fp32 gradients 84 us so against 77, of 8192 x 7168 x 2048 602
 // against 588).
 //
-// Bound by the MFMAs and, as near, by LDS: a 256 x 256 step takes 2048 cycles of
-// MFMAs per SIMD and 256 KB of LDS traffic per unit, also 2048 cycles (a wave's
-// 128 x 64 outputs reuse a fragment 4 to 8 times); 128 x 128 tiles take 768 LDS
-// cycles for 512 of MFMAs.  Reached: 1.27 PFLOP/s forward at 8192 x 7168 x 2048
-// and 1.23 in d_weight with three planes, where a library's plain product runs at
-// 1.31; the chip's power holds the clock below 2 GHz there.
+// Bound by the MFMAs: at 8192 x 7168 x 2048 they are busy 58% of the time at the
+// 2.0 GHz that the chip's power then leaves, the LDS's index unit 23% and without bank
+// conflicts; the rest is the turn from one step to the next and the epilogue.
+// Reached there: 1.27 PFLOP/s forward and 1.24 in d_weight with three planes (1.21
+// with one), where a library's plain product runs at 1.31.  At a contraction of 384 it is
+// 0.57 to 0.68: of a tile's six steps nothing covers the first copies and the epilogue.
 template <int KIND, int BM, int BN, int WM, int WN, int PLANES>
 __global__ __launch_bounds__(64 * WM* WN, WM* WN > 4 ? 1 : 2) void k_linear(LinearGemm g) {
   constexpr bool kAcrossA = KIND == kLinDw, kAcrossB = KIND != kLinFwd;
@@ -718,7 +718,7 @@ constexpr int kDzRows = 32, kDzCols = 256;
 
 // kDzCols columns x kDzRows rows per block, 8 columns a thread.  WIDE: N is a
 // multiple of 8, so that a thread's values are 16-byte pieces.  Bound by memory:
-// 8192 x 2048 with an activation and three planes moves 168 MB in 41 us (4.1 TB/s).
+// 8192 x 2048 with an activation and four planes moves 201 MB in 50 us (4.0 TB/s).
 template <bool WIDE>
 __global__ __launch_bounds__(256) void k_linear_dz(DzArgs a) {
   __shared__ float red[8][kDzCols + 4];
@@ -843,8 +843,10 @@ static int check_linear(const kt_linear* L, int32_t tokens) {
 //            10.1 us for 16 tokens against 15; 512 x 384: 4.4 us for 64 against 8.3.  It reads the inputs once
 //            per block, so it loses where tokens and K are large (7168 x 384, 64 tokens: 30 against 11.7 us).
 //   big      256 x 256 tiles, where they fill three quarters of the chip (two rows of fragments then serve
-//            twice the MFMAs).  Forward of 8192 x 7168 x 2048: 1.27 against 1.11 PFLOP/s with 128 x 128
-//            tiles, d_weight 1.24 against 1.06, grad_input of 16384 x 2048 x 7168 1.25 against 1.01.  With
+//            twice the MFMAs).  Forward of 8192 x 7168 x 2048: 1.27 against 1.14 PFLOP/s with 128 x 128
+//            tiles, d_weight 1.21 against 1.02 (three planes: 1.26 against 1.14), grad_input of 16384 x 2048
+//            from a contraction of 7168 1.25 against 1.04; of 8192 x 7168 from 2048 the same, and within 5% at
+//            contractions of 384 (forward 83 against 87 us, grad_input 68 against 67, 133 against 135).  With
 //            fewer: 4096 x 2048 x 2048 (128 of them) 56 us against 38.
 //   splits   of the contraction, where 128 x 128 tiles alone leave units without the two blocks they can
 //            hold: as many as give 512 blocks (d_weight of 4096 x 7168 x 384 with three planes: 114 us with
