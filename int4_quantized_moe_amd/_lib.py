@@ -1,7 +1,7 @@
 """ctypes binding of ``libkt_rawint4.so`` (argument marshalling only).
 
 Every function has the name and argument order of its C entry point in
-``include/kt_rawint4.h`` or ``include/kt_block.h``.  Tensors are passed as raw pointers (``data_ptr()``),
+``include/kt_rawint4.h``, ``include/kt_block.h`` or ``include/kt_step.h``.  Tensors are passed as raw pointers (``data_ptr()``),
 ``stream`` defaults to torch's current HIP stream, and a nonzero return code
 raises ``KtRawInt4Error`` with the library's message.  There is no fallback:
 without the built library every call raises.
@@ -38,6 +38,17 @@ KT_CKPT8_E4M3 = 1
 CKPT8_FORMATS = {"int8": KT_CKPT8_INT8, "e4m3": KT_CKPT8_E4M3}
 KT_CKPT8_GROUP = 32
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+KT_NORM_RMS = 0
+KT_NORM_LAYER = 1
+NORMS = {"rms": KT_NORM_RMS, "layer": KT_NORM_LAYER}
+KT_NORM_MAX_HIDDEN = 16384
+KT_ADAMW_STATES_F32 = 0
+KT_ADAMW_STATES_E4M3 = 1
+ADAMW_STATES = {"fp32": KT_ADAMW_STATES_F32, "e4m3": KT_ADAMW_STATES_E4M3}
+KT_ADAMW_BLOCK = 256
+KT_ADAMW_MAX_TENSORS = 65536
+KT_MOE_DECODE_MAX_TOKENS = 64
+KT_MOE_DECODE_MAX_SLOTS = 1024
 
 _vp = ctypes.c_void_p
 
@@ -101,6 +112,51 @@ class kt_ckpt8(ctypes.Structure):  # noqa: N801
     _fields_ = [("format", ctypes.c_int32), ("codes", _vp), ("scales", _vp)]
 
 
+class kt_norm(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("hidden", ctypes.c_int32),
+        ("kind", ctypes.c_int32),
+        ("stream_type", ctypes.c_int32),
+        ("branch_norm", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("weight", _vp),
+        ("bias", _vp),
+        ("branch_weight", _vp),
+        ("branch_bias", _vp),
+        ("gate", _vp),
+    ]
+
+
+class kt_adamw(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("max_norm", ctypes.c_double),
+        ("grad_scale", ctypes.c_double),
+        ("state_format", ctypes.c_int32),
+    ]
+
+
+class kt_adamw_tensor(ctypes.Structure):  # noqa: N801
+    _fields_ = [
+        ("count", ctypes.c_int64),
+        ("param_type", ctypes.c_int32),
+        ("grad_type", ctypes.c_int32),
+        ("decay", ctypes.c_int32),
+        ("param", _vp),
+        ("master", _vp),
+        ("grad", _vp),
+        ("m", _vp),
+        ("v", _vp),
+        ("m_scale", _vp),
+        ("v_scale", _vp),
+    ]
+
+
 _lib = None
 
 
@@ -113,6 +169,7 @@ def load_library() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIBRARY_PATH)
     lp = ctypes.POINTER(kt_rawint4_moe_layer)
     rp, np_, cp = ctypes.POINTER(kt_router), ctypes.POINTER(kt_linear), ctypes.POINTER(kt_ckpt8)
+    mp, ap, tp = ctypes.POINTER(kt_norm), ctypes.POINTER(kt_adamw), ctypes.POINTER(kt_adamw_tensor)
     i32, i64, f32, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
     sigs = {
         "kt_rawint4_moe_workspace_bytes": (sz, [lp, i32]),
@@ -136,6 +193,13 @@ def load_library() -> ctypes.CDLL:
         "kt_linear_bwd_workspace_bytes": (sz, [np_, i32, i32]),
         "kt_linear_bwd": (ctypes.c_int,
                           [np_, i32, _vp, cp, _vp, _vp, i32, _vp, _vp, _vp, _vp, i32, f32, _vp, sz, _vp]),
+        "kt_norm_fwd": (ctypes.c_int, [mp, i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+        "kt_norm_bwd_workspace_bytes": (sz, [mp, i32]),
+        "kt_norm_bwd": (ctypes.c_int, [mp, i32] + [_vp] * 8 + [_vp] * 5 + [i32, f32, _vp, sz, _vp]),
+        "kt_adamw_workspace_bytes": (sz, [i32]),
+        "kt_adamw_step": (ctypes.c_int, [ap, tp, i32, _vp, _vp, _vp, _vp, sz, _vp]),
+        "kt_moe_decode_workspace_bytes": (sz, [lp, i32]),
+        "kt_moe_decode": (ctypes.c_int, [lp, i32, _vp, _vp, _vp, _vp, _vp, sz, _vp]),
         "kt_rawint4_unpack": (ctypes.c_int, [_vp, i64, i64, _vp, _vp]),
         "kt_rawint4_dequant": (ctypes.c_int, [_vp, _vp, i64, i64, _vp, _vp]),
         "kt_rawint4_dequant_mxfp4": (ctypes.c_int, [_vp, _vp, i64, i64, _vp, _vp]),
@@ -341,6 +405,45 @@ def kt_linear_bwd(linear, tokens, inputs, checkpoint, preact, grad_output, grad_
         _ptr(preact), _ptr(grad_output), grad_output_type, _ptr(grad_residual), _ptr(grad_input), _ptr(d_weight),
         _ptr(d_bias), int(bool(accumulate)), float(grad_scale), _ptr(workspace),
         _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_norm_fwd(norm, tokens, x, branch, token_gate, h, y, stream=None) -> None:
+    _check(load_library().kt_norm_fwd(ctypes.byref(norm), tokens, _ptr(x), _ptr(branch), _ptr(token_gate), _ptr(h),
+                                      _ptr(y), _stream(stream)))
+
+
+def kt_norm_bwd_workspace_bytes(norm, tokens) -> int:
+    return _checked_size(load_library().kt_norm_bwd_workspace_bytes(ctypes.byref(norm), int(tokens)))
+
+
+def kt_norm_bwd(norm, tokens, h, branch, token_gate, grad_h, grad_y, grad_x, grad_branch, grad_token_gate, d_weight,
+                d_bias, d_branch_weight, d_branch_bias, d_gate, accumulate, grad_scale, workspace, stream=None) -> None:
+    _check(load_library().kt_norm_bwd(
+        ctypes.byref(norm), tokens, _ptr(h), _ptr(branch), _ptr(token_gate), _ptr(grad_h), _ptr(grad_y), _ptr(grad_x),
+        _ptr(grad_branch), _ptr(grad_token_gate), _ptr(d_weight), _ptr(d_bias), _ptr(d_branch_weight),
+        _ptr(d_branch_bias), _ptr(d_gate), int(bool(accumulate)), float(grad_scale), _ptr(workspace),
+        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_adamw_workspace_bytes(num_tensors) -> int:
+    return _checked_size(load_library().kt_adamw_workspace_bytes(int(num_tensors)))
+
+
+def kt_adamw_step(hyper, tensors, num_tensors, step, grad_norm, lr, workspace, stream=None) -> None:
+    """``tensors``: a ctypes array of kt_adamw_tensor, read during the call."""
+    _check(load_library().kt_adamw_step(ctypes.byref(hyper), tensors, num_tensors, _ptr(step), _ptr(grad_norm),
+                                        _ptr(lr), _ptr(workspace),
+                                        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
+
+
+def kt_moe_decode_workspace_bytes(layer: kt_rawint4_moe_layer, tokens: int) -> int:
+    return _checked_size(load_library().kt_moe_decode_workspace_bytes(ctypes.byref(layer), int(tokens)))
+
+
+def kt_moe_decode(layer, tokens, inputs, expert_ids, route_weights, output, workspace, stream=None) -> None:
+    _check(load_library().kt_moe_decode(ctypes.byref(layer), tokens, _ptr(inputs), _ptr(expert_ids),
+                                        _ptr(route_weights), _ptr(output), _ptr(workspace),
+                                        _nbytes(workspace) if workspace is not None else 0, _stream(stream)))
 
 
 def kt_rawint4_unpack(packed, n, k, codes, stream=None) -> None:

@@ -51,12 +51,44 @@ class DeviceLayer:
                                      self.gate_scale, self.up_scale, self.down_scale,
                                      *(self.lora[n] for n in LORA_NAMES), weight_format=cfg.weight_format)
 
+    @classmethod
+    def from_tensors(cls, cfg: LayerConfig, weights: Dict[str, torch.Tensor],
+                     lora: Optional[Dict[str, torch.Tensor]] = None) -> "DeviceLayer":
+        """A layer on tensors that are on the GPU already, used as they are: ``weights`` has gate_packed,
+        up_packed and down_packed [E, N, K/2] uint8 and gate_scale, up_scale and down_scale [E, N, K/32]
+        bf16; ``lora`` the six LoRA tensors (fp32), or None for the frozen base alone."""
+        dev = weights["gate_packed"].device
+        e, h, i = cfg.num_experts, cfg.hidden, cfg.intermediate
+        self = cls.__new__(cls)
+        self.cfg, self.device = cfg, dev
+        for name, n, k in (("gate", i, h), ("up", i, h), ("down", h, i)):
+            _checked(name + "_packed", weights[name + "_packed"], (e, n, k // 2), torch.uint8, dev)
+            _checked(name + "_scale", weights[name + "_scale"], (e, n, k // 32), torch.bfloat16, dev)
+            setattr(self, name + "_packed", weights[name + "_packed"])
+            setattr(self, name + "_scale", weights[name + "_scale"])
+        if lora is not None:
+            for name, shape in cfg.lora_shapes().items():
+                if lora.get(name) is None:
+                    raise ValueError(f"lora has no {name!r}")
+                _checked(name, lora[name], shape, torch.float32, dev)
+        self.lora = {n: None if lora is None else lora[n] for n in LORA_NAMES}
+        self.layer = _lib.make_layer(cfg.num_experts, cfg.top_k, h, i, cfg.rank, cfg.alpha, cfg.swiglu_limit,
+                                     self.gate_packed, self.up_packed, self.down_packed, self.gate_scale,
+                                     self.up_scale, self.down_scale, *(self.lora[n] for n in LORA_NAMES),
+                                     weight_format=cfg.weight_format)
+        return self
+
     def workspace(self, qlen: int) -> torch.Tensor:
         n = _lib.kt_rawint4_moe_workspace_bytes(self.layer, qlen)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def infer_workspace(self, qlen: int) -> torch.Tensor:
         n = _lib.kt_rawint4_moe_infer_workspace_bytes(self.layer, qlen)
+        return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def decode_workspace(self, tokens: int) -> torch.Tensor:
+        """Of decode() for up to so many tokens."""
+        n = _lib.kt_moe_decode_workspace_bytes(self.layer, tokens)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def checkpoint_workspace(self, qlen: int) -> torch.Tensor:
@@ -83,6 +115,27 @@ class DeviceLayer:
         if output is None:
             output = torch.empty((qlen, self.cfg.hidden), dtype=torch.bfloat16, device=self.device)
         _lib.kt_rawint4_moe_infer(self.layer, qlen, inputs, expert_ids, route_weights, output, workspace, stream)
+        return output
+
+    def decode(self, inputs, expert_ids, route_weights, workspace, output=None, stream=None) -> torch.Tensor:
+        """infer() for a few tokens (at most KT_MOE_DECODE_MAX_TOKENS, and KT_MOE_DECODE_MAX_SLOTS
+        token-slots), in a decode_workspace()."""
+        dev, h, k = self.gate_packed.device, self.cfg.hidden, self.cfg.top_k
+        if inputs.dim() != 2:
+            raise ValueError("inputs must be [tokens, hidden]")
+        tokens = inputs.shape[0]
+        _checked("inputs", inputs, (tokens, h), torch.bfloat16, dev)
+        _checked("expert_ids", expert_ids, (tokens, k), torch.int64, dev)
+        _checked("route_weights", route_weights, (tokens, k), torch.float32, dev)
+        _checked("output", output, (tokens, h), torch.bfloat16, dev)
+        if _elsewhere(_gpu(inputs)):
+            with torch.cuda.device(dev):
+                return self.decode(inputs, expert_ids, route_weights, workspace, output, stream)
+        _workspace(workspace, dev)
+        if output is None:
+            output = _empty((tokens, h), torch.bfloat16, dev, stream)
+        _lib.kt_moe_decode(self.layer, tokens, inputs, expert_ids, route_weights, output, workspace,
+                           _handle(stream, dev))
         return output
 
     def backward(self, inputs, expert_ids, route_weights, grad_output, workspace, grads, accumulate=False,
@@ -434,3 +487,201 @@ class DeviceLinear:
                            grad_residual, grad_input, d_weight, d_bias, accumulate, grad_scale, workspace,
                            _handle(stream, dev))
         return grad_input
+
+
+# ---------------------------------------------------------------- what completes a step
+
+
+class DeviceNorm:
+    """The norms on both sides of a block, with the block's gate and scale and the residual stream:
+    h = x + scale * gate * token_gate * n(branch), y = N(h) * weight + bias.  ``kind`` is "rms" or "layer";
+    the vectors are fp32 [hidden] or None; ``branch_norm``: n is a norm too, with branch_weight and
+    branch_bias."""
+
+    def __init__(self, hidden: int, kind: str = "rms", eps: float = 1e-6, scale: float = 1.0,
+                 weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, branch_norm: bool = False,
+                 branch_weight: Optional[torch.Tensor] = None, branch_bias: Optional[torch.Tensor] = None,
+                 gate: Optional[torch.Tensor] = None):
+        if kind not in _lib.NORMS:
+            raise ValueError(f"kind must be one of {sorted(_lib.NORMS)}, not {kind!r}")
+        vectors = {"weight": weight, "bias": bias, "branch_weight": branch_weight, "branch_bias": branch_bias,
+                   "gate": gate}
+        given = [v for v in vectors.values() if v is not None]
+        for name, v in vectors.items():
+            if v is not None:
+                _checked(name, v, (hidden,), torch.float32, given[0].device)
+        self.hidden, self.kind, self.vectors = hidden, kind, vectors
+        self.branch_norm = bool(branch_norm)
+        self.device = given[0].device if given else None
+        pointers = [None if v is None else v.data_ptr() for v in vectors.values()]
+        self._c = {dtype: _lib.kt_norm(hidden, _lib.NORMS[kind], code, int(self.branch_norm), eps, scale, *pointers)
+                   for dtype, code in _TYPES.items()}
+
+    def _stream_type(self, name, x):
+        """(tokens, device) of a tensor of the residual stream."""
+        if x.dtype not in _TYPES:
+            raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {x.dtype}")
+        if x.dim() != 2:
+            raise ValueError(f"{name} must be [tokens, {self.hidden}]")
+        _checked(name, x, (x.shape[0], self.hidden), x.dtype, x.device if self.device is None else self.device)
+        return x.shape[0], x.device
+
+    def forward(self, x, branch=None, token_gate=None, h=None, y=None, need_h=True, need_y=True, stream=None):
+        """(h, y) of the residual stream x [tokens, hidden] (bf16 or fp32) and a block's output ``branch``
+        (bf16; without it h is x), token_gate [tokens] fp32.  ``h`` may be x itself; what is not needed is
+        None."""
+        tokens, dev = self._stream_type("x", x)
+        shape = (tokens, self.hidden)
+        _checked("branch", branch, shape, torch.bfloat16, dev)
+        _checked("token_gate", token_gate, (tokens,), torch.float32, dev)
+        _checked("h", h, shape, x.dtype, dev)
+        _checked("y", y, shape, torch.bfloat16, dev)
+        if branch is None and (h is not None or token_gate is not None):
+            raise ValueError("h and token_gate need a branch (without it h is x)")
+        if _elsewhere(_gpu(x)):
+            with torch.cuda.device(dev):
+                return self.forward(x, branch, token_gate, h, y, need_h, need_y, stream)
+        if h is None and need_h and branch is not None:
+            h = _empty(shape, x.dtype, dev, stream)
+        if y is None and need_y:
+            y = _empty(shape, torch.bfloat16, dev, stream)
+        _lib.kt_norm_fwd(self._c[x.dtype], tokens, x, branch, token_gate, h, y, _handle(stream, dev))
+        return x if branch is None else h, y
+
+    def workspace(self, tokens: int, device=None) -> torch.Tensor:
+        """Of backward() for up to so many tokens."""
+        n = _lib.kt_norm_bwd_workspace_bytes(self._c[torch.bfloat16], tokens)
+        return torch.empty(n, dtype=torch.uint8, device=device or self.device or "cuda")
+
+    def grad_buffers(self, fill: Optional[float] = None, device=None) -> Dict[str, torch.Tensor]:
+        """fp32 gradients of the vectors that the norms have."""
+        new = torch.empty if fill is None else lambda *s, **k: torch.full(s, fill, **k)
+        return {n: new(self.hidden, dtype=torch.float32, device=device or self.device)
+                for n, v in self.vectors.items() if v is not None}
+
+    def backward(self, h, workspace, grads, branch=None, token_gate=None, grad_h=None, grad_y=None, grad_x=None,
+                 grad_branch=None, grad_token_gate=None, accumulate=False, grad_scale=1.0, need_input=True,
+                 stream=None):
+        """Gradients of forward() at its h, from grad_h (the residual stream's) and grad_y: returns
+        (grad_x, grad_branch) and fills ``grads`` (from grad_buffers(); an empty dict: none) by the window
+        rule and grad_token_gate [tokens] fp32.  grad_x may be grad_h itself.  need_input=False makes
+        no grad_x and grad_branch beyond those given."""
+        tokens, dev = self._stream_type("h", h)
+        shape = (tokens, self.hidden)
+        _checked("branch", branch, shape, torch.bfloat16, dev)
+        _checked("token_gate", token_gate, (tokens,), torch.float32, dev)
+        _checked("grad_h", grad_h, shape, h.dtype, dev)
+        _checked("grad_y", grad_y, shape, torch.bfloat16, dev)
+        _checked("grad_x", grad_x, shape, h.dtype, dev)
+        _checked("grad_branch", grad_branch, shape, torch.bfloat16, dev)
+        _checked("grad_token_gate", grad_token_gate, (tokens,), torch.float32, dev)
+        for name in grads:
+            if name not in self.vectors:
+                raise ValueError(f"grads has no place for {name!r}")
+            _checked(f"grads[{name!r}]", grads[name], (self.hidden,), torch.float32, dev)
+        if _elsewhere(_gpu(h)):
+            with torch.cuda.device(dev):
+                return self.backward(h, workspace, grads, branch, token_gate, grad_h, grad_y, grad_x, grad_branch,
+                                     grad_token_gate, accumulate, grad_scale, need_input, stream)
+        _workspace(workspace, dev)
+        if grad_x is None and need_input:
+            grad_x = _empty(shape, h.dtype, dev, stream)
+        if grad_branch is None and need_input and branch is not None:
+            grad_branch = _empty(shape, torch.bfloat16, dev, stream)
+        _lib.kt_norm_bwd(self._c[h.dtype], tokens, h, branch, token_gate, grad_h, grad_y, grad_x, grad_branch,
+                         grad_token_gate, *(grads.get(n) for n in self.vectors), accumulate, grad_scale, workspace,
+                         _handle(stream, dev))
+        return grad_x, grad_branch
+
+
+class DeviceAdamW:
+    """AdamW over a dict of tensors (fp32 or bf16), all in one call.
+
+    ``states``: "fp32", or "e4m3" for 8-bit moments with one fp32 scale per 256 values.  ``master``: bf16
+    tensors keep an fp32 copy that the updates are made to.  ``max_norm`` clips the gradients by their
+    global norm; with it, or with ``check_finite``, the norm is computed (``grad_norm``), and one that is not
+    finite leaves everything as it was.  ``no_decay``: names without weight decay.  ``state`` (as self.state)
+    and ``step`` continue an earlier run; their tensors are used as they are.
+    self.state[name] has m, v (with 8-bit states codes of m and of sqrt(v), and m_scale, v_scale) and master;
+    self.step_count [1] int64 counts the steps on the GPU, so that a step in a graph can be replayed."""
+
+    def __init__(self, params: Dict[str, torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, states: str = "fp32", master: bool = False,
+                 max_norm: Optional[float] = None, check_finite: bool = False, no_decay=(), state=None, step=0):
+        if states not in _lib.ADAMW_STATES:
+            raise ValueError(f"states must be one of {sorted(_lib.ADAMW_STATES)}, not {states!r}")
+        if not params:
+            raise ValueError("params must hold a tensor")
+        unknown = set(no_decay) - set(params)
+        if unknown:
+            raise ValueError(f"no_decay names no tensor of params: {sorted(unknown)}")
+        self.params, self.states = dict(params), states
+        self.device = dev = next(iter(params.values())).device
+        self.lr, self.betas, self.eps, self.weight_decay, self.max_norm = lr, tuple(betas), eps, weight_decay, max_norm
+        self.state = {}
+        eight = states == "e4m3"
+        for name, p in params.items():
+            if p.dtype not in _TYPES:
+                raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, not {p.dtype}")
+            _checked(name, p, tuple(p.shape), p.dtype, dev)
+            n = p.numel()
+            have = dict((state or {}).get(name) or {})
+            blocks = -(-n // _lib.KT_ADAMW_BLOCK)
+            want = {"m": (torch.float8_e4m3fn if eight else torch.float32, (n,)),
+                    "v": (torch.float8_e4m3fn if eight else torch.float32, (n,))}
+            if eight:
+                want.update(m_scale=(torch.float32, (blocks,)), v_scale=(torch.float32, (blocks,)))
+            if master and p.dtype is torch.bfloat16:
+                want["master"] = (torch.float32, tuple(p.shape))
+            extra = set(have) - set(want)
+            if extra:
+                raise ValueError(f"state[{name!r}] has no place for {sorted(extra)}")
+            for key, (dtype, shape) in want.items():
+                t = have.get(key)
+                if t is None:
+                    t = p.detach().float() if key == "master" else torch.zeros(shape, dtype=dtype, device=dev)
+                elif key in ("m", "v") and t.numel() == n and t.dim() != 1:
+                    t = t.view(-1)
+                _checked(f"state[{name!r}][{key!r}]", t, shape, dtype, dev)
+                have[key] = t
+            self.state[name] = have
+        if isinstance(step, torch.Tensor):
+            _checked("step", step, (1,), torch.int64, dev)
+            self.step_count = step
+        else:
+            self.step_count = torch.full((1,), int(step), dtype=torch.int64, device=dev)
+        self.grad_norm = None
+        if max_norm is not None or check_finite:
+            self.grad_norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self._workspace = torch.empty(_lib.kt_adamw_workspace_bytes(len(params)), dtype=torch.uint8, device=dev)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._tensors = (_lib.kt_adamw_tensor * len(params))()
+        for c, (name, p) in zip(self._tensors, params.items()):
+            s = self.state[name]
+            c.count, c.param_type, c.decay = p.numel(), _TYPES[p.dtype], int(name not in no_decay)
+            c.param, c.master, c.m, c.v = ptr(p), ptr(s.get("master")), ptr(s["m"]), ptr(s["v"])
+            c.m_scale, c.v_scale = ptr(s.get("m_scale")), ptr(s.get("v_scale"))
+
+    def step(self, grads: Dict[str, torch.Tensor], grad_scale: float = 1.0, lr: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+        """One step from ``grads`` (a gradient, fp32 or bf16, for every name of params), times grad_scale.
+        ``lr`` [1] fp32 on the GPU replaces self.lr, for schedules inside a graph.  Steps of one optimizer
+        share its state and workspace: they run one after another."""
+        dev = self.device
+        for c, (name, p) in zip(self._tensors, self.params.items()):
+            g = grads.get(name)
+            if g is None:
+                raise ValueError(f"grads has no {name!r}")
+            kind = _TYPES.get(g.dtype)
+            if kind is None:
+                raise ValueError(f"grads[{name!r}] must be torch.float32 or torch.bfloat16, not {g.dtype}")
+            _checked(f"grads[{name!r}]", g, p.shape, g.dtype, dev)
+            c.grad, c.grad_type = g.data_ptr(), kind
+        _checked("lr", lr, (1,), torch.float32, dev)
+        if _elsewhere(_gpu(self.step_count)):
+            with torch.cuda.device(dev):
+                return self.step(grads, grad_scale, lr, stream)
+        hyper = _lib.kt_adamw(self.lr, *self.betas, self.eps, self.weight_decay, self.max_norm or 0.0, grad_scale,
+                              _lib.ADAMW_STATES[self.states])
+        _lib.kt_adamw_step(hyper, self._tensors, len(self._tensors), self.step_count, self.grad_norm, lr,
+                           self._workspace, _handle(stream, dev))
