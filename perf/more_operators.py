@@ -366,7 +366,7 @@ def _own(s, case):
             kept["out"] = {n: {"param": q["param"], **state[n]} for n, q in s["tensors"].items()}
             kept["out"]["step"] = kept["opt"].step_count
             if case["clip"]:
-                kept["out"]["norm"] = kept["opt"].grad_norm
+                kept["out"]["norm"] = kept["opt"].grad_norm.view(())
         elif op == "experts":
             cfg = workloads.LayerConfig("decode", case["experts"], case["top_k"], case["hidden"], case["inter"], case["rank"] or 1, s["lora_scale"] * (case["rank"] or 1), case["tokens"], case["limit"], weight_format=case["format"])
             weights = {n + p: s[n + p] for n in ("gate", "up", "down") for p in ("_packed", "_scale")}
