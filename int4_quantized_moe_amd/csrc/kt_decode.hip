@@ -2,20 +2,26 @@
 // down with the weighted sum over the slots in another, two small ones more with LoRA.
 //
 // With few tokens an expert has one or two of them, and the time is that of
-// reading its packed rows once.  Weights go into the MFMAs as bf16, tokens as
-// the other operand's rows, one MFMA (32 contraction values) per 16 weight rows and
-// scale group, so that the scale multiplies the group's sum in fp32.
+// reading its packed rows once.  Weights go into the MFMAs as bf16, one MFMA
+// (32 contraction values) per 16 weight rows and scale group, so that the
+// scale multiplies the group's sum in fp32.
 //   RAWINT4: a code c becomes 1 + c / 16, by a shift and an and-or for two of
 //   them, exact in bf16, and
 //     sum (c - 8) x = 16 (sum (1 + c / 16) x - 3/2 sum x),
-//   where -3/2 sum x of the group is the MFMA's initial sum.  Products are
-//   exact, whatever the inputs' and scales' size.
+//   where -3/2 sum x of the group is the MFMA's initial sum (an MFMA of x with
+//   -3/2).  Products are exact, whatever the inputs' and scales' size.
 //   MXFP4: a code is converted to bf16 as it is, the initial sum is 0.
-// Inputs are bf16 as given; h, fp32, enters as two bf16 (hi and lo) in two
-// rows of the same MFMA, 2^-16 of it left out.
+// Inputs are bf16 as given; h, fp32, enters as two bf16 (hi and lo), 2^-16 of
+// it left out.
 //
-// A lane loads 16 bytes of a row, a whole scale group; an exchange of 4 x 4
-// dwords between the wave's four rows of 16 lanes gives each MFMA one group.
+// The other operand's 16 rows are four vectors (tokens, or hi and lo of two)
+// by four scale groups: 16 bytes a lane bring 128 contraction values of all
+// four, and of the MFMA with group j's weights the rows of group j are
+// taken, register j of every lane.  So x and h need no staging: they come from
+// the caches in the same stream of loads as the codes, and no workgroup
+// waits for another's.  A lane loads 16 bytes of a weight row, a whole scale
+// group; an exchange of 4 x 4 dwords between the wave's four rows of 16 lanes
+// gives each MFMA one group.
 #include "kt_step_common.hpp"
 
 #include <math.h>
@@ -33,7 +39,8 @@ struct DecodeArgs {
   const uint8_t *wg, *wu, *wd;
   const uint16_t *sg, *su, *sd;
   const float *ag, *bg, *au, *bu, *ad, *bd;
-  float* h;       // [S][I]
+  float* h;       // [S][I], with LoRA
+  uint16_t* hs;   // [S][2][I]: h as bf16 hi and lo, in the codes' order
   int32_t* next;  // [S]: the next slot of the same expert, -1 for none
   int32_t* lead;  // [S]: whether the slot is its expert's first
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
@@ -42,34 +49,26 @@ struct DecodeArgs {
 
 typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
 
-// The slots of slot `s`'s expert from s on, in order, to list[] (wave-uniform
-// count); 0 if the slot is dropped or not its expert's first.  Every wave
-// finds the same; wave 0 writes.  `next`: the slot after s, or -1.
-__device__ __forceinline__ int slots_of(const DecodeArgs& a, int s, uint16_t* list, int& next) {
+// The slots of slot `s`'s expert e from s on, in order, to list[] (wave 0
+// writes; every wave finds the same number); 0 if another slot comes before.
+// `next`: the slot after s, or -1.
+__device__ __forceinline__ int slots_of(const DecodeArgs& a, int s, int64_t e, uint16_t* list, int& next) {
   const int lane = threadIdx.x & 63;
-  const int64_t e = a.ids[s];
   next = -1;
-  if (e < 0 || e >= a.E) return 0;
   int n = 0;
+  bool led = false;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
     const bool hit = s0 + lane < a.S && a.ids[s0 + lane] == e;
     const uint64_t mask = __ballot(hit);
-    if (s0 <= s) {
-      // a hit before s: another slot leads
-      const uint64_t before = s - s0 >= 64 ? ~0ull : (1ull << (s - s0)) - 1;
-      if (mask & before) n = -1024 * 1024;
-    }
-    const int at = n + __popcll(mask & ((1ull << lane) - 1));
-    if (hit && at >= 0 && threadIdx.x < 64) list[at] = (uint16_t)(s0 + lane);
-    if (next < 0) {
-      uint64_t after = mask;
-      if (s0 + 63 <= s) after = 0;
-      else if (s0 <= s) after &= ~((2ull << (s - s0)) - 1);
-      if (after) next = s0 + __ffsll((unsigned long long)after) - 1;
-    }
-    n += __popcll(mask);
+    const uint64_t upto = s - s0 >= 63 ? ~0ull : s < s0 ? 0ull : (2ull << (s - s0)) - 1;  // slots <= s of these 64
+    const uint64_t own = s >= s0 && s - s0 < 64 ? 1ull << (s - s0) : 0ull;
+    led |= (mask & upto & ~own) != 0;
+    const uint64_t rest = mask & ~(upto & ~own);
+    if (hit && (rest >> lane & 1) && threadIdx.x < 64) list[n + __popcll(rest & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+    n += __popcll(rest);
+    if (next < 0 && (rest & ~own)) next = s0 + __ffsll((unsigned long long)(rest & ~own)) - 1;
   }
-  return n > 0 ? n : 0;
+  return led ? 0 : n;
 }
 
 // Registers r[0..3] of a lane in row q hold the 16 bytes (dwords 0..3) of group q; afterwards r[i] is dword q of group i.
@@ -103,102 +102,167 @@ __device__ __forceinline__ u32x4 order8(u32x4 v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 16 weight rows from `w` (row pitch K / 2 bytes) and `sc` (pitch K / 32), contraction
-// groups 4 it .. 4 it + 3: codes and scales of this lane's row.
-struct RowTile {
-  const uint8_t* w;
-  const uint16_t* s;
-  int G;  // groups of a row
+// 256 contraction values (8 scale groups) of 16 weight rows, this lane's share: codes of groups q and 4 + q of row n,
+// and the row's 8 scales.  Bases are the same in all lanes, offsets (bytes) are the lane's.
+struct Codes {
+  u32x4 c[2], s;
 };
-__device__ __forceinline__ u32x4 tile_codes(const RowTile& t, int it, int q) {
-  return 4 * it + q < t.G ? *reinterpret_cast<const u32x4*>(t.w + (size_t)(4 * it + q) * 16) : u32x4{0, 0, 0, 0};
+struct Row {
+  const uint8_t *w, *s;  // an expert's codes and scales
+  uint32_t wo, so;       // the lane's row; codes from group q on
+};
+__device__ __forceinline__ Row row_of(const uint8_t* w, const uint16_t* s, size_t e, int rows, int row, int G, int q) {
+  return {w + e * rows * ((size_t)G * 16), reinterpret_cast<const uint8_t*>(s) + e * rows * ((size_t)G * 2),
+          (uint32_t)row * (uint32_t)(G * 16) + q * 16, (uint32_t)row * (uint32_t)(G * 2)};
 }
-__device__ __forceinline__ void tile_scales(const RowTile& t, int it, float* s) {
+__device__ __forceinline__ void load_codes(const Row& r, int u, Codes& c) {
+  const uint8_t* w = r.w + (size_t)u * 128;
+  c.c[0] = *reinterpret_cast<const u32x4*>(w + r.wo);
+  c.c[1] = *reinterpret_cast<const u32x4*>(w + 64 + r.wo);
+  c.s = *reinterpret_cast<const u32x4_u2*>(r.s + (size_t)u * 16 + r.so);
+}
+// the last unit of a row that ends inside it
+__device__ __forceinline__ void load_codes_end(const Row& r, int u, int G, int q, Codes& c) {
+  const uint8_t* w = r.w + (size_t)u * 128;
+  c.c[0] = c.c[1] = c.s = u32x4{0, 0, 0, 0};
+  if (8 * u + q < G) c.c[0] = *reinterpret_cast<const u32x4*>(w + r.wo);
+  if (8 * u + 4 + q < G) c.c[1] = *reinterpret_cast<const u32x4*>(w + 64 + r.wo);
+  const uint16_t* s = reinterpret_cast<const uint16_t*>(r.s + (size_t)u * 16 + r.so);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) s[g] = 4 * it + g < t.G ? bf16_to_float(t.s[4 * it + g]) : 0.f;
+  for (int g = 0; g < 8; ++g)
+    if (8 * u + g < G) c.s[g / 2] |= (uint32_t)s[g] << (16 * (g & 1));
 }
 
-constexpr int kPadRow = 16;  // bytes between the rows of LDS planes, beyond their length
+// The vectors' share of the same values: of the lane's vector (n / 4) and group
+// n % 4 the 8 values from 8 q on.  `o`: where they start, in bytes.
+struct Vecs {
+  u32x4 v[2];
+};
+__device__ __forceinline__ uint32_t vec_offset(uint32_t vec, int len, int n, int q) {
+  return (vec * (uint32_t)len + (n & 3) * 32 + q * 8) * 2;
+}
+__device__ __forceinline__ void load_vecs(const uint16_t* v, uint32_t o, int u, Vecs& x) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(v) + (size_t)u * 512;
+  x.v[0] = *reinterpret_cast<const u32x4*>(p + o);
+  x.v[1] = *reinterpret_cast<const u32x4*>(p + 256 + o);
+}
+__device__ __forceinline__ void load_vecs_end(const uint16_t* v, uint32_t o, int u, int G, int n, Vecs& x) {
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(v) + (size_t)u * 512;
+  x.v[0] = x.v[1] = u32x4{0, 0, 0, 0};
+  if (8 * u + (n & 3) < G) x.v[0] = *reinterpret_cast<const u32x4*>(p + o);
+  if (8 * u + 4 + (n & 3) < G) x.v[1] = *reinterpret_cast<const u32x4*>(p + 256 + o);
+}
+
+// The MFMAs' initial sums for four groups of the vectors.
+template <bool MX>
+__device__ __forceinline__ floatx4 initial(const u32x4& x) {
+  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
+  return MX ? zero : mfma_bf16(x, u32x4{0xbfc0bfc0u, 0xbfc0bfc0u, 0xbfc0bfc0u, 0xbfc0bfc0u}, zero);
+}
+
+// Adds half i of the codes' values times the vectors to this lane's sum (weight row n, vector q).
+template <bool MX>
+__device__ __forceinline__ void multiply(const Codes& c, int i, const u32x4& x, const floatx4& init, float& acc) {
+  uint32_t r[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
+  transpose4(r);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t s = c.s[2 * i + j / 2];
+    acc = fmaf(j & 1 ? bf_hi(s) : bf_lo(s), mfma_bf16(x, codes_bf16<MX>(r[j]), init)[j], acc);
+  }
+  __builtin_amdgcn_sched_barrier(0);  // (more MFMAs side by side take registers from the loads ahead)
+}
+
+constexpr int kVecs = 4;      // tokens that gate and up take at a time
+constexpr int kLoraParts = 8;  // runs of the ranks
 
 // Gate and up.  A workgroup has 16 columns of I of one expert (its first
-// slot's block; the others leave at once) for all of its tokens, P at a time;
-// the four waves split the contraction.  Lane l: weight row l % 16, MFMA row 4 (l / 16) is token l / 16 (of P = 4).
-template <bool MX, int P>
-__global__ __launch_bounds__(256) void k_decode_gate_up(DecodeArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
+// slot's block; the others leave at once) for all of its tokens, four at a time.
+// Its four waves split the contraction.
+template <bool MX, bool LORA>
+__global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
   __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
-  __shared__ float red[4][2][4][16];
+  __shared__ float red[2][4][kVecs][16];
+  __shared__ float lora[LORA ? kLoraParts : 1][2][kVecs][16];
   const int slot = blockIdx.y, i0 = blockIdx.x * 16;
-  int next;
-  const int M = slots_of(a, slot, list, next);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int64_t e = a.ids[slot];
+  int next = -1, M = 0;
+  if (e >= 0 && e < a.E) M = slots_of(a, slot, e, list, next);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.next[slot] = next;
     a.lead[slot] = M > 0;
   }
   if (!M) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int64_t e = a.ids[slot];
-  const int G = a.H / 32, its = (G + 3) / 4, pitch = its * 256 + kPadRow, gp = its * 4;
-  uint8_t* xs = lds;                                          // [P][pitch]: tokens in the codes' order
-  float* sum = reinterpret_cast<float*>(lds + P * pitch);     // [P][gp]: -3/2 of a group's sum
-  const size_t row = (size_t)e * a.I + i0 + n;
-  const RowTile tg{a.wg + row * (a.H / 2), a.sg + row * G, G}, tu{a.wu + row * (a.H / 2), a.su + row * G, G};
-  const int tok = P == 4 ? q : P == 2 ? q >> 1 : 0;   // whose sums this lane holds
-  const int arow = P == 4 ? n >> 2 : P == 2 ? n >> 3 : 0;  // which token's values it hands in
+  // (the last wave takes the end of rows that are no whole units)
+  const int G = a.H / 32, units = G / 8, per = (units + 3) / 4, kw = __builtin_amdgcn_readfirstlane(wave);
+  const int u0 = min(units, kw * per), u1 = min(units, u0 + per);
+  const Row rg = row_of(a.wg, a.sg, e, a.I, i0 + n, G, q), ru = row_of(a.wu, a.su, e, a.I, i0 + n, G, q);
   __syncthreads();
-  for (int m0 = 0; m0 < M; m0 += P) {
-    const int nt = min(P, M - m0);
-    if (m0) __syncthreads();
-    for (int p = 0; p < nt; ++p) {
-      const uint16_t* x = a.x + (size_t)(list[m0 + p] / a.k) * a.H;
-      for (int c = threadIdx.x; c < its * 16; c += 256) {
-        u32x4 v = {0, 0, 0, 0};
-        if (c * 8 < a.H) v = *reinterpret_cast<const u32x4*>(x + c * 8);
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s += bf_lo(v[j]) + bf_hi(v[j]);
-        s += dpp_f<0xB1>(s);
-        s += dpp_f<0x4E>(s);
-        *reinterpret_cast<u32x4*>(xs + p * pitch + c * 16) = MX ? v : order8(v);
-        if ((c & 3) == 0) sum[p * gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
-      }
-    }
-    __syncthreads();
+  for (int m0 = 0; m0 < M; m0 += kVecs) {
+    const int nt = min(kVecs, M - m0);
+    const uint32_t xo = vec_offset(list[m0 + min(n >> 2, nt - 1)] / a.k, a.H, n, q);
     float g = 0.f, u = 0.f;
-    const int trow = min(arow, nt - 1), ttok = min(tok, nt - 1);
-    for (int it = wave; it < its; it += 4) {
-      u32x4 cg = tile_codes(tg, it, q), cu = tile_codes(tu, it, q);
-      float sg[4], su[4];
-      tile_scales(tg, it, sg);
-      tile_scales(tu, it, su);
-      uint32_t rg[4] = {cg.x, cg.y, cg.z, cg.w}, ru[4] = {cu.x, cu.y, cu.z, cu.w};
-      transpose4(rg);
-      transpose4(ru);
+    auto use = [&](const Codes& cg, const Codes& cu, const Vecs& xv) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const u32x4 xv = *reinterpret_cast<const u32x4*>(xs + trow * pitch + it * 256 + j * 64 + q * 16);
-        const float c0 = sum[ttok * gp + it * 4 + j];
-        const floatx4 init = {c0, 0.f, 0.f, 0.f};
-        g = fmaf(sg[j], mfma_bf16(xv, codes_bf16<MX>(rg[j]), init).x, g);
-        u = fmaf(su[j], mfma_bf16(xv, codes_bf16<MX>(ru[j]), init).x, u);
+      for (int i = 0; i < 2; ++i) {
+        const u32x4 x = MX ? xv.v[i] : order8(xv.v[i]);
+        const floatx4 init = initial<MX>(x);
+        multiply<MX>(cg, i, x, init, g);
+        multiply<MX>(cu, i, x, init, u);
       }
+    };
+    Codes cg[2], cu[2];
+    Vecs xv[2];
+    auto load = [&](int v, int b) {
+      load_codes(rg, v, cg[b]);
+      load_codes(ru, v, cu[b]);
+      load_vecs(a.x, xo, v, xv[b]);
+    };
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (u0 + b < u1) load(u0 + b, b);
+    if (LORA) {
+      // columns by gate and up by runs of the ranks
+      const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
+      const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
+      const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
+      float t[kVecs] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        const float w = b[r];
+#pragma unroll
+        for (int p = 0; p < kVecs; ++p)
+          if (p < nt) t[p] = fmaf(w, a.ua[(size_t)list[m0 + p] * 2 * a.R + up * a.R + r], t[p]);
+      }
+#pragma unroll
+      for (int p = 0; p < kVecs; ++p) lora[part][up][p][c] = t[p];
     }
-    // (P < 4: rows of lanes that hold the same token hold the same sums)
-    red[wave][0][q][n] = g;
-    red[wave][1][q][n] = u;
+    for (int v = u0; v < u1; v += 2) {
+      use(cg[0], cu[0], xv[0]);
+      if (v + 2 < u1) load(v + 2, 0);
+      if (v + 1 < u1) use(cg[1], cu[1], xv[1]);
+      if (v + 3 < u1) load(v + 3, 1);
+    }
+    if (kw == 3 && G % 8) {
+      load_codes_end(rg, units, G, q, cg[0]);
+      load_codes_end(ru, units, G, q, cu[0]);
+      load_vecs_end(a.x, xo, units, G, n, xv[0]);
+      use(cg[0], cu[0], xv[0]);
+    }
+    red[0][kw][q][n] = g;
+    red[1][kw][q][n] = u;
     __syncthreads();
     if (threadIdx.x < 16 * nt) {
-      const int p = threadIdx.x >> 4, c = threadIdx.x & 15, qr = P == 4 ? p : P == 2 ? 2 * p : 0;
+      const int p = threadIdx.x >> 4, c = threadIdx.x & 15;
       const float by = MX ? 1.f : 16.f;
-      float gv = 0.f, uv = 0.f;
-      for (int w = 0; w < 4; ++w) gv += red[w][0][qr][c], uv += red[w][1][qr][c];
-      gv *= by, uv *= by;
+      float gv = by * (red[0][0][p][c] + red[0][1][p][c] + red[0][2][p][c] + red[0][3][p][c]);
+      float uv = by * (red[1][0][p][c] + red[1][1][p][c] + red[1][2][p][c] + red[1][3][p][c]);
       const int s = list[m0 + p];
-      if (a.R) {
-        const float *bg = a.bg + ((size_t)e * a.I + i0 + c) * a.R, *bu = a.bu + ((size_t)e * a.I + i0 + c) * a.R;
-        const float *ug = a.ua + (size_t)s * 2 * a.R, *uu = ug + a.R;
+      if (LORA) {
         float lg = 0.f, lu = 0.f;
-        for (int r = 0; r < a.R; ++r) lg = fmaf(bg[r], ug[r], lg), lu = fmaf(bu[r], uu[r], lu);
+#pragma unroll
+        for (int r = 0; r < kLoraParts; ++r) lg += lora[r][0][p][c], lu += lora[r][1][p][c];
         gv = fmaf(a.sc, lg, gv), uv = fmaf(a.sc, lu, uv);
       }
       if (a.limit > 0.f) {
@@ -206,135 +270,149 @@ __global__ __launch_bounds__(256) void k_decode_gate_up(DecodeArgs a) {
         gv = gv > a.limit ? a.limit : gv;
         uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
       }
-      a.h[(size_t)s * a.I + i0 + c] = gv * sigmoid_f(gv) * uv;
+      const float h = gv * sigmoid_f(gv) * uv;
+      uint16_t hi, lo;
+      split_bf16(h, hi, lo);
+      uint16_t* o = a.hs + (size_t)s * 2 * a.I + i0 + (MX ? c : perm_pos(c));
+      o[0] = hi;
+      o[a.I] = lo;
+      if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
     }
+    if (m0 + kVecs < M) __syncthreads();
   }
 }
 
-// x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens.
+// x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens, four at a time.
 template <bool DOWN>
 __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
+  const int64_t e = a.ids[blockIdx.y];
+  if (e < 0 || e >= a.E) return;
   int next;
-  const int M = slots_of(a, blockIdx.y, list, next);
+  const int M = slots_of(a, blockIdx.y, e, list, next);
   if (!M) return;
   __syncthreads();
   const int rows = DOWN ? a.R : 2 * a.R, r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (r >= rows) return;
-  const size_t e = (size_t)a.ids[blockIdx.y];
   const int K = DOWN ? a.I : a.H;
-  const float* w = (DOWN ? a.ad : r < a.R ? a.ag : a.au) + (e * a.R + (r < a.R ? r : r - a.R)) * K;
-  for (int m = 0; m < M; ++m) {
-    const int s = list[m];
-    float v = 0.f;
+  const float* w = (DOWN ? a.ad : r < a.R ? a.ag : a.au) + ((size_t)e * a.R + (r < a.R ? r : r - a.R)) * K;
+  for (int m0 = 0; m0 < M; m0 += kVecs) {
+    const int nt = min(kVecs, M - m0);
+    float v[kVecs] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int c = lane * 4; c < K; c += 256) {
       const float4 b = *reinterpret_cast<const float4*>(w + c);
-      float4 x;
-      if (DOWN) {
-        x = *reinterpret_cast<const float4*>(a.h + (size_t)s * K + c);
-      } else {
-        const u32pair p = *reinterpret_cast<const u32pair*>(a.x + (size_t)(s / a.k) * K + c);
-        x = float4{bf_lo(p.x), bf_hi(p.x), bf_lo(p.y), bf_hi(p.y)};
+#pragma unroll
+      for (int p = 0; p < kVecs; ++p) {
+        if (p >= nt) break;
+        float4 x;
+        if (DOWN) {
+          x = *reinterpret_cast<const float4*>(a.h + (size_t)list[m0 + p] * K + c);
+        } else {
+          const u32pair t = *reinterpret_cast<const u32pair*>(a.x + (size_t)(list[m0 + p] / a.k) * K + c);
+          x = float4{bf_lo(t.x), bf_hi(t.x), bf_lo(t.y), bf_hi(t.y)};
+        }
+        v[p] = fmaf(b.x, x.x, v[p]);
+        v[p] = fmaf(b.y, x.y, v[p]);
+        v[p] = fmaf(b.z, x.z, v[p]);
+        v[p] = fmaf(b.w, x.w, v[p]);
       }
-      v = fmaf(b.x, x.x, v);
-      v = fmaf(b.y, x.y, v);
-      v = fmaf(b.z, x.z, v);
-      v = fmaf(b.w, x.w, v);
     }
-    v = wave_sum(v);
-    if (lane == 0) (DOWN ? a.ud : a.ua)[(size_t)s * rows + r] = v;
+#pragma unroll
+    for (int p = 0; p < kVecs; ++p) {
+      const float t = wave_sum(v[p]);
+      if (p < nt && lane == 0) (DOWN ? a.ud : a.ua)[(size_t)list[m0 + p] * rows + r] = t;
+    }
   }
 }
 
 constexpr int kDownWaves = 8;
-constexpr int kDownK = 2048;  // contraction values of h staged at a time
+constexpr int kDownDepth = 3;  // units of loads ahead
 
 // Down and the sum over the slots.  A workgroup has 16 columns of H; its waves
-// take the experts in turn (a wave per expert, the whole contraction) for one token at a time
-// and add to sums of their own per token, which the end joins in the waves' order.
-template <bool MX>
-__global__ __launch_bounds__(512) void k_decode_down(DecodeArgs a) {
-  extern __shared__ __align__(16) uint8_t lds[];
+// take the experts in turn (a wave per expert, the whole contraction), two tokens at a
+// time, and add to sums of their own per token, which the end joins in the waves' order.
+template <bool MX, bool LORA>
+__global__ __launch_bounds__(512, 4) void k_decode_down(DecodeArgs a) {
+  extern __shared__ __align__(16) float acc[];  // [waves][T][16]
   __shared__ uint16_t order[KT_MOE_DECODE_MAX_SLOTS];
+  __shared__ int16_t next[KT_MOE_DECODE_MAX_SLOTS];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int h0 = blockIdx.x * 16;
-  const int G = a.I / 32, kc = min(a.I, kDownK), gp = (kc / 32 + 3) / 4 * 4;
-  const int plane = gp * 64 + kPadRow;  // bytes of the hi or the lo plane
-  const int stage = 2 * plane + gp * 4;
-  uint8_t* hs = lds + wave * stage;
-  float* sum = reinterpret_cast<float*>(hs + 2 * plane);
-  float* acc = reinterpret_cast<float*>(lds + kDownWaves * stage);  // [waves][T][16]
-  for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 512) acc[i] = 0.f;
+  const int h0 = blockIdx.x * 16, G = a.I / 32, units = G / 8;
   int U = 0;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
     const bool lead = s0 + lane < a.S && a.lead[s0 + lane];
     const uint64_t mask = __ballot(lead);
-    if (lead && wave == 0) order[U + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+    if (wave == 0) {
+      if (s0 + lane < a.S) next[s0 + lane] = (int16_t)a.next[s0 + lane];
+      if (lead) order[U + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+    }
     U += __popcll(mask);
   }
+  for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 512) acc[i] = 0.f;
   __syncthreads();
   for (int j = wave; j < U; j += kDownWaves) {
-    const int first = order[j];
-    const size_t e = (size_t)a.ids[first], row = e * a.H + h0 + n;
-    for (int s = first; s >= 0; s = a.next[s]) {
+    const int first = __builtin_amdgcn_readfirstlane(order[j]);
+    const size_t e = (size_t)a.ids[first];
+    const Row rd = row_of(a.wd, a.sd, e, a.H, h0 + n, G, q);
+    for (int s = first; s >= 0;) {
+      const int s1 = __builtin_amdgcn_readfirstlane(next[s]);
+      // vectors: hi and lo of slot s, hi and lo of slot s1
+      const uint32_t ho = vec_offset(((n >> 3) && s1 >= 0 ? s1 : s) * 2 + (n >> 2 & 1), a.I, n, q);
+      Codes cd[kDownDepth];
+      Vecs hv[kDownDepth];
       float y = 0.f;
-      for (int k0 = 0; k0 < a.I; k0 += kDownK) {
-        const int len = min(kDownK, a.I - k0), g0 = k0 / 32, g1 = (len / 32 + 3) / 4 * 4;
-        wave_fence();
-        // 4 values a lane to hi and lo planes; an even lane and its neighbour make 16 bytes of each
-        for (int c = lane * 4; c < g1 * 32; c += 256) {
-          float4 v = {0, 0, 0, 0};
-          if (c < len) v = *reinterpret_cast<const float4*>(a.h + (size_t)s * a.I + k0 + c);
-          const float f[4] = {v.x, v.y, v.z, v.w};
-          uint16_t hi[4], lo[4];
-          float t = 0.f;
+      auto use = [&](const Codes& c, const Vecs& v) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            split_bf16(f[i], hi[i], lo[i]);
-            t += bf16_to_float(hi[i]) + bf16_to_float(lo[i]);
-          }
-          t += dpp_f<0xB1>(t);
-          t += dpp_f<0x4E>(t);
-          t += dpp_f<0x141>(t);
-          const uint32_t h01 = pack2(hi[0], hi[1]), h23 = pack2(hi[2], hi[3]);
-          const uint32_t l01 = pack2(lo[0], lo[1]), l23 = pack2(lo[2], lo[3]);
-          // even lanes make the hi plane's 16 bytes, odd ones the lo plane's
-          const bool odd = lane & 1;
-          const uint32_t p01 = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h01 : l01), 0xB1, 0xf, 0xf, true);
-          const uint32_t p23 = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h23 : l23), 0xB1, 0xf, 0xf, true);
-          const u32x4 v8 = odd ? u32x4{p01, p23, l01, l23} : u32x4{h01, h23, p01, p23};
-          *reinterpret_cast<u32x4*>(hs + (odd ? plane : 0) + (c >> 3) * 16) = MX ? v8 : order8(v8);
-          if ((lane & 7) == 0) sum[c >> 5] = MX ? 0.f : -1.5f * t;
-        }
-        wave_fence();
-        const RowTile t{a.wd + row * (a.I / 2) + k0 / 2, a.sd + row * G + g0, len / 32};
-        for (int it = 0; it < g1 / 4; ++it) {
-          const u32x4 cd = tile_codes(t, it, q);
-          float sd[4];
-          tile_scales(t, it, sd);
-          uint32_t rd[4] = {cd.x, cd.y, cd.z, cd.w};
-          transpose4(rd);
+        for (int i = 0; i < 2; ++i) multiply<MX>(c, i, v.v[i], initial<MX>(v.v[i]), y);
+      };
+      auto load = [&](int u, int b) {
+        load_codes(rd, u, cd[b]);
+        load_vecs(a.hs, ho, u, hv[b]);
+      };
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            // MFMA rows in turn: hi, lo
-            const u32x4 hv = *reinterpret_cast<const u32x4*>(hs + (n & 1) * plane + it * 256 + g * 64 + q * 16);
-            const floatx4 d = mfma_bf16(hv, codes_bf16<MX>(rd[g]), floatx4{sum[it * 4 + g], 0.f, 0.f, 0.f});
-            y = fmaf(sd[g], d.x + d.y, y);
-          }
+      for (int b = 0; b < kDownDepth; ++b)
+        if (b < units) load(b, b);
+      for (int u = 0; u < units; u += kDownDepth) {
+#pragma unroll
+        for (int b = 0; b < kDownDepth; ++b) {
+          if (u + b < units) use(cd[b], hv[b]);
+          if (u + b + kDownDepth < units) load(u + b + kDownDepth, b);
         }
       }
+      if (G % 8) {
+        load_codes_end(rd, units, G, q, cd[0]);
+        load_vecs_end(a.hs, ho, units, G, n, hv[0]);
+        use(cd[0], hv[0]);
+      }
+      // hi + lo: rows of lanes 0 and 1 have slot s, 2 and 3 slot s1
+      uint32_t y0 = __float_as_uint(y), y1 = y0;
+      swap16(y0, y1);
+      y = __uint_as_float(y0) + __uint_as_float(y1);
       if (!MX) y *= 16.f;
-      if (a.R) {
+      const int mine = q < 2 ? s : s1;
+      if (LORA) {
         // a quarter of the ranks a row of lanes
-        const float *b = a.bd + row * a.R, *u = a.ud + (size_t)s * a.R;
-        float t = 0.f;
-        for (int r = q; r < a.R; r += 4) t = fmaf(b[r], u[r], t);
-        y = fmaf(a.sc, rows_sum(t), y);
+        const float* b = a.bd + (e * a.H + h0 + n) * a.R;
+        float t0 = 0.f, t1 = 0.f;
+#pragma unroll 1
+        for (int r = q; r < a.R; r += 4) {
+          t0 = fmaf(b[r], a.ud[(size_t)s * a.R + r], t0);
+          if (s1 >= 0) t1 = fmaf(b[r], a.ud[(size_t)s1 * a.R + r], t1);
+        }
+        t0 = rows_sum(t0), t1 = rows_sum(t1);
+        y = fmaf(a.sc, q < 2 ? t0 : t1, y);
       }
-      if (q == 0) {
-        float* o = acc + (wave * a.T + s / a.k) * 16 + n;
-        *o = fmaf(a.rw[s], y, *o);
+      // (both slots may be of one token)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (q == 2 * t && mine >= 0) {
+          float* o = acc + (wave * a.T + mine / a.k) * 16 + n;
+          *o = fmaf(a.rw[mine], y, *o);
+        }
+        wave_fence();
       }
+      s = s1 >= 0 ? __builtin_amdgcn_readfirstlane(next[s1]) : -1;
     }
   }
   __syncthreads();
@@ -348,15 +426,16 @@ __global__ __launch_bounds__(512) void k_decode_down(DecodeArgs a) {
 // ---------------------------------------------------------------- host
 
 struct DecodePlan {
-  size_t h, next, lead, ua, ud, total;
+  size_t hs, h, next, lead, ua, ud, total;
 };
 static DecodePlan plan_decode(const Dims& d) {
   DecodePlan p;
   const size_t S = (size_t)d.Ms;
   p.next = 0;
   p.lead = round256(4 * S);
-  p.h = p.lead + round256(4 * S);
-  p.ua = p.h + round256(4 * S * d.I);
+  p.hs = p.lead + round256(4 * S);
+  p.h = p.hs + round256(4 * S * d.I);
+  p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
   p.total = p.ud + round256(4 * S * d.R);
   return p;
@@ -370,37 +449,19 @@ static int check_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, Dims*
   return KT_RAWINT4_OK;
 }
 
-constexpr size_t kLdsMost = 160 * 1024;
-
-static size_t gate_up_lds(int H, int P) {
-  const size_t its = (size_t)(H / 32 + 3) / 4;
-  return P * (its * 256 + kPadRow) + P * its * 16;
-}
-
-template <bool MX>
+template <bool MX, bool LORA>
 static void launch_decode(const DecodeArgs& a, hipStream_t st) {
-  if (a.R) {
+  if (LORA) {
     k_decode_lora_a<false><<<dim3((unsigned)((2 * a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  int P = a.T >= 4 ? 4 : a.T >= 2 ? 2 : 1;
-  while (P > 1 && gate_up_lds(a.H, P) + 8192 > kLdsMost) P /= 2;
-  const dim3 grid((unsigned)(a.I / 16), (unsigned)a.S);
-  const size_t lds = gate_up_lds(a.H, P);
-  if (P == 4)
-    k_decode_gate_up<MX, 4><<<grid, 256, lds, st>>>(a);
-  else if (P == 2)
-    k_decode_gate_up<MX, 2><<<grid, 256, lds, st>>>(a);
-  else
-    k_decode_gate_up<MX, 1><<<grid, 256, lds, st>>>(a);
+  k_decode_gate_up<MX, LORA><<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, 0, st>>>(a);
   note_launch();
-  if (a.R) {
+  if (LORA) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  const int kc = a.I < kDownK ? a.I : kDownK, gp = (kc / 32 + 3) / 4 * 4;
-  const size_t stage = 2 * (gp * 64 + kPadRow) + gp * 4;
-  k_decode_down<MX><<<(unsigned)(a.H / 16), 512, kDownWaves * (stage + (size_t)a.T * 64), st>>>(a);
+  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 512, (size_t)kDownWaves * a.T * 64, st>>>(a);
   note_launch();
 }
 
@@ -445,15 +506,17 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.ag = layer->gate_lora_a, a.bg = layer->gate_lora_b, a.au = layer->up_lora_a, a.bu = layer->up_lora_b;
   a.ad = layer->down_lora_a, a.bd = layer->down_lora_b;
   a.h = ws_ptr<float>(workspace, p.h);
+  a.hs = ws_ptr<uint16_t>(workspace, p.hs);
   a.next = ws_ptr<int32_t>(workspace, p.next);
   a.lead = ws_ptr<int32_t>(workspace, p.lead);
   a.ua = ws_ptr<float>(workspace, p.ua);
   a.ud = ws_ptr<float>(workspace, p.ud);
+  hipStream_t st = static_cast<hipStream_t>(stream);
   begin_launches();
   if (d.fmt == KT_RAWINT4_FORMAT_MXFP4)
-    launch_decode<true>(a, static_cast<hipStream_t>(stream));
+    d.R ? launch_decode<true, true>(a, st) : launch_decode<true, false>(a, st);
   else
-    launch_decode<false>(a, static_cast<hipStream_t>(stream));
+    d.R ? launch_decode<false, true>(a, st) : launch_decode<false, false>(a, st);
   return finish_launches();
 }
 
