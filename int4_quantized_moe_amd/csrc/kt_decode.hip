@@ -102,55 +102,86 @@ __device__ __forceinline__ u32x4 order8(u32x4 v) {
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// 256 contraction values (8 scale groups) of 16 weight rows, this lane's share: codes of groups q and 4 + q of row n,
-// and the row's 8 scales.  Bases are the same in all lanes, offsets (bytes) are the lane's.
+// Loads through a buffer descriptor: a base and an offset that are the same in
+// all lanes, and the lane's 32-bit offset.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void* p, size_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00020000);
+}
+__device__ __forceinline__ u32x4 buffer16(Buffer b, uint32_t lane, uint32_t base) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)base, 0));
+}
+
+// A contraction goes in units of 256 values (8 scale groups).  Every load is
+// issued, whatever the unit, so that how many are in flight behind a value is
+// known where it is waited for; those of a unit that reaches past the
+// contraction (of G groups) are moved to where they stay inside their matrix,
+// and what they bring is not used (`trim`).
+//
+// A unit of 16 weight rows, this lane's share: codes of groups q and 4 + q of row n, and the row's 8 scales.
 struct Codes {
   u32x4 c[2], s;
 };
-struct Row {
-  const uint8_t *w, *s;  // an expert's codes and scales
-  uint32_t wo, so;       // the lane's row; codes from group q on
+// Where a lane's share lies in an expert's matrix: codes from unit 0 on, those of a unit past the end, the
+// scales, and the last 16 bytes of scales.
+struct Place {
+  uint32_t w, end[2], s, last;
 };
-__device__ __forceinline__ Row row_of(const uint8_t* w, const uint16_t* s, size_t e, int rows, int row, int G, int q) {
-  return {w + e * rows * ((size_t)G * 16), reinterpret_cast<const uint8_t*>(s) + e * rows * ((size_t)G * 2),
-          (uint32_t)row * (uint32_t)(G * 16) + q * 16, (uint32_t)row * (uint32_t)(G * 2)};
+__device__ __forceinline__ Place place_of(int rows, int row, int G, int q) {
+  const uint32_t pitch = (uint32_t)G * 16, first = (uint32_t)row * pitch + q * 16, most = (uint32_t)rows * pitch - 16;
+  const uint32_t tail = first + (uint32_t)(G / 8) * 128;
+  return {first, {min(tail, most), min(tail + 64, most)}, (uint32_t)row * (uint32_t)G * 2, (uint32_t)rows * (uint32_t)G * 2 - 16};
 }
-__device__ __forceinline__ void load_codes(const Row& r, int u, Codes& c) {
-  const uint8_t* w = r.w + (size_t)u * 128;
-  c.c[0] = *reinterpret_cast<const u32x4*>(w + r.wo);
-  c.c[1] = *reinterpret_cast<const u32x4*>(w + 64 + r.wo);
-  c.s = *reinterpret_cast<const u32x4_u2*>(r.s + (size_t)u * 16 + r.so);
+struct Matrix {  // of one expert
+  Buffer w;
+  const uint8_t* s;
+};
+__device__ __forceinline__ Matrix matrix_of(const uint8_t* w, const uint16_t* s, size_t e, int rows, int G) {
+  const size_t n = (size_t)rows * G;
+  return {buffer_of(w + e * n * 16, n * 16), reinterpret_cast<const uint8_t*>(s + e * n)};
 }
-// the last unit of a row that ends inside it
-__device__ __forceinline__ void load_codes_end(const Row& r, int u, int G, int q, Codes& c) {
-  const uint8_t* w = r.w + (size_t)u * 128;
-  c.c[0] = c.c[1] = c.s = u32x4{0, 0, 0, 0};
-  if (8 * u + q < G) c.c[0] = *reinterpret_cast<const u32x4*>(w + r.wo);
-  if (8 * u + 4 + q < G) c.c[1] = *reinterpret_cast<const u32x4*>(w + 64 + r.wo);
-  const uint16_t* s = reinterpret_cast<const uint16_t*>(r.s + (size_t)u * 16 + r.so);
+__device__ __forceinline__ void load_codes(const Matrix& m, const Place& p, int u, bool past, Codes& c) {
+  c.c[0] = buffer16(m.w, past ? p.end[0] : p.w, past ? 0 : (uint32_t)u * 128);
+  c.c[1] = buffer16(m.w, past ? p.end[1] : p.w + 64, past ? 0 : (uint32_t)u * 128);
+  c.s = *reinterpret_cast<const u32x4_u2*>(m.s + min(p.s + (uint32_t)u * 16, p.last));
+}
+// scales of groups behind G are 0
+__device__ __forceinline__ void trim(const Place& p, int u, int G, Codes& c) {
+  const uint32_t at = p.s + (uint32_t)u * 16, d = at > p.last ? (at - p.last) / 2 : 0;  // scales that came before the unit's
+  uint32_t w[4] = {c.s.x, c.s.y, c.s.z, c.s.w};
 #pragma unroll
-  for (int g = 0; g < 8; ++g)
-    if (8 * u + g < G) c.s[g / 2] |= (uint32_t)s[g] << (16 * (g & 1));
+  for (int i = 0; i < 4; ++i) w[i] = d & 1 ? (w[i] >> 16 | (i < 3 ? w[i + 1] << 16 : 0)) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = d & 2 ? (i < 3 ? w[i + 1] : 0) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = d & 4 ? (i < 2 ? w[i + 2] : 0) : w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = 8 * u + 2 * i;
+    c.s[i] = g + 1 < G ? w[i] : g < G ? w[i] & 0xffffu : 0u;
+  }
 }
 
-// The vectors' share of the same values: of the lane's vector (n / 4) and group
-// n % 4 the 8 values from 8 q on.  `o`: where they start, in bytes.
+// The vectors' share of a unit: of the lane's vector (n / 4) and group n % 4 the 8 values from 8 q on.
 struct Vecs {
   u32x4 v[2];
 };
-__device__ __forceinline__ uint32_t vec_offset(uint32_t vec, int len, int n, int q) {
-  return (vec * (uint32_t)len + (n & 3) * 32 + q * 8) * 2;
+struct VecPlace {
+  uint32_t v, end[2];
+};
+__device__ __forceinline__ VecPlace vec_place(uint32_t vec, uint32_t vecs, int G, int n, int q) {
+  const uint32_t first = (vec * (uint32_t)G * 32 + (n & 3) * 32 + q * 8) * 2, most = vecs * (uint32_t)G * 64 - 16;
+  const uint32_t tail = first + (uint32_t)(G / 8) * 512;
+  return {first, {min(tail, most), min(tail + 256, most)}};
 }
-__device__ __forceinline__ void load_vecs(const uint16_t* v, uint32_t o, int u, Vecs& x) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(v) + (size_t)u * 512;
-  x.v[0] = *reinterpret_cast<const u32x4*>(p + o);
-  x.v[1] = *reinterpret_cast<const u32x4*>(p + 256 + o);
+__device__ __forceinline__ void load_vecs(Buffer b, const VecPlace& p, int u, bool past, Vecs& x) {
+  x.v[0] = buffer16(b, past ? p.end[0] : p.v, past ? 0 : (uint32_t)u * 512);
+  x.v[1] = buffer16(b, past ? p.end[1] : p.v + 256, past ? 0 : (uint32_t)u * 512);
 }
-__device__ __forceinline__ void load_vecs_end(const uint16_t* v, uint32_t o, int u, int G, int n, Vecs& x) {
-  const uint8_t* p = reinterpret_cast<const uint8_t*>(v) + (size_t)u * 512;
-  x.v[0] = x.v[1] = u32x4{0, 0, 0, 0};
-  if (8 * u + (n & 3) < G) x.v[0] = *reinterpret_cast<const u32x4*>(p + o);
-  if (8 * u + 4 + (n & 3) < G) x.v[1] = *reinterpret_cast<const u32x4*>(p + 256 + o);
+__device__ __forceinline__ void trim(int u, int G, int n, Vecs& x) {
+  const u32x4 zero = {0, 0, 0, 0};
+  if (8 * u + (n & 3) >= G) x.v[0] = zero;
+  if (8 * u + 4 + (n & 3) >= G) x.v[1] = zero;
 }
 
 // The MFMAs' initial sums for four groups of the vectors.
@@ -194,34 +225,27 @@ __global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
     a.lead[slot] = M > 0;
   }
   if (!M) return;
-  // (the last wave takes the end of rows that are no whole units)
-  const int G = a.H / 32, units = G / 8, per = (units + 3) / 4, kw = __builtin_amdgcn_readfirstlane(wave);
-  const int u0 = min(units, kw * per), u1 = min(units, u0 + per);
-  const Row rg = row_of(a.wg, a.sg, e, a.I, i0 + n, G, q), ru = row_of(a.wu, a.su, e, a.I, i0 + n, G, q);
+  const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, kw = __builtin_amdgcn_readfirstlane(wave);
+  const int u0 = kw * per;
+  const Matrix mg = matrix_of(a.wg, a.sg, e, a.I, G), mu = matrix_of(a.wu, a.su, e, a.I, G);
+  const Place at = place_of(a.I, i0 + n, G, q);
+  const Buffer xb = buffer_of(a.x, (size_t)a.T * a.H * 2);
   __syncthreads();
   for (int m0 = 0; m0 < M; m0 += kVecs) {
     const int nt = min(kVecs, M - m0);
-    const uint32_t xo = vec_offset(list[m0 + min(n >> 2, nt - 1)] / a.k, a.H, n, q);
+    const VecPlace xat = vec_place(list[m0 + min(n >> 2, nt - 1)] / a.k, a.T, G, n, q);
     float g = 0.f, u = 0.f;
-    auto use = [&](const Codes& cg, const Codes& cu, const Vecs& xv) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const u32x4 x = MX ? xv.v[i] : order8(xv.v[i]);
-        const floatx4 init = initial<MX>(x);
-        multiply<MX>(cg, i, x, init, g);
-        multiply<MX>(cu, i, x, init, u);
-      }
-    };
     Codes cg[2], cu[2];
     Vecs xv[2];
     auto load = [&](int v, int b) {
-      load_codes(rg, v, cg[b]);
-      load_codes(ru, v, cu[b]);
-      load_vecs(a.x, xo, v, xv[b]);
+      const bool past = 8 * v + 8 > G;
+      load_codes(mg, at, v, past, cg[b]);
+      load_codes(mu, at, v, past, cu[b]);
+      load_vecs(xb, xat, v, past, xv[b]);
+      asm volatile("" ::: "memory");  // (loads stay here, in this order)
     };
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-      if (u0 + b < u1) load(u0 + b, b);
+    load(u0, 0);
+    load(u0 + 1, 1);
     if (LORA) {
       // columns by gate and up by runs of the ranks
       const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
@@ -238,17 +262,25 @@ __global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
 #pragma unroll
       for (int p = 0; p < kVecs; ++p) lora[part][up][p][c] = t[p];
     }
-    for (int v = u0; v < u1; v += 2) {
-      use(cg[0], cu[0], xv[0]);
-      if (v + 2 < u1) load(v + 2, 0);
-      if (v + 1 < u1) use(cg[1], cu[1], xv[1]);
-      if (v + 3 < u1) load(v + 3, 1);
-    }
-    if (kw == 3 && G % 8) {
-      load_codes_end(rg, units, G, q, cg[0]);
-      load_codes_end(ru, units, G, q, cu[0]);
-      load_vecs_end(a.x, xo, units, G, n, xv[0]);
-      use(cg[0], cu[0], xv[0]);
+    for (int v = u0; v < u0 + per; v += 2) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (8 * (v + b) + 8 > G) {
+          trim(at, v + b, G, cg[b]);
+          trim(at, v + b, G, cu[b]);
+          trim(v + b, G, n, xv[b]);
+        }
+        if (v + b < u0 + per) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const u32x4 x = MX ? xv[b].v[i] : order8(xv[b].v[i]);
+            const floatx4 init = initial<MX>(x);
+            multiply<MX>(cg[b], i, x, init, g);
+            multiply<MX>(cu[b], i, x, init, u);
+          }
+        }
+        load(v + b + 2, b);
+      }
     }
     red[0][kw][q][n] = g;
     red[1][kw][q][n] = u;
@@ -338,7 +370,9 @@ __global__ __launch_bounds__(512, 4) void k_decode_down(DecodeArgs a) {
   __shared__ uint16_t order[KT_MOE_DECODE_MAX_SLOTS];
   __shared__ int16_t next[KT_MOE_DECODE_MAX_SLOTS];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int h0 = blockIdx.x * 16, G = a.I / 32, units = G / 8;
+  const int h0 = blockIdx.x * 16, G = a.I / 32, units = (G + 7) / 8;
+  const Place at = place_of(a.H, h0 + n, G, q);
+  const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 4);
   int U = 0;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
     const bool lead = s0 + lane < a.S && a.lead[s0 + lane];
@@ -354,36 +388,35 @@ __global__ __launch_bounds__(512, 4) void k_decode_down(DecodeArgs a) {
   for (int j = wave; j < U; j += kDownWaves) {
     const int first = __builtin_amdgcn_readfirstlane(order[j]);
     const size_t e = (size_t)a.ids[first];
-    const Row rd = row_of(a.wd, a.sd, e, a.H, h0 + n, G, q);
+    const Matrix md = matrix_of(a.wd, a.sd, e, a.H, G);
     for (int s = first; s >= 0;) {
       const int s1 = __builtin_amdgcn_readfirstlane(next[s]);
       // vectors: hi and lo of slot s, hi and lo of slot s1
-      const uint32_t ho = vec_offset(((n >> 3) && s1 >= 0 ? s1 : s) * 2 + (n >> 2 & 1), a.I, n, q);
+      const VecPlace hat = vec_place(((n >> 3) && s1 >= 0 ? s1 : s) * 2 + (n >> 2 & 1), 2 * a.S, G, n, q);
       Codes cd[kDownDepth];
       Vecs hv[kDownDepth];
       float y = 0.f;
-      auto use = [&](const Codes& c, const Vecs& v) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) multiply<MX>(c, i, v.v[i], initial<MX>(v.v[i]), y);
-      };
       auto load = [&](int u, int b) {
-        load_codes(rd, u, cd[b]);
-        load_vecs(a.hs, ho, u, hv[b]);
+        const bool past = 8 * u + 8 > G;
+        load_codes(md, at, u, past, cd[b]);
+        load_vecs(hb, hat, u, past, hv[b]);
+        asm volatile("" ::: "memory");
       };
 #pragma unroll
-      for (int b = 0; b < kDownDepth; ++b)
-        if (b < units) load(b, b);
+      for (int b = 0; b < kDownDepth; ++b) load(b, b);
       for (int u = 0; u < units; u += kDownDepth) {
 #pragma unroll
         for (int b = 0; b < kDownDepth; ++b) {
-          if (u + b < units) use(cd[b], hv[b]);
-          if (u + b + kDownDepth < units) load(u + b + kDownDepth, b);
+          if (8 * (u + b) + 8 > G) {
+            trim(at, u + b, G, cd[b]);
+            trim(u + b, G, n, hv[b]);
+          }
+          if (u + b < units) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) multiply<MX>(cd[b], i, hv[b].v[i], initial<MX>(hv[b].v[i]), y);
+          }
+          load(u + b + kDownDepth, b);
         }
-      }
-      if (G % 8) {
-        load_codes_end(rd, units, G, q, cd[0]);
-        load_vecs_end(a.hs, ho, units, G, n, hv[0]);
-        use(cd[0], hv[0]);
       }
       // hi + lo: rows of lanes 0 and 1 have slot s, 2 and 3 slot s1
       uint32_t y0 = __float_as_uint(y), y1 = y0;
