@@ -2,29 +2,25 @@
 // down with the weighted sum over the slots in another, two small ones more with LoRA.
 //
 // With few tokens an expert has one or two of them, and the time is that of
-// reading its packed rows once.  Weights go into the MFMAs as bf16, one MFMA
-// (32 contraction values) per 16 weight rows and scale group, so that the
-// scale multiplies the group's sum in fp32.
+// reading its packed rows once.  So the loads decide the layout: eight lanes
+// take 128 bytes of a row in a row, eight rows a load, and a lane's 16 bytes are
+// one scale group, which it multiplies by itself:
 //   RAWINT4: a code c becomes 1 + c / 16, by a shift and an and-or for two of
 //   them, exact in bf16, and
-//     sum (c - 8) x = 16 (sum (1 + c / 16) x - 3/2 sum x),
-//   where -3/2 sum x of the group is the MFMA's initial sum (an MFMA of x with
-//   -3/2).  Products are exact, whatever the inputs' and scales' size.
-//   MXFP4: a code is converted to bf16 as it is, the initial sum is 0.
-// Inputs are bf16 as given; h, fp32, enters as two bf16 (hi and lo), 2^-16 of
-// it left out.
+//     sum (c - 8) x = 16 (sum (1 + c / 16) x - 3/2 sum x)
+//   by dot products of two with fp32 sums that start from -3/2 sum x of the group.
+//   MXFP4: a code is converted to bf16 as it is, the sum starts from 0.
+// The scale then multiplies the group's sum in fp32.  Products are exact,
+// whatever the inputs' and scales' size.  Inputs are bf16 as given; h, fp32,
+// enters as two bf16 (hi and lo), 2^-16 of it left out.
 //
-// The other operand's 16 rows are four vectors (tokens, or hi and lo of two)
-// by four scale groups: 16 bytes a lane bring 128 contraction values of all
-// four, and of the MFMA with group j's weights the rows of group j are
-// taken, register j of every lane.  So x and h need no staging: they come from
-// the caches in the same stream of loads as the codes, and no workgroup
-// waits for another's.  A lane loads 16 bytes of a weight row, a whole scale
-// group; an exchange of 4 x 4 dwords between the wave's four rows of 16 lanes
-// gives each MFMA one group.
+// (The MFMAs' operand layout has another row in every lane of 16: their loads
+// touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
 #include "kt_step_common.hpp"
 
 #include <math.h>
+
+#include <type_traits>
 
 namespace kt {
 
@@ -41,13 +37,12 @@ struct DecodeArgs {
   const float *ag, *bg, *au, *bu, *ad, *bd;
   float* h;       // [S][I], with LoRA
   uint16_t* hs;   // [S][2][I]: h as bf16 hi and lo, in the codes' order
+  float* hsum;    // [S][I / 16]: sums of 16 values of h
   int32_t* next;  // [S]: the next slot of the same expert, -1 for none
   int32_t* lead;  // [S]: whether the slot is its expert's first
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
   float* ud;      // [S][R]: h A_d^T
 };
-
-typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
 
 // The slots of slot `s`'s expert e from s on, in order, to list[] (wave 0
 // writes; every wave finds the same number); 0 if another slot comes before.
@@ -69,14 +64,6 @@ __device__ __forceinline__ int slots_of(const DecodeArgs& a, int s, int64_t e, u
     if (next < 0 && (rest & ~own)) next = s0 + __ffsll((unsigned long long)(rest & ~own)) - 1;
   }
   return led ? 0 : n;
-}
-
-// Registers r[0..3] of a lane in row q hold the 16 bytes (dwords 0..3) of group q; afterwards r[i] is dword q of group i.
-__device__ __forceinline__ void transpose4(uint32_t* r) {
-  swap32(r[0], r[2]);
-  swap32(r[1], r[3]);
-  swap16(r[0], r[1]);
-  swap16(r[2], r[3]);
 }
 
 // 8 codes of a dword as bf16: RAWINT4 1 + c / 16 in the order k0 k4 k1 k5 k2 k6 k3 k7, MXFP4 their values in order.
@@ -101,6 +88,9 @@ __device__ __forceinline__ u32x4 order8(u32x4 v) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a), __builtin_bit_cast(bf16x2_t, b), c, false);
+}
 
 // Loads through a buffer descriptor: a base and an offset that are the same in
 // all lanes, and the lane's 32-bit offset.
@@ -108,115 +98,73 @@ typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer_of(const void* p, size_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00020000);
 }
-__device__ __forceinline__ u32x4 buffer16(Buffer b, uint32_t lane, uint32_t base) {
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)base, 0));
-}
 
-// A contraction goes in units of 256 values (8 scale groups).  Every load is
-// issued, whatever the unit, so that how many are in flight behind a value is
-// known where it is waited for; those of a unit that reaches past the
-// contraction (of G groups) are moved to where they stay inside their matrix,
-// and what they bring is not used (`trim`).
-//
-// A unit of 16 weight rows, this lane's share: codes of groups q and 4 + q of row n, and the row's 8 scales.
-struct Codes {
-  u32x4 c[2], s;
-};
-// Where a lane's share lies in an expert's matrix: codes from unit 0 on, those of a unit past the end, the
-// scales, and the last 16 bytes of scales.
-struct Place {
-  uint32_t w, end[2], s, last;
-};
-__device__ __forceinline__ Place place_of(int rows, int row, int G, int q) {
-  const uint32_t pitch = (uint32_t)G * 16, first = (uint32_t)row * pitch + q * 16, most = (uint32_t)rows * pitch - 16;
-  const uint32_t tail = first + (uint32_t)(G / 8) * 128;
-  return {first, {min(tail, most), min(tail + 64, most)}, (uint32_t)row * (uint32_t)G * 2, (uint32_t)rows * (uint32_t)G * 2 - 16};
-}
-struct Matrix {  // of one expert
-  Buffer w;
-  const uint8_t* s;
+// One expert's matrix of so many rows, G scale groups each.
+struct Matrix {
+  Buffer w, s;
 };
 __device__ __forceinline__ Matrix matrix_of(const uint8_t* w, const uint16_t* s, size_t e, int rows, int G) {
   const size_t n = (size_t)rows * G;
-  return {buffer_of(w + e * n * 16, n * 16), reinterpret_cast<const uint8_t*>(s + e * n)};
-}
-__device__ __forceinline__ void load_codes(const Matrix& m, const Place& p, int u, bool past, Codes& c) {
-  c.c[0] = buffer16(m.w, past ? p.end[0] : p.w, past ? 0 : (uint32_t)u * 128);
-  c.c[1] = buffer16(m.w, past ? p.end[1] : p.w + 64, past ? 0 : (uint32_t)u * 128);
-  c.s = *reinterpret_cast<const u32x4_u2*>(m.s + min(p.s + (uint32_t)u * 16, p.last));
-}
-// scales of groups behind G are 0
-__device__ __forceinline__ void trim(const Place& p, int u, int G, Codes& c) {
-  const uint32_t at = p.s + (uint32_t)u * 16, d = at > p.last ? (at - p.last) / 2 : 0;  // scales that came before the unit's
-  uint32_t w[4] = {c.s.x, c.s.y, c.s.z, c.s.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = d & 1 ? (w[i] >> 16 | (i < 3 ? w[i + 1] << 16 : 0)) : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = d & 2 ? (i < 3 ? w[i + 1] : 0) : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = d & 4 ? (i < 2 ? w[i + 2] : 0) : w[i];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int g = 8 * u + 2 * i;
-    c.s[i] = g + 1 < G ? w[i] : g < G ? w[i] & 0xffffu : 0u;
-  }
+  return {buffer_of(w + e * n * 16, n * 16), buffer_of(s + e * n, n * 2)};
 }
 
-// The vectors' share of a unit: of the lane's vector (n / 4) and group n % 4 the 8 values from 8 q on.
-struct Vecs {
-  u32x4 v[2];
+// A contraction goes in units of 256 values, 8 groups, one for each of a row's
+// eight lanes.  Codes and scale of this lane's group in rows r .. r + 7 (a tile).
+// Every load is issued, whatever the unit, so that how many are in flight
+// behind a value is known where it is waited for; a lane whose group lies behind the
+// row's last reads that one, and its vectors are 0.
+struct Codes {
+  u32x4 c;
+  uint16_t s;
 };
-struct VecPlace {
-  uint32_t v, end[2];
+__device__ __forceinline__ void load_codes(const Matrix& m, uint32_t group, uint32_t base, Codes& c) {
+  c.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(m.w, (int)(group * 16), (int)(base * 16), 0));
+  c.s = __builtin_amdgcn_raw_buffer_load_b16(m.s, (int)(group * 2), (int)(base * 2), 0);
+}
+
+// Vectors in LDS: four planes of 16 bytes a group, so that eight lanes read 128 bytes in a row.
+struct Vec {
+  u32x4 v[4];
 };
-__device__ __forceinline__ VecPlace vec_place(uint32_t vec, uint32_t vecs, int G, int n, int q) {
-  const uint32_t first = (vec * (uint32_t)G * 32 + (n & 3) * 32 + q * 8) * 2, most = vecs * (uint32_t)G * 64 - 16;
-  const uint32_t tail = first + (uint32_t)(G / 8) * 512;
-  return {first, {min(tail, most), min(tail + 256, most)}};
-}
-__device__ __forceinline__ void load_vecs(Buffer b, const VecPlace& p, int u, bool past, Vecs& x) {
-  x.v[0] = buffer16(b, past ? p.end[0] : p.v, past ? 0 : (uint32_t)u * 512);
-  x.v[1] = buffer16(b, past ? p.end[1] : p.v + 256, past ? 0 : (uint32_t)u * 512);
-}
-__device__ __forceinline__ void trim(int u, int G, int n, Vecs& x) {
-  const u32x4 zero = {0, 0, 0, 0};
-  if (8 * u + (n & 3) >= G) x.v[0] = zero;
-  if (8 * u + 4 + (n & 3) >= G) x.v[1] = zero;
+__device__ __forceinline__ void read_vec(const uint8_t* p, int group, int plane, Vec& v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v.v[j] = *reinterpret_cast<const u32x4*>(p + j * plane + group * 16);
 }
 
-// The MFMAs' initial sums for four groups of the vectors.
-template <bool MX>
-__device__ __forceinline__ floatx4 initial(const u32x4& x) {
-  const floatx4 zero = {0.f, 0.f, 0.f, 0.f};
-  return MX ? zero : mfma_bf16(x, u32x4{0xbfc0bfc0u, 0xbfc0bfc0u, 0xbfc0bfc0u, 0xbfc0bfc0u}, zero);
-}
-
-// Adds half i of the codes' values times the vectors to this lane's sum (weight row n, vector q).
-template <bool MX>
-__device__ __forceinline__ void multiply(const Codes& c, int i, const u32x4& x, const floatx4& init, float& acc) {
-  uint32_t r[4] = {c.c[i].x, c.c[i].y, c.c[i].z, c.c[i].w};
-  transpose4(r);
+// The group's product with V vectors, from the sums t[] on.
+template <bool MX, int V>
+__device__ __forceinline__ void multiply(const u32x4& c, const Vec* x, float* t) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t s = c.s[2 * i + j / 2];
-    acc = fmaf(j & 1 ? bf_hi(s) : bf_lo(s), mfma_bf16(x, codes_bf16<MX>(r[j]), init)[j], acc);
+    const u32x4 w = codes_bf16<MX>(c[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) t[v] = dot2(w[i], x[v].v[j][i], t[v]);
   }
-  __builtin_amdgcn_sched_barrier(0);  // (more MFMAs side by side take registers from the loads ahead)
 }
 
-constexpr int kVecs = 4;      // tokens that gate and up take at a time
+// A sum over the eight lanes of a row, in all of them.
+__device__ __forceinline__ float eight_sum(float v) {
+  v += dpp_f<0xB1>(v);
+  v += dpp_f<0x4E>(v);
+  return v + dpp_f<0x141>(v);
+}
+
 constexpr int kLoraParts = 8;  // runs of the ranks
+constexpr int kUpDepth = 2;    // units of loads ahead, gate and up
 
 // Gate and up.  A workgroup has 16 columns of I of one expert (its first
-// slot's block; the others leave at once) for all of its tokens, four at a time.
-// Its four waves split the contraction.
-template <bool MX, bool LORA>
-__global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
+// slot's block; the others leave at once) for all of its tokens, V at a time,
+// which lie in LDS.  Its four waves split the contraction.
+template <bool MX, bool LORA, int V>
+__global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
-  __shared__ float red[2][4][kVecs][16];
-  __shared__ float lora[LORA ? kLoraParts : 1][2][kVecs][16];
+  __shared__ float red[2][4][V][16];
+  __shared__ float lora[LORA ? kLoraParts : 1][2][V][16];
   const int slot = blockIdx.y, i0 = blockIdx.x * 16;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
+  const int kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t e = a.ids[slot];
   int next = -1, M = 0;
   if (e >= 0 && e < a.E) M = slots_of(a, slot, e, list, next);
@@ -225,65 +173,91 @@ __global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
     a.lead[slot] = M > 0;
   }
   if (!M) return;
-  const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, kw = __builtin_amdgcn_readfirstlane(wave);
-  const int u0 = kw * per;
+  const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, u0 = kw * per;
+  const int Gp = per * 32, plane = Gp * 16;      // groups and bytes of a plane in LDS, 0 behind the row's end
+  float* sums = reinterpret_cast<float*>(lds + V * 4 * plane);  // [vectors][Gp]: -3/2 of a group's sum
   const Matrix mg = matrix_of(a.wg, a.sg, e, a.I, G), mu = matrix_of(a.wu, a.su, e, a.I, G);
-  const Place at = place_of(a.I, i0 + n, G, q);
-  const Buffer xb = buffer_of(a.x, (size_t)a.T * a.H * 2);
+  const int c8 = lane & 7, row = lane >> 3;
+  const uint32_t first = (uint32_t)(i0 + row) * G, rows8 = 8u * G;
   __syncthreads();
-  for (int m0 = 0; m0 < M; m0 += kVecs) {
-    const int nt = min(kVecs, M - m0);
-    const VecPlace xat = vec_place(list[m0 + min(n >> 2, nt - 1)] / a.k, a.T, G, n, q);
-    float g = 0.f, u = 0.f;
-    Codes cg[2], cu[2];
-    Vecs xv[2];
-    auto load = [&](int v, int b) {
-      const bool past = 8 * v + 8 > G;
-      load_codes(mg, at, v, past, cg[b]);
-      load_codes(mu, at, v, past, cu[b]);
-      load_vecs(xb, xat, v, past, xv[b]);
-      asm volatile("" ::: "memory");  // (loads stay here, in this order)
+  for (int m0 = 0; m0 < M; m0 += V) {
+    const int nt = min(V, M - m0);
+    Codes cd[kUpDepth][4];  // gate rows 0..7, 8..15, up rows 0..7, 8..15
+    auto load = [&](int u, int b) {
+      const uint32_t g = first + min(8 * u + c8, G - 1);
+      load_codes(mg, g, 0, cd[b][0]);
+      load_codes(mg, g, rows8, cd[b][1]);
+      load_codes(mu, g, 0, cd[b][2]);
+      load_codes(mu, g, rows8, cd[b][3]);
+      __builtin_amdgcn_sched_barrier(0);  // (units' loads stay in order)
     };
-    load(u0, 0);
-    load(u0 + 1, 1);
+#pragma unroll
+    for (int b = 0; b < kUpDepth; ++b) load(u0 + b, b);
+    for (int p = 0; p < nt; ++p) {
+      const uint16_t* x = a.x + (size_t)(list[m0 + p] / a.k) * a.H;
+      for (int c = threadIdx.x; c < Gp * 4; c += 256) {
+        u32x4 v = {0, 0, 0, 0};
+        if (c < G * 4) v = *reinterpret_cast<const u32x4*>(x + c * 8);
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s += bf_lo(v[j]) + bf_hi(v[j]);
+        s += dpp_f<0xB1>(s);
+        s += dpp_f<0x4E>(s);
+        *reinterpret_cast<u32x4*>(lds + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = MX ? v : order8(v);
+        if ((c & 3) == 0) sums[p * Gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
+      }
+    }
     if (LORA) {
       // columns by gate and up by runs of the ranks
       const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
       const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
       const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
-      float t[kVecs] = {0.f, 0.f, 0.f, 0.f};
+      float t[V] = {};
 #pragma unroll 1
       for (int r = r0; r < r1; ++r) {
         const float w = b[r];
 #pragma unroll
-        for (int p = 0; p < kVecs; ++p)
+        for (int p = 0; p < V; ++p)
           if (p < nt) t[p] = fmaf(w, a.ua[(size_t)list[m0 + p] * 2 * a.R + up * a.R + r], t[p]);
       }
 #pragma unroll
-      for (int p = 0; p < kVecs; ++p) lora[part][up][p][c] = t[p];
+      for (int p = 0; p < V; ++p) lora[part][up][p][c] = t[p];
     }
-    for (int v = u0; v < u0 + per; v += 2) {
+    __syncthreads();
+    float acc[4][V] = {};
+    for (int v = 0; v < per; v += kUpDepth) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (8 * (v + b) + 8 > G) {
-          trim(at, v + b, G, cg[b]);
-          trim(at, v + b, G, cu[b]);
-          trim(v + b, G, n, xv[b]);
-        }
-        if (v + b < u0 + per) {
+      for (int b = 0; b < kUpDepth; ++b) {
+        if (v + b < per) {
+          const int g = 8 * (u0 + v + b) + c8;
+          Vec x[V];
+          float sum[V];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const u32x4 x = MX ? xv[b].v[i] : order8(xv[b].v[i]);
-            const floatx4 init = initial<MX>(x);
-            multiply<MX>(cg[b], i, x, init, g);
-            multiply<MX>(cu[b], i, x, init, u);
+          for (int p = 0; p < V; ++p) {
+            read_vec(lds + p * 4 * plane, g, plane, x[p]);
+            sum[p] = sums[p * Gp + g];
+          }
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float d[V];
+#pragma unroll
+            for (int p = 0; p < V; ++p) d[p] = sum[p];
+            multiply<MX, V>(cd[b][t].c, x, d);
+#pragma unroll
+            for (int p = 0; p < V; ++p) acc[t][p] = fmaf(bf16_to_float(cd[b][t].s), d[p], acc[t][p]);
+            __builtin_amdgcn_sched_barrier(0);  // (decoded tiles side by side take registers from the loads ahead)
           }
         }
-        load(v + b + 2, b);
+        load(u0 + v + b + kUpDepth, b);
       }
     }
-    red[0][kw][q][n] = g;
-    red[1][kw][q][n] = u;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int p = 0; p < V; ++p) {
+        const float v = eight_sum(acc[t][p]);
+        if (c8 == 0) red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
+      }
     __syncthreads();
     if (threadIdx.x < 16 * nt) {
       const int p = threadIdx.x >> 4, c = threadIdx.x & 15;
@@ -308,12 +282,15 @@ __global__ __launch_bounds__(256, 3) void k_decode_gate_up(DecodeArgs a) {
       uint16_t* o = a.hs + (size_t)s * 2 * a.I + i0 + (MX ? c : perm_pos(c));
       o[0] = hi;
       o[a.I] = lo;
+      const float sum = row16_sum(bf16_to_float(hi) + bf16_to_float(lo));
+      if (c == 0) a.hsum[(size_t)s * (a.I / 16) + blockIdx.x] = sum;
       if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
     }
-    if (m0 + kVecs < M) __syncthreads();
+    if (m0 + V < M) __syncthreads();
   }
 }
 
+constexpr int kVecs = 4;  // tokens that a row of A takes at a time
 // x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens, four at a time.
 template <bool DOWN>
 __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
@@ -358,98 +335,121 @@ __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   }
 }
 
-constexpr int kDownWaves = 8;
-constexpr int kDownDepth = 3;  // units of loads ahead
+
+constexpr int kDownWaves = 4;
+constexpr int kDownDepth = 4;  // units of loads ahead
+constexpr int kDownK = 64;     // groups of h in LDS at a time
 
 // Down and the sum over the slots.  A workgroup has 16 columns of H; its waves
-// take the experts in turn (a wave per expert, the whole contraction), two tokens at a
-// time, and add to sums of their own per token, which the end joins in the waves' order.
+// take the experts in turn (a wave per expert, the whole contraction), a slot at a
+// time with its h in LDS, and add to sums of their own per token, which the end
+// joins in the waves' order.
 template <bool MX, bool LORA>
-__global__ __launch_bounds__(512, 4) void k_decode_down(DecodeArgs a) {
-  extern __shared__ __align__(16) float acc[];  // [waves][T][16]
-  __shared__ uint16_t order[KT_MOE_DECODE_MAX_SLOTS];
+__global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint16_t order[KT_MOE_DECODE_MAX_SLOTS], expert[KT_MOE_DECODE_MAX_SLOTS];
   __shared__ int16_t next[KT_MOE_DECODE_MAX_SLOTS];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, q = lane >> 4;
-  const int h0 = blockIdx.x * 16, G = a.I / 32, units = (G + 7) / 8;
-  const Place at = place_of(a.H, h0 + n, G, q);
-  const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 4);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
+  const int h0 = blockIdx.x * 16, G = a.I / 32;
+  constexpr int plane = kDownK * 16;
+  uint8_t* hl = lds + wave * (8 * plane + kDownK * 4);  // hi's four planes, lo's four, -3/2 of the groups' sums
+  float* sums = reinterpret_cast<float*>(hl + 8 * plane);
+  float* acc = reinterpret_cast<float*>(lds + kDownWaves * (8 * plane + kDownK * 4));  // [waves][T][16]
   int U = 0;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
-    const bool lead = s0 + lane < a.S && a.lead[s0 + lane];
+    const int s = s0 + lane;
+    const bool lead = s < a.S && a.lead[s];
     const uint64_t mask = __ballot(lead);
     if (wave == 0) {
-      if (s0 + lane < a.S) next[s0 + lane] = (int16_t)a.next[s0 + lane];
-      if (lead) order[U + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
+      if (s < a.S) next[s] = (int16_t)a.next[s];
+      if (lead) {
+        const int at = U + __popcll(mask & ((1ull << lane) - 1));
+        order[at] = (uint16_t)s;
+        expert[at] = (uint16_t)a.ids[s];
+      }
     }
     U += __popcll(mask);
   }
-  for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 512) acc[i] = 0.f;
+  for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 64 * kDownWaves) acc[i] = 0.f;
   __syncthreads();
+  const uint32_t first = (uint32_t)(h0 + row) * G, rows8 = 8u * G;
   for (int j = wave; j < U; j += kDownWaves) {
-    const int first = __builtin_amdgcn_readfirstlane(order[j]);
-    const size_t e = (size_t)a.ids[first];
+    const size_t e = __builtin_amdgcn_readfirstlane(expert[j]);
     const Matrix md = matrix_of(a.wd, a.sd, e, a.H, G);
-    for (int s = first; s >= 0;) {
-      const int s1 = __builtin_amdgcn_readfirstlane(next[s]);
-      // vectors: hi and lo of slot s, hi and lo of slot s1
-      const VecPlace hat = vec_place(((n >> 3) && s1 >= 0 ? s1 : s) * 2 + (n >> 2 & 1), 2 * a.S, G, n, q);
-      Codes cd[kDownDepth];
-      Vecs hv[kDownDepth];
-      float y = 0.f;
-      auto load = [&](int u, int b) {
-        const bool past = 8 * u + 8 > G;
-        load_codes(md, at, u, past, cd[b]);
-        load_vecs(hb, hat, u, past, hv[b]);
-        asm volatile("" ::: "memory");
-      };
+    for (int s = __builtin_amdgcn_readfirstlane(order[j]); s >= 0; s = __builtin_amdgcn_readfirstlane(next[s])) {
+      float y[2] = {0.f, 0.f};
+      for (int k0 = 0; k0 < G; k0 += kDownK) {
+        const int len = min(kDownK, G - k0), units = (len + 7) / 8;
+        Codes cd[kDownDepth][2];
+        auto load = [&](int u, int b) {
+          const uint32_t g = first + min(k0 + 8 * u + c8, G - 1);
+          load_codes(md, g, 0, cd[b][0]);
+          load_codes(md, g, rows8, cd[b][1]);
+          __builtin_amdgcn_sched_barrier(0);
+        };
 #pragma unroll
-      for (int b = 0; b < kDownDepth; ++b) load(b, b);
-      for (int u = 0; u < units; u += kDownDepth) {
+        for (int b = 0; b < kDownDepth; ++b) load(b, b);
+        wave_fence();
+        // (16 bytes of hi or lo: a quarter of a group)
+        for (int c = lane; c < units * 32; c += 64) {
 #pragma unroll
-        for (int b = 0; b < kDownDepth; ++b) {
-          if (8 * (u + b) + 8 > G) {
-            trim(at, u + b, G, cd[b]);
-            trim(u + b, G, n, hv[b]);
+          for (int p = 0; p < 2; ++p) {
+            u32x4 v = {0, 0, 0, 0};
+            if (c < len * 4) v = *reinterpret_cast<const u32x4*>(a.hs + ((size_t)s * 2 + p) * a.I + k0 * 32 + c * 8);
+            *reinterpret_cast<u32x4*>(hl + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = v;
           }
-          if (u + b < units) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) multiply<MX>(cd[b], i, hv[b].v[i], initial<MX>(hv[b].v[i]), y);
+        }
+        if (lane < units * 8) {
+          float t = 0.f;
+          if (!MX && lane < len) {
+            const float* p = a.hsum + (size_t)s * (a.I / 16) + (k0 + lane) * 2;
+            t = -1.5f * (p[0] + p[1]);
           }
-          load(u + b + kDownDepth, b);
-        }
-      }
-      // hi + lo: rows of lanes 0 and 1 have slot s, 2 and 3 slot s1
-      uint32_t y0 = __float_as_uint(y), y1 = y0;
-      swap16(y0, y1);
-      y = __uint_as_float(y0) + __uint_as_float(y1);
-      if (!MX) y *= 16.f;
-      const int mine = q < 2 ? s : s1;
-      if (LORA) {
-        // a quarter of the ranks a row of lanes
-        const float* b = a.bd + (e * a.H + h0 + n) * a.R;
-        float t0 = 0.f, t1 = 0.f;
-#pragma unroll 1
-        for (int r = q; r < a.R; r += 4) {
-          t0 = fmaf(b[r], a.ud[(size_t)s * a.R + r], t0);
-          if (s1 >= 0) t1 = fmaf(b[r], a.ud[(size_t)s1 * a.R + r], t1);
-        }
-        t0 = rows_sum(t0), t1 = rows_sum(t1);
-        y = fmaf(a.sc, q < 2 ? t0 : t1, y);
-      }
-      // (both slots may be of one token)
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (q == 2 * t && mine >= 0) {
-          float* o = acc + (wave * a.T + mine / a.k) * 16 + n;
-          *o = fmaf(a.rw[mine], y, *o);
+          sums[lane] = t;
         }
         wave_fence();
+        for (int u = 0; u < units; u += kDownDepth) {
+#pragma unroll
+          for (int b = 0; b < kDownDepth; ++b) {
+            if (u + b < units) {
+              const int g = 8 * (u + b) + c8;
+              Vec x[2];
+              read_vec(hl, g, plane, x[0]);
+              read_vec(hl + 4 * plane, g, plane, x[1]);
+              const float sum = sums[g];
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                float d[2] = {sum, 0.f};
+                multiply<MX, 2>(cd[b][t].c, x, d);
+                y[t] = fmaf(bf16_to_float(cd[b][t].s), d[0] + d[1], y[t]);
+              }
+            }
+            load(u + b + kDownDepth, b);
+          }
+        }
       }
-      s = s1 >= 0 ? __builtin_amdgcn_readfirstlane(next[s1]) : -1;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        y[t] = eight_sum(y[t]);
+        if (!MX) y[t] *= 16.f;
+        if (LORA) {
+          // an eighth of the ranks a lane
+          const float *b = a.bd + (e * a.H + h0 + 8 * t + row) * a.R, *u = a.ud + (size_t)s * a.R;
+          float l = 0.f;
+#pragma unroll 1
+          for (int r = c8; r < a.R; r += 8) l = fmaf(b[r], u[r], l);
+          y[t] = fmaf(a.sc, eight_sum(l), y[t]);
+        }
+      }
+      if (c8 == 0) {
+        float* o = acc + (wave * a.T + s / a.k) * 16 + row;
+        o[0] = fmaf(a.rw[s], y[0], o[0]);
+        o[8] = fmaf(a.rw[s], y[1], o[8]);
+      }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.T * 16; i += 512) {
+  for (int i = threadIdx.x; i < a.T * 16; i += 64 * kDownWaves) {
     float v = 0.f;
     for (int w = 0; w < kDownWaves; ++w) v += acc[w * a.T * 16 + i];
     a.out[(size_t)(i >> 4) * a.H + h0 + (i & 15)] = float_to_bf16(v);
@@ -459,7 +459,7 @@ __global__ __launch_bounds__(512, 4) void k_decode_down(DecodeArgs a) {
 // ---------------------------------------------------------------- host
 
 struct DecodePlan {
-  size_t hs, h, next, lead, ua, ud, total;
+  size_t hs, hsum, h, next, lead, ua, ud, total;
 };
 static DecodePlan plan_decode(const Dims& d) {
   DecodePlan p;
@@ -467,7 +467,8 @@ static DecodePlan plan_decode(const Dims& d) {
   p.next = 0;
   p.lead = round256(4 * S);
   p.hs = p.lead + round256(4 * S);
-  p.h = p.hs + round256(4 * S * d.I);
+  p.hsum = p.hs + round256(4 * S * d.I);
+  p.h = p.hsum + round256(4 * S * (d.I / 16));
   p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
   p.total = p.ud + round256(4 * S * d.R);
@@ -488,13 +489,18 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     k_decode_lora_a<false><<<dim3((unsigned)((2 * a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  k_decode_gate_up<MX, LORA><<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, 0, st>>>(a);
+  const size_t groups = (size_t)((a.H / 32 + 7) / 8 + 3) / 4 * 32;
+  const dim3 grid((unsigned)(a.I / 16), (unsigned)a.S);
+  if (a.T == 1)
+    k_decode_gate_up<MX, LORA, 1><<<grid, 256, groups * 68, st>>>(a);
+  else
+    k_decode_gate_up<MX, LORA, 2><<<grid, 256, 2 * groups * 68, st>>>(a);
   note_launch();
   if (LORA) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 512, (size_t)kDownWaves * a.T * 64, st>>>(a);
+  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 64 * kDownWaves, kDownWaves * (kDownK * 132 + (size_t)a.T * 64), st>>>(a);
   note_launch();
 }
 
@@ -540,6 +546,7 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.ad = layer->down_lora_a, a.bd = layer->down_lora_b;
   a.h = ws_ptr<float>(workspace, p.h);
   a.hs = ws_ptr<uint16_t>(workspace, p.hs);
+  a.hsum = ws_ptr<float>(workspace, p.hsum);
   a.next = ws_ptr<int32_t>(workspace, p.next);
   a.lead = ws_ptr<int32_t>(workspace, p.lead);
   a.ua = ws_ptr<float>(workspace, p.ua);
