@@ -11,8 +11,9 @@
 //   by dot products of two with fp32 sums that start from -3/2 sum x of the group.
 //   MXFP4: a code is converted to bf16 as it is, the sum starts from 0.
 // The scale then multiplies the group's sum in fp32.  Products are exact,
-// whatever the inputs' and scales' size.  Inputs are bf16 as given; h, fp32,
-// enters as two bf16 (hi and lo), 2^-16 of it left out.
+// whatever the inputs' and scales' size.  Inputs are bf16 as given; h enters
+// down in fp16 with a power of two for 16 columns, rounded by at most 2^-11 of
+// itself (2e-4 of the output, whose own rounding to bf16 is 1.7e-3).
 //
 // (The MFMAs' operand layout has another row in every lane of 16: their loads
 // touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
@@ -23,6 +24,8 @@
 #include <type_traits>
 
 namespace kt {
+
+typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
 
 struct DecodeArgs {
   int S, k, T;  // slots, slots a token, tokens
@@ -36,8 +39,8 @@ struct DecodeArgs {
   const uint16_t *sg, *su, *sd;
   const float *ag, *bg, *au, *bu, *ad, *bd;
   float* h;       // [S][I], with LoRA
-  uint16_t* hs;   // [S][2][I]: h as bf16 hi and lo, in the codes' order
-  float* hsum;    // [S][I / 16]: sums of 16 values of h
+  uint16_t* hs;   // [S][I]: h in fp16 times a power of two, in the codes' order
+  float2_t* hsf;  // [S][I / 16]: -3/2 of the sum of 16 of them, and what their products with the codes are to be multiplied by
   int32_t* next;  // [S]: the next slot of the same expert, -1 for none
   int32_t* lead;  // [S]: whether the slot is its expert's first
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
@@ -66,21 +69,36 @@ __device__ __forceinline__ int slots_of(const DecodeArgs& a, int s, int64_t e, u
   return led ? 0 : n;
 }
 
-// 8 codes of a dword as bf16: RAWINT4 1 + c / 16 in the order k0 k4 k1 k5 k2 k6 k3 k7, MXFP4 their values in order.
-template <bool MX>
-__device__ __forceinline__ u32x4 codes_bf16(uint32_t w) {
+// 8 codes of a dword as two-byte floats (bf16, or fp16 with HALF): RAWINT4 1 + c / 16 in the order k0 k4 k1 k5 k2 k6 k3 k7,
+// MXFP4 their values in order.
+struct DotConsts {
+  uint32_t m, o;
+};
+template <bool HALF>
+__device__ __forceinline__ DotConsts dot_consts() {
+  // (values the compiler cannot see through, in a scalar and a vector register: (w & m) | o is then one instruction)
+  uint32_t m = HALF ? 0x03c003c0u : 0x00780078u, o = HALF ? 0x3c003c00u : 0x3f803f80u;
+  asm volatile("" : "+s"(m));
+  asm volatile("" : "+v"(o));
+  return DotConsts{m, o};
+}
+template <bool MX, bool HALF>
+__device__ __forceinline__ u32x4 decode8(uint32_t w, DotConsts dc) {
   if (MX) {
     auto two = [&](auto sel) {
-      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, decltype(sel)::value));
+      constexpr int k = decltype(sel)::value;
+      if (HALF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, k));
+      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, k));
     };
     return u32x4{two(std::integral_constant<int, 0>()), two(std::integral_constant<int, 1>()),
                  two(std::integral_constant<int, 2>()), two(std::integral_constant<int, 3>())};
   }
-  const uint32_t m = 0x00780078u, o = 0x3f803f80u;
-  return u32x4{((w << 3) & m) | o, ((w >> 1) & m) | o, ((w >> 5) & m) | o, ((w >> 9) & m) | o};
+  if (HALF)
+    return u32x4{((w << 6) & dc.m) | dc.o, ((w << 2) & dc.m) | dc.o, ((w >> 2) & dc.m) | dc.o, ((w >> 6) & dc.m) | dc.o};
+  return u32x4{((w << 3) & dc.m) | dc.o, ((w >> 1) & dc.m) | dc.o, ((w >> 5) & dc.m) | dc.o, ((w >> 9) & dc.m) | dc.o};
 }
 
-// 8 bf16 in order -> the order of codes_bf16<false>
+// 8 two-byte values in order -> the order of RAWINT4's decode8
 __device__ __forceinline__ u32x4 order8(u32x4 v) {
   return u32x4{__builtin_amdgcn_perm(v.z, v.x, 0x05040100u), __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
                __builtin_amdgcn_perm(v.w, v.y, 0x05040100u), __builtin_amdgcn_perm(v.w, v.y, 0x07060302u)};
@@ -88,7 +106,9 @@ __device__ __forceinline__ u32x4 order8(u32x4 v) {
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+template <bool HALF>
 __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c) {
+  if (HALF) return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, a), __builtin_bit_cast(half2_t, b), c, false);
   return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, a), __builtin_bit_cast(bf16x2_t, b), c, false);
 }
 
@@ -98,29 +118,15 @@ typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer_of(const void* p, size_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)(uint32_t)bytes, 0x00020000);
 }
-
-// One expert's matrix of so many rows, G scale groups each.
-struct Matrix {
-  Buffer w, s;
-};
-__device__ __forceinline__ Matrix matrix_of(const uint8_t* w, const uint16_t* s, size_t e, int rows, int G) {
-  const size_t n = (size_t)rows * G;
-  return {buffer_of(w + e * n * 16, n * 16), buffer_of(s + e * n, n * 2)};
+__device__ __forceinline__ u32x4 buffer16(Buffer b, uint32_t lane, uint32_t base) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)lane, (int)base, 0));
 }
 
 // A contraction goes in units of 256 values, 8 groups, one for each of a row's
-// eight lanes.  Codes and scale of this lane's group in rows r .. r + 7 (a tile).
-// Every load is issued, whatever the unit, so that how many are in flight
-// behind a value is known where it is waited for; a lane whose group lies behind the
-// row's last reads that one, and its vectors are 0.
-struct Codes {
-  u32x4 c;
-  uint16_t s;
-};
-__device__ __forceinline__ void load_codes(const Matrix& m, uint32_t group, uint32_t base, Codes& c) {
-  c.c = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(m.w, (int)(group * 16), (int)(base * 16), 0));
-  c.s = __builtin_amdgcn_raw_buffer_load_b16(m.s, (int)(group * 2), (int)(base * 2), 0);
-}
+// eight lanes; a load brings a unit of eight rows (a tile).  Every load of
+// codes is issued, whatever the unit, so that how many are in flight behind a value
+// is known where it is waited for; a lane whose group lies behind the row's
+// last reads that one, and its vectors are 0.
 
 // Vectors in LDS: four planes of 16 bytes a group, so that eight lanes read 128 bytes in a row.
 struct Vec {
@@ -129,19 +135,6 @@ struct Vec {
 __device__ __forceinline__ void read_vec(const uint8_t* p, int group, int plane, Vec& v) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) v.v[j] = *reinterpret_cast<const u32x4*>(p + j * plane + group * 16);
-}
-
-// The group's product with V vectors, from the sums t[] on.
-template <bool MX, int V>
-__device__ __forceinline__ void multiply(const u32x4& c, const Vec* x, float* t) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const u32x4 w = codes_bf16<MX>(c[j]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int v = 0; v < V; ++v) t[v] = dot2(w[i], x[v].v[j][i], t[v]);
-  }
 }
 
 // A sum over the eight lanes of a row, in all of them.
@@ -153,18 +146,114 @@ __device__ __forceinline__ float eight_sum(float v) {
 
 constexpr int kLoraParts = 8;  // runs of the ranks
 constexpr int kUpDepth = 2;    // units of loads ahead, gate and up
+constexpr int kUpVecs = 2;     // tokens that gate and up take at a time
+
+// What a gate and up workgroup keeps in LDS behind its list.
+struct UpLds {
+  uint8_t* x;        // [V][4][Gp][16 bytes]
+  float* sums;       // [V][Gp]: -3/2 of a group's sum
+  uint16_t* scales;  // [2][16][G]: of gate and of up
+};
+
+// One pass of a workgroup's four waves over its columns for V tokens: acc[tile][token], tiles gate 0..7, 8..15, up 0..7, 8..15.
+template <bool MX, int V>
+__device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int i0, const uint16_t* list, bool first_pass,
+                                             const UpLds& l, float (*red)[4][kUpVecs][16]) {
+  const int kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
+  const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, u0 = kw * per;
+  const int Gp = per * 32, plane = Gp * 16;  // groups and bytes of a plane in LDS, 0 behind the row's end
+  const size_t n = (size_t)a.I * G;
+  const Buffer wg = buffer_of(a.wg + e * n * 16, n * 16), wu = buffer_of(a.wu + e * n * 16, n * 16);
+  const uint32_t at = (uint32_t)(i0 + row) * G, rows8 = 128u * G;
+  u32x4 cd[kUpDepth][4];
+  auto load = [&](int u, int b) {
+    const uint32_t o = (at + min(8 * u + c8, G - 1)) * 16;
+    cd[b][0] = buffer16(wg, o, 0);
+    cd[b][1] = buffer16(wg, o, rows8);
+    cd[b][2] = buffer16(wu, o, 0);
+    cd[b][3] = buffer16(wu, o, rows8);
+    __builtin_amdgcn_sched_barrier(0);  // (units' loads stay in order)
+  };
+#pragma unroll
+  for (int b = 0; b < kUpDepth; ++b) load(u0 + b, b);
+  if (first_pass) {
+    // the rows' scales, as they lie: 32 G bytes of each matrix
+    const uint16_t *sg = a.sg + e * n + (size_t)i0 * G, *su = a.su + e * n + (size_t)i0 * G;
+    for (int c = threadIdx.x; c < 4 * G; c += 256)
+      *reinterpret_cast<u32x4*>(l.scales + c * 8) =
+          *reinterpret_cast<const u32x4_u2*>(c < 2 * G ? sg + c * 8 : su + (c - 2 * G) * 8);
+  }
+#pragma unroll
+  for (int p = 0; p < V; ++p) {
+    const uint16_t* x = a.x + (size_t)(list[p] / a.k) * a.H;
+    for (int c = threadIdx.x; c < Gp * 4; c += 256) {
+      u32x4 v = {0, 0, 0, 0};
+      if (c < G * 4) v = *reinterpret_cast<const u32x4*>(x + c * 8);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s += bf_lo(v[j]) + bf_hi(v[j]);
+      s += dpp_f<0xB1>(s);
+      s += dpp_f<0x4E>(s);
+      *reinterpret_cast<u32x4*>(l.x + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = MX ? v : order8(v);
+      if ((c & 3) == 0) l.sums[p * Gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
+    }
+  }
+  __syncthreads();
+  const DotConsts dc = dot_consts<false>();
+  float acc[4][V] = {};
+  for (int v = 0; v < per; v += kUpDepth) {
+#pragma unroll
+    for (int b = 0; b < kUpDepth; ++b) {
+      if (v + b < per) {
+        const int g = 8 * (u0 + v + b) + c8;
+        Vec x[V];
+        float sum[V];
+#pragma unroll
+        for (int p = 0; p < V; ++p) {
+          read_vec(l.x + p * 4 * plane, g, plane, x[p]);
+          sum[p] = l.sums[p * Gp + g];
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float s = bf16_to_float(l.scales[(t * 8 + row) * G + min(g, G - 1)]);
+          float d[V];
+#pragma unroll
+          for (int p = 0; p < V; ++p) d[p] = sum[p];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4 w = decode8<MX, false>(cd[b][t][j], dc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int p = 0; p < V; ++p) d[p] = dot2<false>(w[i], x[p].v[j][i], d[p]);
+          }
+#pragma unroll
+          for (int p = 0; p < V; ++p) acc[t][p] = fmaf(s, d[p], acc[t][p]);
+          __builtin_amdgcn_sched_barrier(0);  // (decoded tiles side by side take registers from the loads ahead)
+        }
+      }
+      load(u0 + v + b + kUpDepth, b);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int p = 0; p < V; ++p) {
+      const float v = eight_sum(acc[t][p]);
+      if (c8 == 0) red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
+    }
+}
 
 // Gate and up.  A workgroup has 16 columns of I of one expert (its first
-// slot's block; the others leave at once) for all of its tokens, V at a time,
+// slot's block; the others leave at once) for all of its tokens, one or two at a time,
 // which lie in LDS.  Its four waves split the contraction.
-template <bool MX, bool LORA, int V>
+template <bool MX, bool LORA>
 __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
-  __shared__ float red[2][4][V][16];
-  __shared__ float lora[LORA ? kLoraParts : 1][2][V][16];
+  __shared__ float red[2][4][kUpVecs][16];
+  __shared__ float lora[LORA ? kLoraParts : 1][2][kUpVecs][16];
   const int slot = blockIdx.y, i0 = blockIdx.x * 16;
-  const int kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t e = a.ids[slot];
   int next = -1, M = 0;
   if (e >= 0 && e < a.E) M = slots_of(a, slot, e, list, next);
@@ -173,91 +262,34 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
     a.lead[slot] = M > 0;
   }
   if (!M) return;
-  const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, u0 = kw * per;
-  const int Gp = per * 32, plane = Gp * 16;      // groups and bytes of a plane in LDS, 0 behind the row's end
-  float* sums = reinterpret_cast<float*>(lds + V * 4 * plane);  // [vectors][Gp]: -3/2 of a group's sum
-  const Matrix mg = matrix_of(a.wg, a.sg, e, a.I, G), mu = matrix_of(a.wu, a.su, e, a.I, G);
-  const int c8 = lane & 7, row = lane >> 3;
-  const uint32_t first = (uint32_t)(i0 + row) * G, rows8 = 8u * G;
+  const int G = a.H / 32, Gp = ((G + 7) / 8 + 3) / 4 * 32, V = min(kUpVecs, a.T);
+  UpLds l;
+  l.x = lds;
+  l.sums = reinterpret_cast<float*>(lds + V * Gp * 64);
+  l.scales = reinterpret_cast<uint16_t*>(l.sums + V * Gp);
   __syncthreads();
-  for (int m0 = 0; m0 < M; m0 += V) {
-    const int nt = min(V, M - m0);
-    Codes cd[kUpDepth][4];  // gate rows 0..7, 8..15, up rows 0..7, 8..15
-    auto load = [&](int u, int b) {
-      const uint32_t g = first + min(8 * u + c8, G - 1);
-      load_codes(mg, g, 0, cd[b][0]);
-      load_codes(mg, g, rows8, cd[b][1]);
-      load_codes(mu, g, 0, cd[b][2]);
-      load_codes(mu, g, rows8, cd[b][3]);
-      __builtin_amdgcn_sched_barrier(0);  // (units' loads stay in order)
-    };
-#pragma unroll
-    for (int b = 0; b < kUpDepth; ++b) load(u0 + b, b);
-    for (int p = 0; p < nt; ++p) {
-      const uint16_t* x = a.x + (size_t)(list[m0 + p] / a.k) * a.H;
-      for (int c = threadIdx.x; c < Gp * 4; c += 256) {
-        u32x4 v = {0, 0, 0, 0};
-        if (c < G * 4) v = *reinterpret_cast<const u32x4*>(x + c * 8);
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s += bf_lo(v[j]) + bf_hi(v[j]);
-        s += dpp_f<0xB1>(s);
-        s += dpp_f<0x4E>(s);
-        *reinterpret_cast<u32x4*>(lds + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = MX ? v : order8(v);
-        if ((c & 3) == 0) sums[p * Gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
-      }
-    }
+  for (int m0 = 0; m0 < M; m0 += kUpVecs) {
+    const int nt = min(kUpVecs, M - m0);
+    if (nt == 1)
+      gate_up_pass<MX, 1>(a, e, i0, list + m0, m0 == 0, l, red);
+    else
+      gate_up_pass<MX, kUpVecs>(a, e, i0, list + m0, m0 == 0, l, red);
     if (LORA) {
       // columns by gate and up by runs of the ranks
       const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
       const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
       const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
-      float t[V] = {};
-#pragma unroll 1
+      float t[kUpVecs] = {};
+#pragma unroll 4
       for (int r = r0; r < r1; ++r) {
         const float w = b[r];
 #pragma unroll
-        for (int p = 0; p < V; ++p)
+        for (int p = 0; p < kUpVecs; ++p)
           if (p < nt) t[p] = fmaf(w, a.ua[(size_t)list[m0 + p] * 2 * a.R + up * a.R + r], t[p]);
       }
 #pragma unroll
-      for (int p = 0; p < V; ++p) lora[part][up][p][c] = t[p];
+      for (int p = 0; p < kUpVecs; ++p) lora[part][up][p][c] = t[p];
     }
-    __syncthreads();
-    float acc[4][V] = {};
-    for (int v = 0; v < per; v += kUpDepth) {
-#pragma unroll
-      for (int b = 0; b < kUpDepth; ++b) {
-        if (v + b < per) {
-          const int g = 8 * (u0 + v + b) + c8;
-          Vec x[V];
-          float sum[V];
-#pragma unroll
-          for (int p = 0; p < V; ++p) {
-            read_vec(lds + p * 4 * plane, g, plane, x[p]);
-            sum[p] = sums[p * Gp + g];
-          }
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            float d[V];
-#pragma unroll
-            for (int p = 0; p < V; ++p) d[p] = sum[p];
-            multiply<MX, V>(cd[b][t].c, x, d);
-#pragma unroll
-            for (int p = 0; p < V; ++p) acc[t][p] = fmaf(bf16_to_float(cd[b][t].s), d[p], acc[t][p]);
-            __builtin_amdgcn_sched_barrier(0);  // (decoded tiles side by side take registers from the loads ahead)
-          }
-        }
-        load(u0 + v + b + kUpDepth, b);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int p = 0; p < V; ++p) {
-        const float v = eight_sum(acc[t][p]);
-        if (c8 == 0) red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
-      }
     __syncthreads();
     if (threadIdx.x < 16 * nt) {
       const int p = threadIdx.x >> 4, c = threadIdx.x & 15;
@@ -276,17 +308,16 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
         gv = gv > a.limit ? a.limit : gv;
         uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
       }
+      // h in fp16 times a power of two that brings the largest of the 16 below 2^15: a rounding of 2^-11 of the value
       const float h = gv * sigmoid_f(gv) * uv;
-      uint16_t hi, lo;
-      split_bf16(h, hi, lo);
-      uint16_t* o = a.hs + (size_t)s * 2 * a.I + i0 + (MX ? c : perm_pos(c));
-      o[0] = hi;
-      o[a.I] = lo;
-      const float sum = row16_sum(bf16_to_float(hi) + bf16_to_float(lo));
-      if (c == 0) a.hsum[(size_t)s * (a.I / 16) + blockIdx.x] = sum;
+      const int ex = pow2_exponent_for(row16_max(fabsf(h)));
+      const uint16_t bits = float_to_half_bits(ldexpf(h, ex));
+      a.hs[(size_t)s * a.I + i0 + (MX ? c : perm_pos(c))] = bits;
+      const float sum = row16_sum(half_bits_to_float(bits));
+      if (c == 0) a.hsf[(size_t)s * (a.I / 16) + blockIdx.x] = float2_t{MX ? 0.f : -1.5f * sum, ldexpf(MX ? 1.f : 16.f, -ex)};
       if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
     }
-    if (m0 + V < M) __syncthreads();
+    if (m0 + kUpVecs < M) __syncthreads();
   }
 }
 
@@ -336,14 +367,16 @@ __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
 }
 
 
-constexpr int kDownWaves = 4;
-constexpr int kDownDepth = 4;  // units of loads ahead
-constexpr int kDownK = 64;     // groups of h in LDS at a time
+constexpr int kDownWaves = 8;
+constexpr int kDownUnits = 4;               // units of a chunk: the loads ahead
+constexpr int kDownK = kDownUnits * 8;      // its groups
+constexpr int kDownLds = kDownK * (64 + 16 + 32);  // bytes a wave: h, sums and factors, scales of 16 rows
 
 // Down and the sum over the slots.  A workgroup has 16 columns of H; its waves
 // take the experts in turn (a wave per expert, the whole contraction), a slot at a
-// time with its h in LDS, and add to sums of their own per token, which the end
-// joins in the waves' order.
+// time, and add to sums of their own per token, which the end joins in the waves'
+// order.  A wave goes through its slots' contractions in chunks without a stop:
+// while it multiplies one, the codes, scales and h of the next are on their way.
 template <bool MX, bool LORA>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -352,9 +385,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
   const int h0 = blockIdx.x * 16, G = a.I / 32;
   constexpr int plane = kDownK * 16;
-  uint8_t* hl = lds + wave * (8 * plane + kDownK * 4);  // hi's four planes, lo's four, -3/2 of the groups' sums
-  float* sums = reinterpret_cast<float*>(hl + 8 * plane);
-  float* acc = reinterpret_cast<float*>(lds + kDownWaves * (8 * plane + kDownK * 4));  // [waves][T][16]
+  uint8_t* hl = lds + wave * kDownLds;                             // four planes of h
+  u32x4* sf = reinterpret_cast<u32x4*>(hl + 4 * plane);            // [group]: sum and factor of its halves
+  uint16_t* sl = reinterpret_cast<uint16_t*>(sf + kDownK);         // [16][kDownK] scales
+  float* acc = reinterpret_cast<float*>(lds + kDownWaves * kDownLds);  // [waves][T][16]
   int U = 0;
   for (int s0 = 0; s0 < a.S; s0 += 64) {
     const int s = s0 + lane;
@@ -372,79 +406,122 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   }
   for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 64 * kDownWaves) acc[i] = 0.f;
   __syncthreads();
-  const uint32_t first = (uint32_t)(h0 + row) * G, rows8 = 8u * G;
-  for (int j = wave; j < U; j += kDownWaves) {
-    const size_t e = __builtin_amdgcn_readfirstlane(expert[j]);
-    const Matrix md = matrix_of(a.wd, a.sd, e, a.H, G);
-    for (int s = __builtin_amdgcn_readfirstlane(order[j]); s >= 0; s = __builtin_amdgcn_readfirstlane(next[s])) {
-      float y[2] = {0.f, 0.f};
-      for (int k0 = 0; k0 < G; k0 += kDownK) {
-        const int len = min(kDownK, G - k0), units = (len + 7) / 8;
-        Codes cd[kDownDepth][2];
-        auto load = [&](int u, int b) {
-          const uint32_t g = first + min(k0 + 8 * u + c8, G - 1);
-          load_codes(md, g, 0, cd[b][0]);
-          load_codes(md, g, rows8, cd[b][1]);
-          __builtin_amdgcn_sched_barrier(0);
-        };
+  if (wave < U) {
+    const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 2), fb = buffer_of(a.hsf, (size_t)a.S * (a.I / 16) * 8);
+    const uint32_t at = (uint32_t)(h0 + row) * G, rows8 = 128u * G;
+    const size_t n = (size_t)a.H * G;
+    // the chunk whose loads are issued next
+    int j = wave, s = __builtin_amdgcn_readfirstlane(order[j]), k0 = 0;
+    size_t e = __builtin_amdgcn_readfirstlane(expert[j]);
+    u32x4 cd[kDownUnits][2], hn[2], sn;
+    float2_t fn;
+    auto load_codes = [&](int b) {
+      const Buffer w = buffer_of(a.wd + e * n * 16, n * 16);
+      const uint32_t o = (at + min(k0 + 8 * b + c8, G - 1)) * 16;
+      cd[b][0] = buffer16(w, o, 0);
+      cd[b][1] = buffer16(w, o, rows8);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_rest = [&] {
+      // scales: a lane has 8 groups of one of the 16 rows
+      const uint16_t* p = a.sd + e * n + (size_t)(h0 + (lane >> 2)) * G;
+      const int g = k0 + (lane & 3) * 8;
+      if (k0 + kDownK <= G) {
+        sn = *reinterpret_cast<const u32x4_u2*>(p + g);
+      } else {
+        uint32_t v[8];
 #pragma unroll
-        for (int b = 0; b < kDownDepth; ++b) load(b, b);
-        wave_fence();
-        // (16 bytes of hi or lo: a quarter of a group)
-        for (int c = lane; c < units * 32; c += 64) {
+        for (int i = 0; i < 8; ++i) v[i] = p[min(g + i, G - 1)];
 #pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            u32x4 v = {0, 0, 0, 0};
-            if (c < len * 4) v = *reinterpret_cast<const u32x4*>(a.hs + ((size_t)s * 2 + p) * a.I + k0 * 32 + c * 8);
-            *reinterpret_cast<u32x4*>(hl + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = v;
-          }
-        }
-        if (lane < units * 8) {
-          float t = 0.f;
-          if (!MX && lane < len) {
-            const float* p = a.hsum + (size_t)s * (a.I / 16) + (k0 + lane) * 2;
-            t = -1.5f * (p[0] + p[1]);
-          }
-          sums[lane] = t;
-        }
-        wave_fence();
-        for (int u = 0; u < units; u += kDownDepth) {
-#pragma unroll
-          for (int b = 0; b < kDownDepth; ++b) {
-            if (u + b < units) {
-              const int g = 8 * (u + b) + c8;
-              Vec x[2];
-              read_vec(hl, g, plane, x[0]);
-              read_vec(hl + 4 * plane, g, plane, x[1]);
-              const float sum = sums[g];
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                float d[2] = {sum, 0.f};
-                multiply<MX, 2>(cd[b][t].c, x, d);
-                y[t] = fmaf(bf16_to_float(cd[b][t].s), d[0] + d[1], y[t]);
-              }
-            }
-            load(u + b + kDownDepth, b);
-          }
-        }
+        for (int i = 0; i < 4; ++i) sn[i] = v[2 * i] | v[2 * i + 1] << 16;
       }
+      // h: quarters of groups; sums and factors: halves
+      const uint32_t last = (uint32_t)(s + 1) * G * 64 - 16, ho = ((uint32_t)s * G + k0) * 64 + lane * 16;
+      hn[0] = buffer16(hb, min(ho, last), 0);
+      hn[1] = buffer16(hb, min(ho + 1024, last), 0);
+      const uint32_t fo = min(((uint32_t)s * G + k0) * 16 + lane * 8, (uint32_t)(s + 1) * G * 16 - 8);
+      fn = __builtin_bit_cast(float2_t, __builtin_amdgcn_raw_buffer_load_b64(fb, (int)fo, 0, 0));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    load_rest();
+#pragma unroll
+    for (int b = 0; b < kDownUnits; ++b) load_codes(b);
+    const DotConsts dc = dot_consts<true>();
+    float y[2] = {0.f, 0.f};
+    for (bool more = true; more;) {
+      // this chunk's h, sums, factors and scales to LDS, 0 behind the contraction's end
+      const int cs = s, ck = k0, len = min(kDownK, G - ck);
+      const size_t ce = e;
+      const u32x4 zero = {0, 0, 0, 0};
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = lane + 64 * i;
+        *reinterpret_cast<u32x4*>(hl + (c & 3) * plane + (c >> 2) * 16) = c < 4 * len ? hn[i] : zero;
+      }
+      reinterpret_cast<float2_t*>(sf)[lane] = lane < 2 * len ? fn : float2_t{0.f, 0.f};
+      *reinterpret_cast<u32x4*>(sl + lane * 8) = sn;
+      wave_fence();
+      // the next one
+      k0 += kDownK;
+      if (k0 >= G) {
+        k0 = 0;
+        int t = __builtin_amdgcn_readfirstlane(next[s]);
+        if (t < 0) {
+          j += kDownWaves;
+          more = j < U;
+          if (more) {
+            t = __builtin_amdgcn_readfirstlane(order[j]);
+            e = __builtin_amdgcn_readfirstlane(expert[j]);
+          } else {
+            t = s;
+          }
+        }
+        s = t;
+      }
+      load_rest();
+      const int units = (len + 7) / 8;
+#pragma unroll
+      for (int b = 0; b < kDownUnits; ++b) {
+        if (b < units) {
+          const int g = 8 * b + c8;
+          Vec x;
+          read_vec(hl, g, plane, x);
+          const u32x4 f = sf[g];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            float d[2] = {__uint_as_float(f.x), __uint_as_float(f.z)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const u32x4 w = decode8<MX, true>(cd[b][t][i], dc);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) d[i / 2] = dot2<true>(w[v], x.v[i][v], d[i / 2]);
+            }
+            const float sc = bf16_to_float(sl[(t * 8 + row) * kDownK + g]);
+            y[t] = fmaf(sc, fmaf(__uint_as_float(f.y), d[0], __uint_as_float(f.w) * d[1]), y[t]);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        load_codes(b);
+      }
+      if (ck + kDownK < G) continue;
+      // the slot is done
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        y[t] = eight_sum(y[t]);
-        if (!MX) y[t] *= 16.f;
+        float v = eight_sum(y[t]);
+        y[t] = 0.f;
         if (LORA) {
           // an eighth of the ranks a lane
-          const float *b = a.bd + (e * a.H + h0 + 8 * t + row) * a.R, *u = a.ud + (size_t)s * a.R;
+          const float *b = a.bd + (ce * a.H + h0 + 8 * t + row) * a.R, *u = a.ud + (size_t)cs * a.R;
           float l = 0.f;
-#pragma unroll 1
+#pragma unroll 2
           for (int r = c8; r < a.R; r += 8) l = fmaf(b[r], u[r], l);
-          y[t] = fmaf(a.sc, eight_sum(l), y[t]);
+          v = fmaf(a.sc, eight_sum(l), v);
         }
-      }
-      if (c8 == 0) {
-        float* o = acc + (wave * a.T + s / a.k) * 16 + row;
-        o[0] = fmaf(a.rw[s], y[0], o[0]);
-        o[8] = fmaf(a.rw[s], y[1], o[8]);
+        if (c8 == 0) {
+          float* o = acc + (wave * a.T + cs / a.k) * 16 + 8 * t + row;
+          *o = fmaf(a.rw[cs], v, *o);
+        }
       }
     }
   }
@@ -459,7 +536,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
 // ---------------------------------------------------------------- host
 
 struct DecodePlan {
-  size_t hs, hsum, h, next, lead, ua, ud, total;
+  size_t hs, hsf, h, next, lead, ua, ud, total;
 };
 static DecodePlan plan_decode(const Dims& d) {
   DecodePlan p;
@@ -467,8 +544,8 @@ static DecodePlan plan_decode(const Dims& d) {
   p.next = 0;
   p.lead = round256(4 * S);
   p.hs = p.lead + round256(4 * S);
-  p.hsum = p.hs + round256(4 * S * d.I);
-  p.h = p.hsum + round256(4 * S * (d.I / 16));
+  p.hsf = p.hs + round256(2 * S * d.I);
+  p.h = p.hsf + round256(8 * S * (d.I / 16));
   p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
   p.total = p.ud + round256(4 * S * d.R);
@@ -490,17 +567,15 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     note_launch();
   }
   const size_t groups = (size_t)((a.H / 32 + 7) / 8 + 3) / 4 * 32;
-  const dim3 grid((unsigned)(a.I / 16), (unsigned)a.S);
-  if (a.T == 1)
-    k_decode_gate_up<MX, LORA, 1><<<grid, 256, groups * 68, st>>>(a);
-  else
-    k_decode_gate_up<MX, LORA, 2><<<grid, 256, 2 * groups * 68, st>>>(a);
+  const size_t scales = (size_t)(a.H / 32) * 64;
+  const int V = a.T < kUpVecs ? a.T : kUpVecs;
+  k_decode_gate_up<MX, LORA><<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, V * groups * 68 + scales, st>>>(a);
   note_launch();
   if (LORA) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 64 * kDownWaves, kDownWaves * (kDownK * 132 + (size_t)a.T * 64), st>>>(a);
+  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 64 * kDownWaves, kDownWaves * (kDownLds + (size_t)a.T * 64), st>>>(a);
   note_launch();
 }
 
@@ -546,7 +621,7 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.ad = layer->down_lora_a, a.bd = layer->down_lora_b;
   a.h = ws_ptr<float>(workspace, p.h);
   a.hs = ws_ptr<uint16_t>(workspace, p.hs);
-  a.hsum = ws_ptr<float>(workspace, p.hsum);
+  a.hsf = ws_ptr<float2_t>(workspace, p.hsf);
   a.next = ws_ptr<int32_t>(workspace, p.next);
   a.lead = ws_ptr<int32_t>(workspace, p.lead);
   a.ua = ws_ptr<float>(workspace, p.ua);

@@ -199,11 +199,11 @@ def experts(x, ids, rw, layer, fmt="rawint4", limit=0.0, lora=None, sc=0.0):
     e_count = layer["gate_packed"].shape[0]
     out, bound = torch.zeros_like(x), torch.zeros_like(x)
 
-    def product(name, e, v, dv, split):
+    def product(name, e, v, dv, split):  # split: what v is rounded by before the product
         w, mag = weights(layer[name + "_packed"][e].cpu(), layer[name + "_scale"][e].cpu(), fmt)
         n = v.numel()
         y = w @ v
-        d = w.abs() @ dv + (8 * math.sqrt(2 * n) * U + split) * (mag @ v.abs())
+        d = w.abs() @ (dv + split * v.abs()) + 8 * math.sqrt(2 * n) * U * (mag @ v.abs())
         if lora is not None:
             a, b = lora[name + "_lora_a"][e].double().cpu(), lora[name + "_lora_b"][e].double().cpu()
             t = a @ v
@@ -225,7 +225,7 @@ def experts(x, ids, rw, layer, fmt="rawint4", limit=0.0, lora=None, sc=0.0):
             silu = g / (1 + torch.exp(-g))
             h = silu * u
             dh = 1.1 * (1.1 * dg * u.abs() + silu.abs() * du + 1.1 * dg * du) + 16 * U * (1 + g.abs()) * h.abs()
-            y, dy = product("down", e, h, dh, 2.0**-16)
+            y, dy = product("down", e, h, dh, 2.0**-11)
             out[t] += rw[t, j] * y
             bound[t] += rw[t, j].abs() * (dy + 2 * U * y.abs())
     return out, 1.1 * bound + 8 * U * out.abs()
