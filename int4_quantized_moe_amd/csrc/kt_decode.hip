@@ -156,9 +156,9 @@ struct UpLds {
 };
 
 // One pass of a workgroup's four waves over its columns for V tokens: acc[tile][token], tiles gate 0..7, 8..15, up 0..7, 8..15.
-template <bool MX, int V>
+template <bool MX, bool LORA, int V>
 __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int i0, const uint16_t* list, bool first_pass,
-                                             const UpLds& l, float (*red)[4][kUpVecs][16]) {
+                                             const UpLds& l, float (*red)[4][kUpVecs][16], float (*lora)[2][kUpVecs][16]) {
   const int kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
   const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, u0 = kw * per;
   const int Gp = per * 32, plane = Gp * 16;  // groups and bytes of a plane in LDS, 0 behind the row's end
@@ -197,6 +197,19 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
       *reinterpret_cast<u32x4*>(l.x + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = MX ? v : order8(v);
       if ((c & 3) == 0) l.sums[p * Gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
     }
+  }
+  if (LORA) {
+    // B times (A x): columns by gate and up by runs of the ranks, behind the loads of codes
+    const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
+    const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
+    const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
+    float t[V] = {};
+#pragma unroll 4
+    for (int r = r0; r < r1; ++r)
+#pragma unroll
+      for (int p = 0; p < V; ++p) t[p] = fmaf(b[r], a.ua[(size_t)list[p] * 2 * a.R + up * a.R + r], t[p]);
+#pragma unroll
+    for (int p = 0; p < V; ++p) lora[part][up][p][c] = t[p];
   }
   __syncthreads();
   const DotConsts dc = dot_consts<false>();
@@ -271,25 +284,9 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   for (int m0 = 0; m0 < M; m0 += kUpVecs) {
     const int nt = min(kUpVecs, M - m0);
     if (nt == 1)
-      gate_up_pass<MX, 1>(a, e, i0, list + m0, m0 == 0, l, red);
+      gate_up_pass<MX, LORA, 1>(a, e, i0, list + m0, m0 == 0, l, red, lora);
     else
-      gate_up_pass<MX, kUpVecs>(a, e, i0, list + m0, m0 == 0, l, red);
-    if (LORA) {
-      // columns by gate and up by runs of the ranks
-      const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
-      const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
-      const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
-      float t[kUpVecs] = {};
-#pragma unroll 4
-      for (int r = r0; r < r1; ++r) {
-        const float w = b[r];
-#pragma unroll
-        for (int p = 0; p < kUpVecs; ++p)
-          if (p < nt) t[p] = fmaf(w, a.ua[(size_t)list[m0 + p] * 2 * a.R + up * a.R + r], t[p]);
-      }
-#pragma unroll
-      for (int p = 0; p < kUpVecs; ++p) lora[part][up][p][c] = t[p];
-    }
+      gate_up_pass<MX, LORA, kUpVecs>(a, e, i0, list + m0, m0 == 0, l, red, lora);
     __syncthreads();
     if (threadIdx.x < 16 * nt) {
       const int p = threadIdx.x >> 4, c = threadIdx.x & 15;
@@ -321,8 +318,48 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   }
 }
 
-constexpr int kVecs = 4;  // tokens that a row of A takes at a time
-// x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens, four at a time.
+// A row of A times V tokens' vectors (bf16 x, or fp32 h), by a wave: 1024 values in flight a vector.
+template <bool DOWN, int V>
+__device__ __forceinline__ void lora_row(const DecodeArgs& a, const float* w, const uint16_t* list, float* out, int pitch) {
+  const int K = DOWN ? a.I : a.H, lane = threadIdx.x & 63;
+  float v[V] = {};
+  for (int c0 = lane * 4; c0 < K; c0 += 1024) {
+    float4 b[4], x[4][V];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // (values behind the row's end: its last ones, times 0)
+      const int c = min(c0 + 256 * i, K - 4);
+      b[i] = *reinterpret_cast<const float4*>(w + c);
+#pragma unroll
+      for (int p = 0; p < V; ++p) {
+        if (DOWN) {
+          x[i][p] = *reinterpret_cast<const float4*>(a.h + (size_t)list[p] * K + c);
+        } else {
+          const u32pair t = *reinterpret_cast<const u32pair*>(a.x + (size_t)(list[p] / a.k) * K + c);
+          x[i][p] = float4{bf_lo(t.x), bf_hi(t.x), bf_lo(t.y), bf_hi(t.y)};
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c0 + 256 * i >= K) b[i] = float4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int p = 0; p < V; ++p) {
+        v[p] = fmaf(b[i].x, x[i][p].x, v[p]);
+        v[p] = fmaf(b[i].y, x[i][p].y, v[p]);
+        v[p] = fmaf(b[i].z, x[i][p].z, v[p]);
+        v[p] = fmaf(b[i].w, x[i][p].w, v[p]);
+      }
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < V; ++p) {
+    const float t = wave_sum(v[p]);
+    if (lane == 0) out[(size_t)list[p] * pitch] = t;
+  }
+}
+
+// x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens, one or two at a time.
 template <bool DOWN>
 __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
@@ -332,40 +369,15 @@ __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   const int M = slots_of(a, blockIdx.y, e, list, next);
   if (!M) return;
   __syncthreads();
-  const int rows = DOWN ? a.R : 2 * a.R, r = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int rows = DOWN ? a.R : 2 * a.R, r = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= rows) return;
   const int K = DOWN ? a.I : a.H;
   const float* w = (DOWN ? a.ad : r < a.R ? a.ag : a.au) + ((size_t)e * a.R + (r < a.R ? r : r - a.R)) * K;
-  for (int m0 = 0; m0 < M; m0 += kVecs) {
-    const int nt = min(kVecs, M - m0);
-    float v[kVecs] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int c = lane * 4; c < K; c += 256) {
-      const float4 b = *reinterpret_cast<const float4*>(w + c);
-#pragma unroll
-      for (int p = 0; p < kVecs; ++p) {
-        if (p >= nt) break;
-        float4 x;
-        if (DOWN) {
-          x = *reinterpret_cast<const float4*>(a.h + (size_t)list[m0 + p] * K + c);
-        } else {
-          const u32pair t = *reinterpret_cast<const u32pair*>(a.x + (size_t)(list[m0 + p] / a.k) * K + c);
-          x = float4{bf_lo(t.x), bf_hi(t.x), bf_lo(t.y), bf_hi(t.y)};
-        }
-        v[p] = fmaf(b.x, x.x, v[p]);
-        v[p] = fmaf(b.y, x.y, v[p]);
-        v[p] = fmaf(b.z, x.z, v[p]);
-        v[p] = fmaf(b.w, x.w, v[p]);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < kVecs; ++p) {
-      const float t = wave_sum(v[p]);
-      if (p < nt && lane == 0) (DOWN ? a.ud : a.ua)[(size_t)list[m0 + p] * rows + r] = t;
-    }
-  }
+  float* out = (DOWN ? a.ud : a.ua) + r;
+  int m = 0;
+  for (; m + 2 <= M; m += 2) lora_row<DOWN, 2>(a, w, list + m, out, rows);
+  if (m < M) lora_row<DOWN, 1>(a, w, list + m, out, rows);
 }
-
 
 constexpr int kDownWaves = 8;
 constexpr int kDownUnits = 4;               // units of a chunk: the loads ahead
