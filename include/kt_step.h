@@ -155,16 +155,18 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
 
 #define KT_MOE_DECODE_MAX_TOKENS 64
 #define KT_MOE_DECODE_MAX_SLOTS 1024 /* tokens * top_k */
+#define KT_MOE_DECODE_MAX_HIDDEN 16384
 
 /*
- * kt_rawint4_moe_infer for up to KT_MOE_DECODE_MAX_TOKENS tokens: the same
- * arguments and formula, in two kernels (four with LoRA), without sorting,
- * converted scales or staged rows.  It reads the packed rows of each chosen expert once
- * for up to four tokens.  Inputs and bf16 scales keep their whole range
- * (no numeric domain); h is kept in fp32 and multiplied to 2^-16; an input
- * that is not finite makes its token's output NaN.  tokens == 0 is a valid
- * no-op.  A workspace of the size for some number of tokens serves every
- * smaller number too.
+ * kt_rawint4_moe_infer for up to KT_MOE_DECODE_MAX_TOKENS tokens (and a hidden
+ * of up to KT_MOE_DECODE_MAX_HIDDEN): the same arguments and formula, in two
+ * kernels (four with LoRA), without sorting, converted scales or staged rows.
+ * The packed rows of each chosen expert are read once for its tokens.  Inputs
+ * and bf16 scales keep their whole range (no numeric domain); products and
+ * sums are fp32, h is rounded to fp16 in between (2^-11 of a value; a power of
+ * two keeps its range); an input that is not finite makes its token's output
+ * NaN.  tokens == 0 is a valid no-op.  A workspace of the size for some
+ * number of tokens serves every smaller number too.
  */
 size_t kt_moe_decode_workspace_bytes(const kt_rawint4_moe_layer* layer, int32_t tokens);
 int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint16_t* inputs, const int64_t* expert_ids,

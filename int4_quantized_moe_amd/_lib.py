@@ -49,6 +49,7 @@ KT_ADAMW_BLOCK = 256
 KT_ADAMW_MAX_TENSORS = 65536
 KT_MOE_DECODE_MAX_TOKENS = 64
 KT_MOE_DECODE_MAX_SLOTS = 1024
+KT_MOE_DECODE_MAX_HIDDEN = 16384
 
 _vp = ctypes.c_void_p
 

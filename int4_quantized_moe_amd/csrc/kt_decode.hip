@@ -47,26 +47,54 @@ struct DecodeArgs {
   float* ud;      // [S][R]: h A_d^T
 };
 
-// The slots of slot `s`'s expert e from s on, in order, to list[] (wave 0
-// writes; every wave finds the same number); 0 if another slot comes before.
-// `next`: the slot after s, or -1.
-__device__ __forceinline__ int slots_of(const DecodeArgs& a, int s, int64_t e, uint16_t* list, int& next) {
-  const int lane = threadIdx.x & 63;
+// The slots of an expert, in order, by the masks of all slots that chose it.
+constexpr int kSlotWords = KT_MOE_DECODE_MAX_SLOTS / 64;
+struct Slots {
+  const uint64_t* mask;  // in LDS
+  int word;
+  uint64_t rest;
+  __device__ __forceinline__ int take() {  // the next slot; there has to be one
+    while (!rest) rest = get(++word);
+    const int s = word * 64 + __ffsll((unsigned long long)rest) - 1;
+    rest &= rest - 1;
+    return s;
+  }
+  __device__ __forceinline__ uint64_t get(int w) const {
+    const uint64_t m = mask[w];
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(m >> 32)) << 32 |
+           (uint32_t)__builtin_amdgcn_readfirstlane((int)m);
+  }
+};
+// A workgroup's slots: those of slot s's expert e, if s is its first (count > 0); next: the one after s, or -1.
+// Ends with a barrier.
+__device__ __forceinline__ Slots find_slots(const DecodeArgs& a, int s, int64_t e, uint64_t* mask, int& count, int& next) {
+  const int words = (a.S + 63) / 64, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+  for (int w = wave; w < words; w += waves) {
+    const int i = w * 64 + lane;
+    const uint64_t m = __ballot(i < a.S && a.ids[min(i, a.S - 1)] == e);
+    if (lane == 0) mask[w] = m;
+  }
+  __syncthreads();
+  Slots r{mask, 0, 0};
+  r.rest = r.get(0);
   next = -1;
   int n = 0;
   bool led = false;
-  for (int s0 = 0; s0 < a.S; s0 += 64) {
-    const bool hit = s0 + lane < a.S && a.ids[s0 + lane] == e;
-    const uint64_t mask = __ballot(hit);
-    const uint64_t upto = s - s0 >= 63 ? ~0ull : s < s0 ? 0ull : (2ull << (s - s0)) - 1;  // slots <= s of these 64
-    const uint64_t own = s >= s0 && s - s0 < 64 ? 1ull << (s - s0) : 0ull;
-    led |= (mask & upto & ~own) != 0;
-    const uint64_t rest = mask & ~(upto & ~own);
-    if (hit && (rest >> lane & 1) && threadIdx.x < 64) list[n + __popcll(rest & ((1ull << lane) - 1))] = (uint16_t)(s0 + lane);
-    n += __popcll(rest);
-    if (next < 0 && (rest & ~own)) next = s0 + __ffsll((unsigned long long)(rest & ~own)) - 1;
+  for (int w = 0; w < words; ++w) {
+    uint64_t m = r.get(w);
+    n += __popcll(m);
+    if (w < s >> 6) {
+      led |= m != 0;
+      continue;
+    }
+    if (w == s >> 6) {
+      led |= (m & ((1ull << (s & 63)) - 1)) != 0;
+      m &= ~((2ull << (s & 63)) - 1);
+    }
+    if (m && next < 0) next = w * 64 + __ffsll((unsigned long long)m) - 1;
   }
-  return led ? 0 : n;
+  count = led ? 0 : n;
+  return r;
 }
 
 // 8 codes of a dword as two-byte floats (bf16, or fp16 with HALF): RAWINT4 1 + c / 16 in the order k0 k4 k1 k5 k2 k6 k3 k7,
@@ -148,23 +176,88 @@ constexpr int kLoraParts = 8;  // runs of the ranks
 constexpr int kUpDepth = 2;    // units of loads ahead, gate and up
 constexpr int kUpVecs = 2;     // tokens that gate and up take at a time
 
-// What a gate and up workgroup keeps in LDS behind its list.
+// What a gate and up workgroup keeps in LDS.
 struct UpLds {
   uint8_t* x;        // [V][4][Gp][16 bytes]
   float* sums;       // [V][Gp]: -3/2 of a group's sum
   uint16_t* scales;  // [2][16][G]: of gate and of up
+  float* b;          // [2][16][R]: rows of B
+  float* ua;         // [V][2 R]
+  float (*red)[4][kUpVecs][16];            // [gate, up][wave][token][column]
+  float (*lora)[2][kUpVecs][16];           // [run of ranks][gate, up][token][column]
 };
 
-// One pass of a workgroup's four waves over its columns for V tokens: acc[tile][token], tiles gate 0..7, 8..15, up 0..7, 8..15.
+constexpr int kStage = 4;  // 16-byte pieces a thread takes at a time while LDS is filled
+
+// (`first`: the thread's first piece)  Pieces of two runs of n, one behind the other in LDS, kStage of a thread's: loads (those behind the end: the
+// last piece again) and stores.
+template <typename T>
+__device__ __forceinline__ void stage_load(const void* p, const void* q, int n, int first, u32x4* v) {
+#pragma unroll
+  for (int i = 0; i < kStage; ++i) {
+    const int c = min(first + 256 * i, 2 * n - 1);
+    v[i] = c < n ? *(reinterpret_cast<const T*>(p) + c) : *(reinterpret_cast<const T*>(q) + (c - n));
+  }
+}
+__device__ __forceinline__ void stage_store(void* p, int n, int first, const u32x4* v) {
+#pragma unroll
+  for (int i = 0; i < kStage; ++i) {
+    const int c = first + 256 * i;
+    if (c < 2 * n) reinterpret_cast<u32x4*>(p)[c] = v[i];
+  }
+}
+__device__ __forceinline__ void token_load(const uint16_t* x, int n, int first, u32x4* v) {
+#pragma unroll
+  for (int i = 0; i < kStage; ++i)
+    v[i] = *(reinterpret_cast<const u32x4*>(x) + min(first + 256 * i, n - 1));
+}
+// a token's pieces to its planes, 0 behind the row's end, with the groups' sums
+template <bool MX>
+__device__ __forceinline__ void stage_token(uint8_t* x, float* sums, int G, int Gp, int first, const u32x4* v) {
+#pragma unroll
+  for (int i = 0; i < kStage; ++i) {
+    const int c = first + 256 * i;
+    u32x4 w = v[i];
+    if (c >= G * 4) w = u32x4{0, 0, 0, 0};
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += bf_lo(w[j]) + bf_hi(w[j]);
+    s += dpp_f<0xB1>(s);
+    s += dpp_f<0x4E>(s);
+    if (c < Gp * 4) {
+      *reinterpret_cast<u32x4*>(x + ((c & 3) * Gp + (c >> 2)) * 16) = MX ? w : order8(w);
+      if ((c & 3) == 0) sums[c >> 2] = MX ? 0.f : -1.5f * s;
+    }
+  }
+}
+
+// One pass of a workgroup's four waves over its columns for V tokens (slots sl[]): sums to l.red and l.lora.
 template <bool MX, bool LORA, int V>
-__device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int i0, const uint16_t* list, bool first_pass,
-                                             const UpLds& l, float (*red)[4][kUpVecs][16], float (*lora)[2][kUpVecs][16]) {
-  const int kw = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
+__device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int i0, const int* sl, bool first_pass,
+                                             const UpLds& l) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));  // (or the addresses below are kept in registers over the passes, which there are too few for)
+  const int kw = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c8 = lane & 7, row = lane >> 3;
   const int G = a.H / 32, units = (G + 7) / 8, per = (units + 3) / 4, u0 = kw * per;
   const int Gp = per * 32, plane = Gp * 16;  // groups and bytes of a plane in LDS, 0 behind the row's end
   const size_t n = (size_t)a.I * G;
   const Buffer wg = buffer_of(a.wg + e * n * 16, n * 16), wu = buffer_of(a.wu + e * n * 16, n * 16);
   const uint32_t at = (uint32_t)(i0 + row) * G, rows8 = 128u * G;
+  // Into LDS: the rows' scales as they lie, 32 G bytes of each matrix, the tokens, and with LoRA rows of B and ua.
+  // Their loads are on their way before the first codes', so that waiting for them waits for no codes.
+  const uint16_t *sg = a.sg + e * n + (size_t)i0 * G, *su = a.su + e * n + (size_t)i0 * G;
+  const uint16_t* x[V];
+  u32x4 tv[V][kStage];
+#pragma unroll
+  for (int p = 0; p < V; ++p) {
+    x[p] = a.x + (size_t)(sl[p] / a.k) * a.H;
+    token_load(x[p], G * 4, tid, tv[p]);
+  }
+  float uv[V];
+  if (LORA) {
+#pragma unroll
+    for (int p = 0; p < V; ++p) uv[p] = a.ua[(size_t)sl[p] * 2 * a.R + min(tid, 2 * a.R - 1)];  // (R is at most 128)
+  }
   u32x4 cd[kUpDepth][4];
   auto load = [&](int u, int b) {
     const uint32_t o = (at + min(8 * u + c8, G - 1)) * 16;
@@ -174,44 +267,51 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
     cd[b][3] = buffer16(wu, o, rows8);
     __builtin_amdgcn_sched_barrier(0);  // (units' loads stay in order)
   };
+  auto load_ahead = [&] {
 #pragma unroll
-  for (int b = 0; b < kUpDepth; ++b) load(u0 + b, b);
+    for (int b = 0; b < kUpDepth; ++b) load(u0 + b, b);
+  };
   if (first_pass) {
-    // the rows' scales, as they lie: 32 G bytes of each matrix
-    const uint16_t *sg = a.sg + e * n + (size_t)i0 * G, *su = a.su + e * n + (size_t)i0 * G;
-    for (int c = threadIdx.x; c < 4 * G; c += 256)
-      *reinterpret_cast<u32x4*>(l.scales + c * 8) =
-          *reinterpret_cast<const u32x4_u2*>(c < 2 * G ? sg + c * 8 : su + (c - 2 * G) * 8);
-  }
-#pragma unroll
-  for (int p = 0; p < V; ++p) {
-    const uint16_t* x = a.x + (size_t)(list[p] / a.k) * a.H;
-    for (int c = threadIdx.x; c < Gp * 4; c += 256) {
-      u32x4 v = {0, 0, 0, 0};
-      if (c < G * 4) v = *reinterpret_cast<const u32x4*>(x + c * 8);
-      float s = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s += bf_lo(v[j]) + bf_hi(v[j]);
-      s += dpp_f<0xB1>(s);
-      s += dpp_f<0x4E>(s);
-      *reinterpret_cast<u32x4*>(l.x + (p * 4 + (c & 3)) * plane + (c >> 2) * 16) = MX ? v : order8(v);
-      if ((c & 3) == 0) l.sums[p * Gp + (c >> 2)] = MX ? 0.f : -1.5f * s;
+    u32x4 sv[kStage], bv[kStage];
+    stage_load<u32x4_u2>(sg, su, 2 * G, tid, sv);
+    if (LORA) stage_load<u32x4>(a.bg + ((size_t)e * a.I + i0) * a.R, a.bu + ((size_t)e * a.I + i0) * a.R, 4 * a.R, tid, bv);
+    __builtin_amdgcn_sched_barrier(0);
+    load_ahead();
+    stage_store(l.scales, 2 * G, tid, sv);
+    if (LORA) stage_store(l.b, 4 * a.R, tid, bv);  // (R is at most 128: all of it)
+    for (int c = 256 * kStage; c < 4 * G; c += 256 * kStage) {
+      stage_load<u32x4_u2>(sg, su, 2 * G, c + tid, sv);
+      stage_store(l.scales, 2 * G, c + tid, sv);
     }
+  } else {
+    __builtin_amdgcn_sched_barrier(0);
+    load_ahead();
   }
+#pragma unroll
+  for (int p = 0; p < V; ++p) stage_token<MX>(l.x + p * 4 * plane, l.sums + p * Gp, G, Gp, tid, tv[p]);
+  for (int c = 256 * kStage; c < 4 * Gp; c += 256 * kStage)
+#pragma unroll
+    for (int p = 0; p < V; ++p) {
+      token_load(x[p], G * 4, c + tid, tv[p]);
+      stage_token<MX>(l.x + p * 4 * plane, l.sums + p * Gp, G, Gp, c + tid, tv[p]);
+    }
   if (LORA) {
-    // B times (A x): columns by gate and up by runs of the ranks, behind the loads of codes
-    const int c = threadIdx.x & 15, up = threadIdx.x >> 4 & 1, part = threadIdx.x >> 5;
-    const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
-    const float* b = (up ? a.bu : a.bg) + ((size_t)e * a.I + i0 + c) * a.R;
-    float t[V] = {};
-#pragma unroll 4
-    for (int r = r0; r < r1; ++r)
 #pragma unroll
-      for (int p = 0; p < V; ++p) t[p] = fmaf(b[r], a.ua[(size_t)list[p] * 2 * a.R + up * a.R + r], t[p]);
-#pragma unroll
-    for (int p = 0; p < V; ++p) lora[part][up][p][c] = t[p];
+    for (int p = 0; p < V; ++p)
+      if (tid < 2 * a.R) l.ua[p * 2 * a.R + tid] = uv[p];
   }
   __syncthreads();
+  if (LORA) {
+    // B times (A x): columns by gate and up by runs of the ranks
+    const int c = tid & 15, up = tid >> 4 & 1, part = tid >> 5;
+    const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
+    float t[V] = {};
+    for (int r = r0; r < r1; ++r)
+#pragma unroll
+      for (int p = 0; p < V; ++p) t[p] = fmaf(l.b[(up * 16 + c) * a.R + r], l.ua[(p * 2 + up) * a.R + r], t[p]);
+#pragma unroll
+    for (int p = 0; p < V; ++p) l.lora[part][up][p][c] = t[p];
+  }
   const DotConsts dc = dot_consts<false>();
   float acc[4][V] = {};
   for (int v = 0; v < per; v += kUpDepth) {
@@ -253,8 +353,14 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
 #pragma unroll
     for (int p = 0; p < V; ++p) {
       const float v = eight_sum(acc[t][p]);
-      if (c8 == 0) red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
+      if (c8 == 0) l.red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
     }
+}
+
+// bytes of dynamic LDS: V tokens, scales, and with LoRA B and ua
+static __host__ __device__ inline size_t up_lds(int H, int R, int V) {
+  const size_t G = (size_t)H / 32, Gp = ((G + 7) / 8 + 3) / 4 * 32;
+  return V * Gp * 68 + 64 * G + (128 + 8 * V) * (size_t)R;
 }
 
 // Gate and up.  A workgroup has 16 columns of I of one expert (its first
@@ -263,13 +369,14 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
 template <bool MX, bool LORA>
 __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
+  __shared__ uint64_t mask[kSlotWords];
   __shared__ float red[2][4][kUpVecs][16];
   __shared__ float lora[LORA ? kLoraParts : 1][2][kUpVecs][16];
   const int slot = blockIdx.y, i0 = blockIdx.x * 16;
   const int64_t e = a.ids[slot];
   int next = -1, M = 0;
-  if (e >= 0 && e < a.E) M = slots_of(a, slot, e, list, next);
+  Slots slots = find_slots(a, slot, e, mask, M, next);
+  if (e < 0 || e >= a.E) M = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.next[slot] = next;
     a.lead[slot] = M > 0;
@@ -280,20 +387,26 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   l.x = lds;
   l.sums = reinterpret_cast<float*>(lds + V * Gp * 64);
   l.scales = reinterpret_cast<uint16_t*>(l.sums + V * Gp);
-  __syncthreads();
+  l.b = reinterpret_cast<float*>(l.scales + 32 * G);
+  l.ua = l.b + 32 * a.R;
+  l.red = red;
+  l.lora = lora;
   for (int m0 = 0; m0 < M; m0 += kUpVecs) {
     const int nt = min(kUpVecs, M - m0);
+    int sl[kUpVecs];
+    sl[0] = slots.take();
+    sl[1] = nt > 1 ? slots.take() : sl[0];
     if (nt == 1)
-      gate_up_pass<MX, LORA, 1>(a, e, i0, list + m0, m0 == 0, l, red, lora);
+      gate_up_pass<MX, LORA, 1>(a, e, i0, sl, m0 == 0, l);
     else
-      gate_up_pass<MX, LORA, kUpVecs>(a, e, i0, list + m0, m0 == 0, l, red, lora);
+      gate_up_pass<MX, LORA, kUpVecs>(a, e, i0, sl, m0 == 0, l);
     __syncthreads();
-    if (threadIdx.x < 16 * nt) {
+    if ((int)threadIdx.x < 16 * nt) {
       const int p = threadIdx.x >> 4, c = threadIdx.x & 15;
       const float by = MX ? 1.f : 16.f;
       float gv = by * (red[0][0][p][c] + red[0][1][p][c] + red[0][2][p][c] + red[0][3][p][c]);
       float uv = by * (red[1][0][p][c] + red[1][1][p][c] + red[1][2][p][c] + red[1][3][p][c]);
-      const int s = list[m0 + p];
+      const int s = p ? sl[1] : sl[0];
       if (LORA) {
         float lg = 0.f, lu = 0.f;
 #pragma unroll
@@ -320,7 +433,7 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
 
 // A row of A times V tokens' vectors (bf16 x, or fp32 h), by a wave: 1024 values in flight a vector.
 template <bool DOWN, int V>
-__device__ __forceinline__ void lora_row(const DecodeArgs& a, const float* w, const uint16_t* list, float* out, int pitch) {
+__device__ __forceinline__ void lora_row(const DecodeArgs& a, const float* w, const int* sl, float* out, int pitch) {
   const int K = DOWN ? a.I : a.H, lane = threadIdx.x & 63;
   float v[V] = {};
   for (int c0 = lane * 4; c0 < K; c0 += 1024) {
@@ -333,9 +446,9 @@ __device__ __forceinline__ void lora_row(const DecodeArgs& a, const float* w, co
 #pragma unroll
       for (int p = 0; p < V; ++p) {
         if (DOWN) {
-          x[i][p] = *reinterpret_cast<const float4*>(a.h + (size_t)list[p] * K + c);
+          x[i][p] = *reinterpret_cast<const float4*>(a.h + (size_t)sl[p] * K + c);
         } else {
-          const u32pair t = *reinterpret_cast<const u32pair*>(a.x + (size_t)(list[p] / a.k) * K + c);
+          const u32pair t = *reinterpret_cast<const u32pair*>(a.x + (size_t)(sl[p] / a.k) * K + c);
           x[i][p] = float4{bf_lo(t.x), bf_hi(t.x), bf_lo(t.y), bf_hi(t.y)};
         }
       }
@@ -355,28 +468,33 @@ __device__ __forceinline__ void lora_row(const DecodeArgs& a, const float* w, co
 #pragma unroll
   for (int p = 0; p < V; ++p) {
     const float t = wave_sum(v[p]);
-    if (lane == 0) out[(size_t)list[p] * pitch] = t;
+    if (lane == 0) out[(size_t)sl[p] * pitch] = t;
   }
 }
 
 // x A_g^T | x A_u^T of every slot (DOWN: h A_d^T): a wave per row of A of an expert, for all of its tokens, one or two at a time.
 template <bool DOWN>
 __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
-  __shared__ uint16_t list[KT_MOE_DECODE_MAX_SLOTS];
+  __shared__ uint64_t mask[kSlotWords];
   const int64_t e = a.ids[blockIdx.y];
-  if (e < 0 || e >= a.E) return;
-  int next;
-  const int M = slots_of(a, blockIdx.y, e, list, next);
-  if (!M) return;
-  __syncthreads();
+  int next, M;
+  Slots slots = find_slots(a, blockIdx.y, e, mask, M, next);
+  if (!M || e < 0 || e >= a.E) return;
   const int rows = DOWN ? a.R : 2 * a.R, r = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= rows) return;
   const int K = DOWN ? a.I : a.H;
   const float* w = (DOWN ? a.ad : r < a.R ? a.ag : a.au) + ((size_t)e * a.R + (r < a.R ? r : r - a.R)) * K;
   float* out = (DOWN ? a.ud : a.ua) + r;
-  int m = 0;
-  for (; m + 2 <= M; m += 2) lora_row<DOWN, 2>(a, w, list + m, out, rows);
-  if (m < M) lora_row<DOWN, 1>(a, w, list + m, out, rows);
+  for (int m = 0; m < M; m += 2) {
+    int sl[2];
+    sl[0] = slots.take();
+    if (m + 1 < M) {
+      sl[1] = slots.take();
+      lora_row<DOWN, 2>(a, w, sl, out, rows);
+    } else {
+      lora_row<DOWN, 1>(a, w, sl, out, rows);
+    }
+  }
 }
 
 constexpr int kDownWaves = 8;
@@ -401,22 +519,25 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   u32x4* sf = reinterpret_cast<u32x4*>(hl + 4 * plane);            // [group]: sum and factor of its halves
   uint16_t* sl = reinterpret_cast<uint16_t*>(sf + kDownK);         // [16][kDownK] scales
   float* acc = reinterpret_cast<float*>(lds + kDownWaves * kDownLds);  // [waves][T][16]
-  int U = 0;
-  for (int s0 = 0; s0 < a.S; s0 += 64) {
-    const int s = s0 + lane;
-    const bool lead = s < a.S && a.lead[s];
-    const uint64_t mask = __ballot(lead);
-    if (wave == 0) {
-      if (s < a.S) next[s] = (int16_t)a.next[s];
-      if (lead) {
-        const int at = U + __popcll(mask & ((1ull << lane) - 1));
-        order[at] = (uint16_t)s;
-        expert[at] = (uint16_t)a.ids[s];
-      }
-    }
-    U += __popcll(mask);
+  // the experts' first slots, in order
+  __shared__ uint64_t mask[kSlotWords];
+  const int words = (a.S + 63) / 64;
+  for (int w = wave; w < words; w += kDownWaves) {
+    const int s = w * 64 + lane, i = min(s, a.S - 1);
+    const int lead = a.lead[i], after = a.next[i], id = (int)a.ids[i];
+    const uint64_t m = __ballot(s < a.S && lead);
+    if (lane == 0) mask[w] = m;
+    next[s] = (int16_t)after;
+    expert[s] = (uint16_t)id;
   }
   for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 64 * kDownWaves) acc[i] = 0.f;
+  __syncthreads();
+  int U = 0;
+  for (int w = 0; w < words; ++w) {
+    const uint64_t m = mask[w];
+    if ((w & (kDownWaves - 1)) == wave && (m >> lane & 1)) order[U + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(w * 64 + lane);
+    U += __popcll(m);
+  }
   __syncthreads();
   if (wave < U) {
     const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 2), fb = buffer_of(a.hsf, (size_t)a.S * (a.I / 16) * 8);
@@ -424,7 +545,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
     const size_t n = (size_t)a.H * G;
     // the chunk whose loads are issued next
     int j = wave, s = __builtin_amdgcn_readfirstlane(order[j]), k0 = 0;
-    size_t e = __builtin_amdgcn_readfirstlane(expert[j]);
+    size_t e = __builtin_amdgcn_readfirstlane(expert[s]);
     u32x4 cd[kDownUnits][2], hn[2], sn;
     float2_t fn;
     auto load_codes = [&](int b) {
@@ -484,7 +605,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
           more = j < U;
           if (more) {
             t = __builtin_amdgcn_readfirstlane(order[j]);
-            e = __builtin_amdgcn_readfirstlane(expert[j]);
+            e = __builtin_amdgcn_readfirstlane(expert[t]);
           } else {
             t = s;
           }
@@ -567,6 +688,7 @@ static DecodePlan plan_decode(const Dims& d) {
 static int check_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, Dims* d) {
   const int rc = check_layer_dims(layer, tokens, d, true);
   if (rc) return rc;
+  if (layer->hidden > KT_MOE_DECODE_MAX_HIDDEN) return set_error(KT_RAWINT4_EINVAL, "hidden must be at most 16384");
   if (tokens > KT_MOE_DECODE_MAX_TOKENS || d->Ms > KT_MOE_DECODE_MAX_SLOTS)
     return set_error(KT_RAWINT4_EINVAL, "at most 64 tokens and 1024 token-slots: use kt_rawint4_moe_infer");
   return KT_RAWINT4_OK;
@@ -578,10 +700,8 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     k_decode_lora_a<false><<<dim3((unsigned)((2 * a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  const size_t groups = (size_t)((a.H / 32 + 7) / 8 + 3) / 4 * 32;
-  const size_t scales = (size_t)(a.H / 32) * 64;
-  const int V = a.T < kUpVecs ? a.T : kUpVecs;
-  k_decode_gate_up<MX, LORA><<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, V * groups * 68 + scales, st>>>(a);
+  k_decode_gate_up<MX, LORA>
+      <<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, up_lds(a.H, a.R, a.T < kUpVecs ? a.T : kUpVecs), st>>>(a);
   note_launch();
   if (LORA) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);

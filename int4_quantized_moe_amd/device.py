@@ -119,7 +119,7 @@ class DeviceLayer:
 
     def decode(self, inputs, expert_ids, route_weights, workspace, output=None, stream=None) -> torch.Tensor:
         """infer() for a few tokens (at most KT_MOE_DECODE_MAX_TOKENS, and KT_MOE_DECODE_MAX_SLOTS
-        token-slots), in a decode_workspace()."""
+        token-slots; hidden at most KT_MOE_DECODE_MAX_HIDDEN), in a decode_workspace()."""
         dev, h, k = self.gate_packed.device, self.cfg.hidden, self.cfg.top_k
         if inputs.dim() != 2:
             raise ValueError("inputs must be [tokens, hidden]")

@@ -33,7 +33,7 @@ def test_constants_and_structs_match_the_header():
     for name, value in re.findall(r"#define (KT_\w+) (\d+)", HEADER):
         assert getattr(_lib, name) == int(value), name
         seen += 1
-    assert seen == 9
+    assert seen == 10
     for struct in ("kt_norm", "kt_adamw", "kt_adamw_tensor"):
         body = re.search(r"typedef struct %s \{(.*?)\}" % struct, HEADER, re.S).group(1)
         names = re.findall(r"(\w+);", re.sub(r"/\*.*?\*/", "", body, flags=re.S))
@@ -244,6 +244,7 @@ def test_decode_arguments_are_refused():
 
     _fails(call(layer=None), "layer is NULL")
     _fails(call(layer=_layer(h=48)), "hidden")
+    _fails(call(layer=_layer(h=16416)), "16384")
     _fails(call(layer=_layer(k=9)), "top_k")
     _fails(call(layer=_layer(fmt=2)), "weight_format")
     _fails(call(layer=_layer(limit=NAN)), "swiglu_limit")
