@@ -27,108 +27,162 @@ struct NormArgs {
   int nvec;     // backward: bit i, vector i is wanted; forward: whether the branch is normalised
 };
 
-// A thread's columns: chunks of 8 neighbours (VEC: rows of whole 16 bytes), or
-// single ones a row's threads apart.
-template <bool VEC>
+// A thread's columns: chunks of 8 neighbours, a row's threads apart.  MODE 0: rows
+// are whole chunks.  MODE 1: they are not; the last chunk then is the row's
+// last 8 columns, some of which another thread has too: both store the same
+// values, and sums over a row count them once.  Rows start at any multiple
+// of their type (the hardware's unaligned accesses serve as well).  MODE 2: a row
+// has fewer than 8 columns, which one thread takes one by one.
+// Loads are issued whatever the thread (one without a chunk loads the row's last 8
+// columns and takes zeros instead), so that how many are in flight is known
+// where one is waited for.
+template <int MODE>
 struct Cols {
   int tid, nt, H;
-  __device__ __forceinline__ int at(int j) const { return VEC ? 8 * (tid + (j >> 3) * nt) + (j & 7) : tid + j * nt; }
-  __device__ __forceinline__ bool has(int j) const { return VEC ? 8 * (tid + (j >> 3) * nt) < H : tid + j * nt < H; }
+  __device__ __forceinline__ int own(int chunk) const { return 8 * (tid + chunk * nt); }
+  __device__ __forceinline__ int at(int chunk) const { return MODE == 2 ? 0 : min(own(chunk), H - 8); }
+  __device__ __forceinline__ bool on(int chunk) const { return own(chunk) < H; }
+  // value j, or 0 where it does not exist; for a sum over the row, or where another thread counts it
+  __device__ __forceinline__ float real(int j, float v) const {
+    return on(j >> 3) && (MODE < 2 || (j & 7) < H) ? v : 0.f;
+  }
+  __device__ __forceinline__ float once(int j, float v) const {
+    return MODE != 1 || at(j >> 3) + (j & 7) >= own(j >> 3) ? v : 0.f;
+  }
 };
 
-template <bool VEC, int N>
-__device__ __forceinline__ void load_row(const float* p, const Cols<VEC>& c, float* v) {
-  if (VEC) {
+typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
+typedef float f32x4_u4 __attribute__((ext_vector_type(4), aligned(4)));
+
+// A chunk as it lies in memory, and as numbers; what is not in the row is 0.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4 w;
+  template <int MODE>
+  __device__ __forceinline__ void load(const uint16_t* row, const Cols<MODE>& c, int chunk) {
+    const uint16_t* p = row + c.at(chunk);
+    if (MODE == 0) w = *reinterpret_cast<const u32x4*>(p);
+    if (MODE == 1) w = *reinterpret_cast<const u32x4_u2*>(p);
+    if (MODE == 2) {
 #pragma unroll
-    for (int j = 0; j < N; j += 8) {
-      float4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      if (c.has(j)) {
-        a = *reinterpret_cast<const float4*>(p + c.at(j));
-        b = *reinterpret_cast<const float4*>(p + c.at(j) + 4);
+      for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)p[min(2 * i, c.H - 1)] | (uint32_t)p[min(2 * i + 1, c.H - 1)] << 16;
+    }
+  }
+  template <int MODE>
+  __device__ __forceinline__ void numbers(const Cols<MODE>& c, int chunk, float* v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t t = c.on(chunk) ? w[i] : 0u;
+      v[2 * i] = __uint_as_float(t << 16), v[2 * i + 1] = __uint_as_float(t & 0xffff0000u);
+    }
+    if (MODE == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < c.H ? v[i] : 0.f;
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  floatx4 lo, hi;
+  template <int MODE>
+  __device__ __forceinline__ void load(const float* row, const Cols<MODE>& c, int chunk) {
+    const float* p = row + c.at(chunk);
+    if (MODE == 0) lo = *reinterpret_cast<const floatx4*>(p), hi = *reinterpret_cast<const floatx4*>(p + 4);
+    if (MODE == 1) lo = *reinterpret_cast<const f32x4_u4*>(p), hi = *reinterpret_cast<const f32x4_u4*>(p + 4);
+    if (MODE == 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lo[i] = p[min(i, c.H - 1)], hi[i] = p[min(4 + i, c.H - 1)];
+    }
+  }
+  template <int MODE>
+  __device__ __forceinline__ void numbers(const Cols<MODE>& c, int chunk, float* v) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = c.on(chunk) ? lo[i] : 0.f, v[4 + i] = c.on(chunk) ? hi[i] : 0.f;
+    if (MODE == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < c.H ? v[i] : 0.f;
+    }
+  }
+};
+
+template <int N, typename T, int MODE>
+__device__ __forceinline__ void load_row(const T* p, const Cols<MODE>& c, float* v) {
+#pragma unroll
+  for (int j = 0; j < N; j += 8) {
+    Raw<T> r;
+    r.load(p, c, j >> 3);
+    r.numbers(c, j >> 3, v + j);
+  }
+}
+
+template <int N, int MODE>
+__device__ __forceinline__ void store_row(float* p, const Cols<MODE>& c, const float* v) {
+#pragma unroll
+  for (int j = 0; j < N; j += 8) {
+    const int at = c.at(j >> 3);
+    if (!c.on(j >> 3)) continue;
+    if (MODE == 2) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < c.H) p[i] = v[j + i];
+    } else {
+      const floatx4 lo = {v[j], v[j + 1], v[j + 2], v[j + 3]}, hi = {v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
+      if (MODE == 0) {
+        *reinterpret_cast<floatx4*>(p + at) = lo;
+        *reinterpret_cast<floatx4*>(p + at + 4) = hi;
+      } else {
+        *reinterpret_cast<f32x4_u4*>(p + at) = lo;
+        *reinterpret_cast<f32x4_u4*>(p + at + 4) = hi;
       }
-      v[j] = a.x, v[j + 1] = a.y, v[j + 2] = a.z, v[j + 3] = a.w;
-      v[j + 4] = b.x, v[j + 5] = b.y, v[j + 6] = b.z, v[j + 7] = b.w;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = c.has(j) ? p[c.at(j)] : 0.f;
   }
 }
 
-template <bool VEC, int N>
-__device__ __forceinline__ void load_row(const uint16_t* p, const Cols<VEC>& c, float* v) {
-  if (VEC) {
+template <int N, int MODE>
+__device__ __forceinline__ void store_row(uint16_t* p, const Cols<MODE>& c, const float* v) {
 #pragma unroll
-    for (int j = 0; j < N; j += 8) {
-      u32x4 a = {0, 0, 0, 0};
-      if (c.has(j)) a = *reinterpret_cast<const u32x4*>(p + c.at(j));
+  for (int j = 0; j < N; j += 8) {
+    const int at = c.at(j >> 3);
+    if (!c.on(j >> 3)) continue;
+    if (MODE == 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[j + 2 * i] = __uint_as_float(a[i] << 16);
-        v[j + 2 * i + 1] = __uint_as_float(a[i] & 0xffff0000u);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = c.has(j) ? bf16_to_float(p[c.at(j)]) : 0.f;
-  }
-}
-
-template <bool VEC, int N>
-__device__ __forceinline__ void store_row(float* p, const Cols<VEC>& c, const float* v) {
-  if (VEC) {
-#pragma unroll
-    for (int j = 0; j < N; j += 8) {
-      if (!c.has(j)) continue;
-      *reinterpret_cast<float4*>(p + c.at(j)) = float4{v[j], v[j + 1], v[j + 2], v[j + 3]};
-      *reinterpret_cast<float4*>(p + c.at(j) + 4) = float4{v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (c.has(j)) p[c.at(j)] = v[j];
-  }
-}
-
-template <bool VEC, int N>
-__device__ __forceinline__ void store_row(uint16_t* p, const Cols<VEC>& c, const float* v) {
-  if (VEC) {
-#pragma unroll
-    for (int j = 0; j < N; j += 8) {
-      if (!c.has(j)) continue;
+      for (int i = 0; i < 8; ++i)
+        if (i < c.H) p[i] = float_to_bf16(v[j + i]);
+    } else {
       u32x4 o;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = pack2(float_to_bf16(v[j + 2 * i]), float_to_bf16(v[j + 2 * i + 1]));
-      *reinterpret_cast<u32x4*>(p + c.at(j)) = o;
+      if (MODE == 0)
+        *reinterpret_cast<u32x4*>(p + at) = o;
+      else
+        *reinterpret_cast<u32x4_u2*>(p + at) = o;
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (c.has(j)) p[c.at(j)] = float_to_bf16(v[j]);
   }
 }
 
-// Sums of M values over a row's threads, the same bits in all of them: in a
-// wave by lanes, between waves through LDS in the waves' order.  Two buffers in
-// turn: one barrier a sum.
+// Sums of M values over a row's threads (the waves first .. first + waves - 1
+// of a workgroup), the same bits in all of them: in a wave by lanes, between
+// waves through LDS in the waves' order.  Two buffers in turn: one barrier a sum.
 template <bool ONE, int M>
 struct RowSums {
   float (*buf)[M][kNormMaxWaves];
-  int waves, turn;
+  int first, waves, turn;
   __device__ __forceinline__ void operator()(float* s) {
 #pragma unroll
     for (int i = 0; i < M; ++i) s[i] = wave_sum(s[i]);
     if (ONE) return;
-    const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-      for (int i = 0; i < M; ++i) buf[turn][i][wave] = s[i];
+      for (int i = 0; i < M; ++i) buf[turn][i][threadIdx.x >> 6] = s[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      float t = buf[turn][i][0];
-      for (int w = 1; w < waves; ++w) t += buf[turn][i][w];
+      float t = buf[turn][i][first];
+      for (int w = 1; w < waves; ++w) t += buf[turn][i][first + w];
       s[i] = t;
     }
     turn ^= 1;
@@ -136,20 +190,20 @@ struct RowSums {
 };
 
 // v normalised in place
-template <bool VEC, int N, typename Sums>
-__device__ __forceinline__ void normalise(const NormArgs& a, const Cols<VEC>& c, Sums& sums, float* v) {
+template <int N, typename Sums, int MODE>
+__device__ __forceinline__ void normalise(const NormArgs& a, const Cols<MODE>& c, Sums& sums, float* v) {
   float s = 0.f, mean = 0.f;
   if (a.kind == KT_NORM_LAYER) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) s += v[j];
+    for (int j = 0; j < N; ++j) s += c.once(j, v[j]);
     sums(&s);
     mean = s * a.inv_h;
     s = 0.f;
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    v[j] = c.has(j) ? v[j] - mean : 0.f;
-    s = fmaf(v[j], v[j], s);
+    v[j] = c.real(j, v[j] - mean);
+    s = fmaf(c.once(j, v[j]), v[j], s);
   }
   sums(&s);
   const float r = 1.f / sqrtf(s * a.inv_h + a.eps);
@@ -157,108 +211,156 @@ __device__ __forceinline__ void normalise(const NormArgs& a, const Cols<VEC>& c,
   for (int j = 0; j < N; ++j) v[j] *= r;
 }
 
-template <bool VEC, int N>
-__device__ __forceinline__ void affine(const Cols<VEC>& c, const float* w, const float* bias, float* v) {
+template <int N, int MODE>
+__device__ __forceinline__ void affine(const Cols<MODE>& c, const float* w, const float* bias, float* v) {
   float t[N];
   if (w) {
-    load_row<VEC, N>(w, c, t);
+    load_row<N>(w, c, t);
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] *= t[j];
   }
   if (bias) {
-    load_row<VEC, N>(bias, c, t);
+    load_row<N>(bias, c, t);
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] += t[j];
   }
 }
 
-template <typename S, bool VEC, int VPT, bool ONE>
+template <typename S, int MODE, int VPT, bool ONE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
   constexpr int N = 8 * VPT;
   __shared__ float buf[2][1][kNormMaxWaves];
-  RowSums<ONE, 1> sums{buf, (int)(blockDim.x >> 6), 0};
-  const Cols<VEC> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
+  RowSums<ONE, 1> sums{buf, 0, (int)(blockDim.x >> 6), 0};
+  const Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
   const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
   for (int64_t row = first; row < a.T; row += step) {
     float v[N];
-    load_row<VEC, N>(static_cast<const S*>(a.x) + row * a.H, c, v);
+    load_row<N>(static_cast<const S*>(a.x) + row * a.H, c, v);
     if (a.b) {
       float b[N];
-      load_row<VEC, N>(a.b + row * a.H, c, b);
-      if (a.nvec) normalise<VEC, N>(a, c, sums, b);
-      affine<VEC, N>(c, a.bw, a.bc, b);
+      load_row<N>(a.b + row * a.H, c, b);
+      if (a.nvec) normalise<N>(a, c, sums, b);
+      affine<N>(c, a.bw, a.bc, b);
       const float s = a.tg ? a.scale * a.tg[row] : a.scale;
-      affine<VEC, N>(c, a.gate, nullptr, b);
+      affine<N>(c, a.gate, nullptr, b);
 #pragma unroll
       for (int j = 0; j < N; ++j) v[j] = fmaf(s, b[j], v[j]);
-      if (a.h) store_row<VEC, N>(static_cast<S*>(a.h) + row * a.H, c, v);
+      if (a.h) store_row<N>(static_cast<S*>(a.h) + row * a.H, c, v);
     }
     if (a.y) {
-      normalise<VEC, N>(a, c, sums, v);
-      affine<VEC, N>(c, a.w, a.c, v);
-      store_row<VEC, N>(a.y + row * a.H, c, v);
+      normalise<N>(a, c, sums, v);
+      affine<N>(c, a.w, a.c, v);
+      store_row<N>(a.y + row * a.H, c, v);
     }
   }
 }
 
-// POST: the norm behind the block; BR: a block's output; NEXT: grad_y.
-template <typename S, bool VEC, int VPT, bool ONE, bool BR, bool POST, bool NEXT>
-__global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_bwd(NormArgs a) {
+// A row of the backward's inputs as it lies in memory.
+template <typename S, int MODE, int VPT, bool BR, bool NEXT>
+struct BwdRow {
+  Raw<S> h[VPT], gh[VPT];
+  Raw<uint16_t> y[VPT], b[VPT];
+  float tg;
+  __device__ __forceinline__ void load(const NormArgs& a, const Cols<MODE>& c, int64_t row) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (NEXT) h[i].load(static_cast<const S*>(a.x) + row * a.H, c, i);
+      if (NEXT) y[i].load(a.gy + row * a.H, c, i);
+      if (BR) b[i].load(a.b + row * a.H, c, i);
+      gh[i].load(static_cast<const S*>(a.gh ? a.gh : a.x) + row * a.H, c, i);  // (without grad_h: not used)
+    }
+    if (BR) tg = a.tg ? a.tg[row] : 1.f;
+  }
+};
+
+// The backward.  Teams of waves take a row each, a workgroup has as many teams
+// as fit; a thread keeps its columns and their parts of the parameters'
+// gradients over all rows, which the teams join in LDS at the end: one partial
+// sum a workgroup.  The next row's inputs are on their way while one is worked on,
+// and the vectors lie in LDS (they would have to come from the L2 four times a
+// row, with every wave waiting).
+// BR: a block's output; POST: the norm behind it; NEXT: grad_y; BIAS: d_bias or d_branch_bias.
+template <typename S, int MODE, int VPT, bool ONE, bool BR, bool POST, bool NEXT, bool BIAS>
+__global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a, int waves) {
   constexpr int N = 8 * VPT;
   __shared__ float buf[2][3][kNormMaxWaves];
-  RowSums<ONE, 3> sums{buf, (int)(blockDim.x >> 6), 0};
-  const Cols<VEC> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
-  const int64_t group = ONE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
-  const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
+  extern __shared__ __align__(16) float lds[];  // the vectors in use (up to 8192 columns), [teams][H]
+  const int wave = threadIdx.x >> 6, team = wave / waves, teams = (blockDim.x >> 6) / waves;
+  RowSums<ONE, 3> sums{buf, team * waves, waves, 0};
+  const Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H};
   const bool layer = a.kind == KT_NORM_LAYER;
   float dw[N], dc[N], dbw[N], dbc[N], dg[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) dw[j] = dc[j] = dbw[j] = dbc[j] = dg[j] = 0.f;
-  for (int64_t row = group; row < a.T; row += step) {
-    float v[N], d[N], b[N], e[N];
-    float s[3] = {0.f, 0.f, 0.f};
-    if (NEXT) {
-      load_row<VEC, N>(static_cast<const S*>(a.x) + row * a.H, c, v);
-      load_row<VEC, N>(a.gy + row * a.H, c, e);
-      if (a.w) {
-        load_row<VEC, N>(a.w, c, d);
-      } else {
+  // weight, branch_weight, branch_bias, gate
+  const float* vec[4] = {NEXT ? a.w : nullptr, POST ? a.bw : nullptr, POST ? a.bc : nullptr, BR ? a.gate : nullptr};
+  float* join = lds;
+  if (VPT == 1) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) d[j] = 1.f;
+    for (int i = 0; i < 4; ++i) {
+      if (!vec[i]) continue;
+      if (MODE == 0) {
+        for (int j = threadIdx.x * 4; j < a.H; j += blockDim.x * 4)
+          *reinterpret_cast<floatx4*>(join + j) = *reinterpret_cast<const floatx4*>(vec[i] + j);
+      } else {
+        for (int j = threadIdx.x; j < a.H; j += blockDim.x) join[j] = vec[i][j];
       }
+      vec[i] = join;
+      join += (a.H + 3) & ~3;
     }
-    if (BR) load_row<VEC, N>(a.b + row * a.H, c, b);
+    __syncthreads();
+  }
+  const int64_t step = (int64_t)gridDim.x * teams;
+  int64_t row = (int64_t)blockIdx.x * teams + team;
+  BwdRow<S, MODE, VPT, BR, NEXT> in;
+  in.load(a, c, min(row, a.T - 1));
+  // (all teams make the same number of rounds; one without a row works on the last and keeps nothing)
+  for (int64_t base = (int64_t)blockIdx.x * teams; base < a.T; base += step, row += step) {
+    const bool mine = row < a.T;
+    const int64_t here = min(row, a.T - 1);
+    float v[N], d[N], b[N], e[N];
+    Raw<S> gh[VPT];
+    float s[3] = {0.f, 0.f, 0.f};
+    const float sc = BR ? a.scale * in.tg : 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (NEXT) in.h[i].numbers(c, i, v + 8 * i), in.y[i].numbers(c, i, e + 8 * i);
+      if (BR) in.b[i].numbers(c, i, b + 8 * i);
+      gh[i] = in.gh[i];
+    }
+    in.load(a, c, min(row + step, a.T - 1));
     // means and deviations of h and b; d = grad_y * weight
     float r1 = 0.f, r2 = 0.f, m1 = 0.f, m2 = 0.f;
     if (NEXT) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        dc[j] += e[j];
-        d[j] *= e[j];
-      }
+      for (int j = 0; j < N; ++j) d[j] = e[j];
+      affine<N>(c, vec[0], nullptr, d);
     }
     if (layer && (NEXT || POST)) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (NEXT) s[0] += v[j], s[1] += d[j];
-        if (POST) s[2] += b[j];
+        if (NEXT) s[0] += c.once(j, v[j]), s[1] += c.once(j, d[j]);
+        if (POST) s[2] += c.once(j, b[j]);
       }
       sums(s);
       m1 = s[1] * a.inv_h;
       const float mv = s[0] * a.inv_h, mb = s[2] * a.inv_h;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (NEXT) v[j] = c.has(j) ? v[j] - mv : 0.f;
-        if (POST) b[j] = c.has(j) ? b[j] - mb : 0.f;
+        if (NEXT) v[j] = c.real(j, v[j] - mv);
+        if (POST) b[j] = c.real(j, b[j] - mb);
       }
       s[0] = s[1] = s[2] = 0.f;
     }
     if (NEXT || POST) {
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (NEXT) s[0] = fmaf(v[j], v[j], s[0]), s[1] = fmaf(d[j], v[j], s[1]);
-        if (POST) s[2] = fmaf(b[j], b[j], s[2]);
+        if (NEXT) {
+          const float o = c.once(j, v[j]);
+          s[0] = fmaf(o, v[j], s[0]), s[1] = fmaf(d[j], o, s[1]);
+        }
+        if (POST) s[2] = fmaf(c.once(j, b[j]), b[j], s[2]);
       }
       sums(s);
       if (NEXT) {
@@ -270,22 +372,26 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_bwd(NormArgs a) {
     // d = grad of h
     if (NEXT) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        v[j] *= r1;
-        dw[j] = fmaf(e[j], v[j], dw[j]);
-        d[j] = r1 * (d[j] - m1 - v[j] * m2);
-      }
-    }
-    if (a.gh) {
-      if (NEXT) {
-        load_row<VEC, N>(static_cast<const S*>(a.gh) + row * a.H, c, e);
+      for (int j = 0; j < N; ++j) v[j] *= r1;
+      if (mine) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) d[j] += e[j];
-      } else {
-        load_row<VEC, N>(static_cast<const S*>(a.gh) + row * a.H, c, d);
+        for (int j = 0; j < N; ++j) {
+          dw[j] = fmaf(e[j], v[j], dw[j]);
+          if (BIAS) dc[j] += e[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) d[j] = r1 * (d[j] - m1 - v[j] * m2);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (a.gh) {
+        gh[i].numbers(c, i, e + 8 * i);
+#pragma unroll
+        for (int j = 8 * i; j < 8 * i + 8; ++j) d[j] = NEXT ? d[j] + e[j] : e[j];
       }
     }
-    if (a.h) store_row<VEC, N>(static_cast<S*>(a.h) + row * a.H, c, d);
+    if (a.h && mine) store_row<N>(static_cast<S*>(a.h) + here * a.H, c, d);
     if (!BR) continue;
     // e = n, the block's output behind its norm
 #pragma unroll
@@ -293,54 +399,74 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_bwd(NormArgs a) {
       if (POST) b[j] *= r2;
       e[j] = b[j];
     }
-    if (POST) affine<VEC, N>(c, a.bw, a.bc, e);
+    if (POST) affine<N>(c, vec[1], vec[2], e);
     s[0] = s[1] = s[2] = 0.f;
-    const float sc = a.tg ? a.scale * a.tg[row] : a.scale;
     // the token gate's gradient is without it, the channel gate's with it
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      e[j] = c.has(j) ? e[j] * d[j] : 0.f;
-      dg[j] = fmaf(sc, e[j], dg[j]);
+      e[j] = c.real(j, e[j] * d[j]);
+      if (mine) dg[j] = fmaf(sc, e[j], dg[j]);
     }
-    affine<VEC, N>(c, a.gate, nullptr, d);
-    if (a.gtg) {
-      affine<VEC, N>(c, a.gate, nullptr, e);
+    if (vec[3]) {
+      float g[N];
+      load_row<N>(vec[3], c, g);
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[2] += e[j];
+      for (int j = 0; j < N; ++j) d[j] *= g[j], e[j] *= g[j];
     }
 #pragma unroll
     for (int j = 0; j < N; ++j) {
+      s[2] += c.once(j, e[j]);
       d[j] *= sc;
-      if (POST) {
-        dbw[j] = fmaf(d[j], b[j], dbw[j]);
-        dbc[j] += d[j];
-      }
     }
     if (POST) {
-      affine<VEC, N>(c, a.bw, nullptr, d);
+      if (mine) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          dbw[j] = fmaf(d[j], b[j], dbw[j]);
+          if (BIAS) dbc[j] += d[j];
+        }
+      }
+      affine<N>(c, vec[1], nullptr, d);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        d[j] = c.has(j) ? d[j] : 0.f;
-        s[0] += d[j];
-        s[1] = fmaf(d[j], b[j], s[1]);
+        d[j] = c.real(j, d[j]);
+        const float o = c.once(j, d[j]);
+        s[0] += o;
+        s[1] = fmaf(o, b[j], s[1]);
       }
     }
     if (POST || a.gtg) sums(s);
-    if (a.gtg && (ONE ? (threadIdx.x & 63) == 0 : threadIdx.x == 0)) a.gtg[row] = a.scale * s[2];
+    if (a.gtg && mine && c.tid == 0) a.gtg[here] = a.scale * s[2];
     if (!a.gb) continue;
     if (POST) {
       const float k1 = layer ? s[0] * a.inv_h : 0.f, k2 = s[1] * a.inv_h;
 #pragma unroll
       for (int j = 0; j < N; ++j) d[j] = r2 * (d[j] - k1 - b[j] * k2);
     }
-    store_row<VEC, N>(a.gb + row * a.H, c, d);
+    if (mine) store_row<N>(a.gb + here * a.H, c, d);
   }
-  float* part = a.part + group * 5 * a.H;
-  if (a.nvec & 1) store_row<VEC, N>(part, c, dw);
-  if (a.nvec & 2) store_row<VEC, N>(part + a.H, c, dc);
-  if (a.nvec & 4) store_row<VEC, N>(part + 2 * (int64_t)a.H, c, dbw);
-  if (a.nvec & 8) store_row<VEC, N>(part + 3 * (int64_t)a.H, c, dbc);
-  if (a.nvec & 16) store_row<VEC, N>(part + 4 * (int64_t)a.H, c, dg);
+  float* part = a.part + (int64_t)blockIdx.x * 5 * a.H;
+  auto give = [&](int i, const float* v) {
+    if (!(a.nvec >> i & 1)) return;
+    float* out = part + (int64_t)i * a.H;
+    if (teams == 1) {
+      store_row<N>(out, c, v);
+      return;
+    }
+    __syncthreads();
+    store_row<N>(join + team * a.H, c, v);
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
+      float s = join[j];
+      for (int t = 1; t < teams; ++t) s += join[t * a.H + j];
+      out[j] = s;
+    }
+  };
+  give(0, dw);
+  give(1, dc);
+  give(2, dbw);
+  give(3, dbc);
+  give(4, dg);
 }
 
 // The parameters' gradients from the groups' partial sums: 64 columns by 16
@@ -360,6 +486,7 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormJoin a) {
   float s = 0.f;
   if (col < a.H) {
     const int64_t per = (a.groups + 15) / 16, end = min(a.groups, (run + 1) * per);
+#pragma unroll 8
     for (int64_t g = run * per; g < end; ++g) s += a.part[(g * 5 + vec) * a.H + col];
   }
   red[run][lane] = s;
@@ -372,24 +499,33 @@ __global__ __launch_bounds__(1024) void k_norm_join(NormJoin a) {
 // ---------------------------------------------------------------- host
 
 struct NormShape {
-  bool vec, one;
-  int vpt, threads;
+  bool one;    // a row is one wave's
+  int vpt, waves, threads;
 };
 static NormShape norm_shape(int H) {
   NormShape s;
-  s.vec = H % 8 == 0;
   const int units = (H + 7) / 8;
   s.one = units <= 64;
   s.vpt = units <= 1024 ? 1 : 2;
-  s.threads = s.one ? 256 : (units + 64 * s.vpt - 1) / (64 * s.vpt) * 64;
+  s.waves = (units + 64 * s.vpt - 1) / (64 * s.vpt);
+  s.threads = s.one ? 256 : s.waves * 64;
   return s;
 }
-constexpr int64_t kNormGroups = 512;  // blocks of a backward (waves where a row is one wave's)
 
-// groups of rows that have a partial sum of their own
-static int64_t norm_groups(const NormShape& s, int64_t T) {
-  if (s.one) return (T < 4 * kNormGroups ? (T + 3) / 4 : kNormGroups) * 4;
-  return T < kNormGroups ? T : kNormGroups;
+// The backward's workgroups, one a unit of the chip, and their teams: as many as fit
+// (16 waves), unless fewer give every unit a row.
+constexpr int64_t kNormGroups = 256;
+struct NormTeams {
+  int teams;
+  int64_t groups;
+};
+static NormTeams norm_teams(const NormShape& s, int64_t T) {
+  NormTeams t;
+  const int64_t most = kNormMaxWaves / s.waves, want = (T + kNormGroups - 1) / kNormGroups;
+  t.teams = (int)(want < most ? want : most);
+  const int64_t groups = (T + t.teams - 1) / t.teams;
+  t.groups = groups < kNormGroups ? groups : kNormGroups;
+  return t;
 }
 
 static int check_norm(const kt_norm* n, int32_t tokens) {
@@ -428,39 +564,54 @@ static NormArgs norm_args(const kt_norm* n, int64_t T) {
   return a;
 }
 
-template <typename S, bool VEC>
+template <typename S, bool WHOLE>
 static void launch_norm_fwd(const NormArgs& a, const NormShape& s, hipStream_t st) {
   const int64_t rows = s.one ? (a.T + 3) / 4 : a.T;
   const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
-  if (s.one)
-    k_norm_fwd<S, VEC, 1, true><<<grid, 256, 0, st>>>(a);
+  if (a.H < 8)
+    k_norm_fwd<S, 2, 1, true><<<grid, 256, 0, st>>>(a);
+  else if (s.one)
+    k_norm_fwd<S, WHOLE ? 0 : 1, 1, true><<<grid, 256, 0, st>>>(a);
   else if (s.vpt == 1)
-    k_norm_fwd<S, VEC, 1, false><<<grid, s.threads, 0, st>>>(a);
+    k_norm_fwd<S, WHOLE ? 0 : 1, 1, false><<<grid, s.threads, 0, st>>>(a);
   else
-    k_norm_fwd<S, VEC, 2, false><<<grid, s.threads, 0, st>>>(a);
+    k_norm_fwd<S, WHOLE ? 0 : 1, 2, false><<<grid, s.threads, 0, st>>>(a);
   note_launch();
 }
 
-template <typename S, bool VEC, bool BR, bool POST, bool NEXT>
+template <typename S, bool WHOLE, bool BR, bool POST, bool NEXT, bool BIAS>
 static void launch_norm_bwd(const NormArgs& a, const NormShape& s, hipStream_t st) {
-  const int64_t groups = norm_groups(s, a.T);
-  if (s.one)
-    k_norm_bwd<S, VEC, 1, true, BR, POST, NEXT><<<(unsigned)(groups / 4), 256, 0, st>>>(a);
+  const NormTeams t = norm_teams(s, a.T);
+  const unsigned grid = (unsigned)t.groups, threads = (unsigned)(t.teams * s.waves * 64);
+  const int vectors = (NEXT && a.w) + (POST && a.bw) + (POST && a.bc) + (BR && a.gate);
+  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (s.vpt == 1 ? (size_t)vectors * ((a.H + 3) & ~3) * 4 : 0);
+  if (a.H < 8)
+    k_norm_bwd<S, 2, 1, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
+  else if (s.one)
+    k_norm_bwd<S, WHOLE ? 0 : 1, 1, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
   else if (s.vpt == 1)
-    k_norm_bwd<S, VEC, 1, false, BR, POST, NEXT><<<(unsigned)groups, s.threads, 0, st>>>(a);
+    k_norm_bwd<S, WHOLE ? 0 : 1, 1, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
   else
-    k_norm_bwd<S, VEC, 2, false, BR, POST, NEXT><<<(unsigned)groups, s.threads, 0, st>>>(a);
+    k_norm_bwd<S, WHOLE ? 0 : 1, 2, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
   note_launch();
 }
 
-template <typename S, bool VEC>
+template <typename S, bool WHOLE, bool BIAS>
 static void launch_norm_bwd_parts(const NormArgs& a, const NormShape& s, bool post, hipStream_t st) {
   if (!a.b)
-    a.gy ? launch_norm_bwd<S, VEC, false, false, true>(a, s, st) : launch_norm_bwd<S, VEC, false, false, false>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, false, false, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, false, false, false, false>(a, s, st);
   else if (post)
-    a.gy ? launch_norm_bwd<S, VEC, true, true, true>(a, s, st) : launch_norm_bwd<S, VEC, true, true, false>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, true, true, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, true, true, false, BIAS>(a, s, st);
   else
-    a.gy ? launch_norm_bwd<S, VEC, true, false, true>(a, s, st) : launch_norm_bwd<S, VEC, true, false, false>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, true, false, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, true, false, false, false>(a, s, st);
+}
+
+template <typename S>
+static void launch_norm_bwd_type(const NormArgs& a, const NormShape& s, bool post, bool bias, hipStream_t st) {
+  if (a.H % 8 == 0)
+    bias ? launch_norm_bwd_parts<S, true, true>(a, s, post, st) : launch_norm_bwd_parts<S, true, false>(a, s, post, st);
+  else
+    bias ? launch_norm_bwd_parts<S, false, true>(a, s, post, st) : launch_norm_bwd_parts<S, false, false>(a, s, post, st);
 }
 
 }  // namespace kt
@@ -491,17 +642,20 @@ int kt_norm_fwd(const kt_norm* norm, int32_t tokens, const void* x, const uint16
   const NormShape s = norm_shape(a.H);
   hipStream_t st = static_cast<hipStream_t>(stream);
   begin_launches();
+  const bool whole = a.H % 8 == 0;
   if (norm->stream_type == KT_TYPE_BF16)
-    s.vec ? launch_norm_fwd<uint16_t, true>(a, s, st) : launch_norm_fwd<uint16_t, false>(a, s, st);
+    whole ? launch_norm_fwd<uint16_t, true>(a, s, st) : launch_norm_fwd<uint16_t, false>(a, s, st);
   else
-    s.vec ? launch_norm_fwd<float, true>(a, s, st) : launch_norm_fwd<float, false>(a, s, st);
+    whole ? launch_norm_fwd<float, true>(a, s, st) : launch_norm_fwd<float, false>(a, s, st);
   return finish_launches();
 }
 
 size_t kt_norm_bwd_workspace_bytes(const kt_norm* norm, int32_t tokens) {
   if (check_norm(norm, tokens)) return 0;
   set_error(KT_RAWINT4_OK, "");
-  return round256((size_t)norm_groups(norm_shape(norm->hidden), tokens) * 5 * (size_t)norm->hidden * 4);
+  // (more teams a group may make fewer groups of more tokens: the most over all numbers up to this one)
+  const int64_t groups = tokens < kNormGroups ? tokens : kNormGroups;
+  return round256((size_t)groups * 5 * (size_t)norm->hidden * 4);
 }
 
 int kt_norm_bwd(const kt_norm* norm, int32_t tokens, const void* h, const uint16_t* branch, const float* token_gate,
@@ -551,14 +705,14 @@ int kt_norm_bwd(const kt_norm* norm, int32_t tokens, const void* h, const uint16
   a.part = static_cast<float*>(workspace);
   for (int i = 0; i < 5; ++i) a.nvec |= (params[i] != nullptr) << i;
   const NormShape s = norm_shape(H);
-  const bool post = norm->branch_norm != 0;
+  const bool post = norm->branch_norm != 0, bias = d_bias || d_branch_bias;
   begin_launches();
   if (norm->stream_type == KT_TYPE_BF16)
-    s.vec ? launch_norm_bwd_parts<uint16_t, true>(a, s, post, st) : launch_norm_bwd_parts<uint16_t, false>(a, s, post, st);
+    launch_norm_bwd_type<uint16_t>(a, s, post, bias, st);
   else
-    s.vec ? launch_norm_bwd_parts<float, true>(a, s, post, st) : launch_norm_bwd_parts<float, false>(a, s, post, st);
+    launch_norm_bwd_type<float>(a, s, post, bias, st);
   if (a.nvec) {
-    NormJoin j{a.part, norm_groups(s, tokens), H, accumulate, grad_scale, {d_weight, d_bias, d_branch_weight, d_branch_bias, d_gate}};
+    NormJoin j{a.part, norm_teams(s, tokens).groups, H, accumulate, grad_scale, {d_weight, d_bias, d_branch_weight, d_branch_bias, d_gate}};
     k_norm_join<<<dim3((unsigned)((H + 63) / 64), 5), 1024, 0, st>>>(j);
     note_launch();
   }
