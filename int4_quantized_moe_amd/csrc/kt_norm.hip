@@ -259,7 +259,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
 // A row of the backward's inputs as it lies in memory.
 template <typename S, int MODE, int VPT, bool BR, bool NEXT>
 struct BwdRow {
-  Raw<S> h[VPT], gh[VPT];
+  Raw<S> h[VPT];
   Raw<uint16_t> y[VPT], b[VPT];
   float tg;
   __device__ __forceinline__ void load(const NormArgs& a, const Cols<MODE>& c, int64_t row) {
@@ -268,7 +268,6 @@ struct BwdRow {
       if (NEXT) h[i].load(static_cast<const S*>(a.x) + row * a.H, c, i);
       if (NEXT) y[i].load(a.gy + row * a.H, c, i);
       if (BR) b[i].load(a.b + row * a.H, c, i);
-      gh[i].load(static_cast<const S*>(a.gh ? a.gh : a.x) + row * a.H, c, i);  // (without grad_h: not used)
     }
     if (BR) tg = a.tg ? a.tg[row] : 1.f;
   }
@@ -281,9 +280,10 @@ struct BwdRow {
 // and the vectors lie in LDS (they would have to come from the L2 four times a
 // row, with every wave waiting).
 // BR: a block's output; POST: the norm behind it; NEXT: grad_y; BIAS: d_bias or d_branch_bias.
-template <typename S, int MODE, int VPT, bool ONE, bool BR, bool POST, bool NEXT, bool BIAS>
-__global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a, int waves) {
+template <typename S, int MODE, int VPT, int MOST, bool ONE, bool BR, bool POST, bool NEXT, bool BIAS>
+__global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   constexpr int N = 8 * VPT;
+  constexpr bool AHEAD = VPT == 1 || MOST == 512;
   __shared__ float buf[2][3][kNormMaxWaves];
   extern __shared__ __align__(16) float lds[];  // the vectors in use (up to 8192 columns), [teams][H]
   const int wave = threadIdx.x >> 6, team = wave / waves, teams = (blockDim.x >> 6) / waves;
@@ -296,7 +296,7 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a, int waves) {
   // weight, branch_weight, branch_bias, gate
   const float* vec[4] = {NEXT ? a.w : nullptr, POST ? a.bw : nullptr, POST ? a.bc : nullptr, BR ? a.gate : nullptr};
   float* join = lds;
-  if (VPT == 1) {
+  if (AHEAD) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!vec[i]) continue;
@@ -314,11 +314,12 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a, int waves) {
   const int64_t step = (int64_t)gridDim.x * teams;
   int64_t row = (int64_t)blockIdx.x * teams + team;
   BwdRow<S, MODE, VPT, BR, NEXT> in;
-  in.load(a, c, min(row, a.T - 1));
+  if (AHEAD) in.load(a, c, min(row, a.T - 1));
   // (all teams make the same number of rounds; one without a row works on the last and keeps nothing)
   for (int64_t base = (int64_t)blockIdx.x * teams; base < a.T; base += step, row += step) {
     const bool mine = row < a.T;
     const int64_t here = min(row, a.T - 1);
+    if (!AHEAD) in.load(a, c, here);
     float v[N], d[N], b[N], e[N];
     Raw<S> gh[VPT];
     float s[3] = {0.f, 0.f, 0.f};
@@ -327,9 +328,10 @@ __global__ __launch_bounds__(1024) void k_norm_bwd(NormArgs a, int waves) {
     for (int i = 0; i < VPT; ++i) {
       if (NEXT) in.h[i].numbers(c, i, v + 8 * i), in.y[i].numbers(c, i, e + 8 * i);
       if (BR) in.b[i].numbers(c, i, b + 8 * i);
-      gh[i] = in.gh[i];
+      // (wanted late in the row, which hides its way; without grad_h: not used)
+      gh[i].load(static_cast<const S*>(a.gh ? a.gh : a.x) + here * a.H, c, i);
     }
-    in.load(a, c, min(row + step, a.T - 1));
+    if (AHEAD) in.load(a, c, min(row + step, a.T - 1));
     // means and deviations of h and b; d = grad_y * weight
     float r1 = 0.f, r2 = 0.f, m1 = 0.f, m2 = 0.f;
     if (NEXT) {
@@ -513,15 +515,22 @@ static NormShape norm_shape(int H) {
 }
 
 // The backward's workgroups, one a unit of the chip, and their teams: as many as fit
-// (16 waves), unless fewer give every unit a row.
+// in 16 waves, unless fewer give every unit a row.  Rows of 4097 to 8192 columns take 16
+// columns a thread and 8 waves, whose 256 registers each hold the parameters' gradients
+// and the next row (4096 rows of 7168, everything on: 121 us; 8 columns a thread in 14 waves
+// of 128 registers: 128).  Shorter rows take 8 columns a thread, in as many teams as
+// fit in 16 waves (8192 rows of 4096: 133 us, 4001 of 2049: 71; in 8 waves 172 and 98).
 constexpr int64_t kNormGroups = 256;
 struct NormTeams {
-  int teams;
+  int vpt, waves, teams;
   int64_t groups;
 };
-static NormTeams norm_teams(const NormShape& s, int64_t T) {
+static NormTeams norm_teams(int H, int64_t T) {
   NormTeams t;
-  const int64_t most = kNormMaxWaves / s.waves, want = (T + kNormGroups - 1) / kNormGroups;
+  const int units = (H + 7) / 8;
+  t.vpt = units <= 512 ? 1 : 2;
+  t.waves = (units + 64 * t.vpt - 1) / (64 * t.vpt);
+  const int64_t most = t.vpt == 2 ? 1 : 16 / t.waves, want = (T + kNormGroups - 1) / kNormGroups;
   t.teams = (int)(want < most ? want : most);
   const int64_t groups = (T + t.teams - 1) / t.teams;
   t.groups = groups < kNormGroups ? groups : kNormGroups;
@@ -580,38 +589,40 @@ static void launch_norm_fwd(const NormArgs& a, const NormShape& s, hipStream_t s
 }
 
 template <typename S, bool WHOLE, bool BR, bool POST, bool NEXT, bool BIAS>
-static void launch_norm_bwd(const NormArgs& a, const NormShape& s, hipStream_t st) {
-  const NormTeams t = norm_teams(s, a.T);
-  const unsigned grid = (unsigned)t.groups, threads = (unsigned)(t.teams * s.waves * 64);
+static void launch_norm_bwd(const NormArgs& a, hipStream_t st) {
+  const NormTeams t = norm_teams(a.H, a.T);
+  const unsigned grid = (unsigned)t.groups, threads = (unsigned)(t.teams * t.waves * 64);
   const int vectors = (NEXT && a.w) + (POST && a.bw) + (POST && a.bc) + (BR && a.gate);
-  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (s.vpt == 1 ? (size_t)vectors * ((a.H + 3) & ~3) * 4 : 0);
+  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (a.H <= 8192 ? (size_t)vectors * ((a.H + 3) & ~3) * 4 : 0);
   if (a.H < 8)
-    k_norm_bwd<S, 2, 1, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
-  else if (s.one)
-    k_norm_bwd<S, WHOLE ? 0 : 1, 1, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
-  else if (s.vpt == 1)
-    k_norm_bwd<S, WHOLE ? 0 : 1, 1, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
+    k_norm_bwd<S, 2, 1, 1024, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
+  else if (t.waves == 1)
+    k_norm_bwd<S, WHOLE ? 0 : 1, 1, 1024, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
+  else if (t.vpt == 1)
+    k_norm_bwd<S, WHOLE ? 0 : 1, 1, 1024, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
+  else if (t.waves <= 8)
+    k_norm_bwd<S, WHOLE ? 0 : 1, 2, 512, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
   else
-    k_norm_bwd<S, WHOLE ? 0 : 1, 2, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, s.waves);
+    k_norm_bwd<S, WHOLE ? 0 : 1, 2, 1024, false, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
   note_launch();
 }
 
 template <typename S, bool WHOLE, bool BIAS>
-static void launch_norm_bwd_parts(const NormArgs& a, const NormShape& s, bool post, hipStream_t st) {
+static void launch_norm_bwd_parts(const NormArgs& a, bool post, hipStream_t st) {
   if (!a.b)
-    a.gy ? launch_norm_bwd<S, WHOLE, false, false, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, false, false, false, false>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, false, false, true, BIAS>(a, st) : launch_norm_bwd<S, WHOLE, false, false, false, false>(a, st);
   else if (post)
-    a.gy ? launch_norm_bwd<S, WHOLE, true, true, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, true, true, false, BIAS>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, true, true, true, BIAS>(a, st) : launch_norm_bwd<S, WHOLE, true, true, false, BIAS>(a, st);
   else
-    a.gy ? launch_norm_bwd<S, WHOLE, true, false, true, BIAS>(a, s, st) : launch_norm_bwd<S, WHOLE, true, false, false, false>(a, s, st);
+    a.gy ? launch_norm_bwd<S, WHOLE, true, false, true, BIAS>(a, st) : launch_norm_bwd<S, WHOLE, true, false, false, false>(a, st);
 }
 
 template <typename S>
-static void launch_norm_bwd_type(const NormArgs& a, const NormShape& s, bool post, bool bias, hipStream_t st) {
+static void launch_norm_bwd_type(const NormArgs& a, bool post, bool bias, hipStream_t st) {
   if (a.H % 8 == 0)
-    bias ? launch_norm_bwd_parts<S, true, true>(a, s, post, st) : launch_norm_bwd_parts<S, true, false>(a, s, post, st);
+    bias ? launch_norm_bwd_parts<S, true, true>(a, post, st) : launch_norm_bwd_parts<S, true, false>(a, post, st);
   else
-    bias ? launch_norm_bwd_parts<S, false, true>(a, s, post, st) : launch_norm_bwd_parts<S, false, false>(a, s, post, st);
+    bias ? launch_norm_bwd_parts<S, false, true>(a, post, st) : launch_norm_bwd_parts<S, false, false>(a, post, st);
 }
 
 }  // namespace kt
@@ -704,15 +715,14 @@ int kt_norm_bwd(const kt_norm* norm, int32_t tokens, const void* h, const uint16
   a.gtg = grad_token_gate;
   a.part = static_cast<float*>(workspace);
   for (int i = 0; i < 5; ++i) a.nvec |= (params[i] != nullptr) << i;
-  const NormShape s = norm_shape(H);
   const bool post = norm->branch_norm != 0, bias = d_bias || d_branch_bias;
   begin_launches();
   if (norm->stream_type == KT_TYPE_BF16)
-    launch_norm_bwd_type<uint16_t>(a, s, post, bias, st);
+    launch_norm_bwd_type<uint16_t>(a, post, bias, st);
   else
-    launch_norm_bwd_type<float>(a, s, post, bias, st);
+    launch_norm_bwd_type<float>(a, post, bias, st);
   if (a.nvec) {
-    NormJoin j{a.part, norm_teams(s, tokens).groups, H, accumulate, grad_scale, {d_weight, d_bias, d_branch_weight, d_branch_bias, d_gate}};
+    NormJoin j{a.part, norm_teams(H, tokens).groups, H, accumulate, grad_scale, {d_weight, d_bias, d_branch_weight, d_branch_bias, d_gate}};
     k_norm_join<<<dim3((unsigned)((H + 63) / 64), 5), 1024, 0, st>>>(j);
     note_launch();
   }
