@@ -41,6 +41,11 @@ struct Cols {
   int tid, nt, H;
   __device__ __forceinline__ int own(int chunk) const { return 8 * (tid + chunk * nt); }
   __device__ __forceinline__ int at(int chunk) const { return MODE == 2 ? 0 : min(own(chunk), H - 8); }
+  // (a 32-bit offset in bytes to a row's scalar address)
+  template <typename T>
+  __device__ __forceinline__ T* column(T* row, int chunk) const {
+    return (T*)((char*)row + (uint32_t)at(chunk) * (uint32_t)sizeof(T));
+  }
   __device__ __forceinline__ bool on(int chunk) const { return own(chunk) < H; }
   // value j, or 0 where it does not exist; for a sum over the row, or where another thread counts it
   __device__ __forceinline__ float real(int j, float v) const {
@@ -62,7 +67,7 @@ struct Raw<uint16_t> {
   u32x4 w;
   template <int MODE>
   __device__ __forceinline__ void load(const uint16_t* row, const Cols<MODE>& c, int chunk) {
-    const uint16_t* p = row + c.at(chunk);
+    const uint16_t* p = c.column(row, chunk);
     if (MODE == 0) w = *reinterpret_cast<const u32x4*>(p);
     if (MODE == 1) w = *reinterpret_cast<const u32x4_u2*>(p);
     if (MODE == 2) {
@@ -89,7 +94,7 @@ struct Raw<float> {
   floatx4 lo, hi;
   template <int MODE>
   __device__ __forceinline__ void load(const float* row, const Cols<MODE>& c, int chunk) {
-    const float* p = row + c.at(chunk);
+    const float* p = c.column(row, chunk);
     if (MODE == 0) lo = *reinterpret_cast<const floatx4*>(p), hi = *reinterpret_cast<const floatx4*>(p + 4);
     if (MODE == 1) lo = *reinterpret_cast<const f32x4_u4*>(p), hi = *reinterpret_cast<const f32x4_u4*>(p + 4);
     if (MODE == 2) {
@@ -122,7 +127,7 @@ template <int N, int MODE>
 __device__ __forceinline__ void store_row(float* p, const Cols<MODE>& c, const float* v) {
 #pragma unroll
   for (int j = 0; j < N; j += 8) {
-    const int at = c.at(j >> 3);
+    float* at = c.column(p, j >> 3);
     if (!c.on(j >> 3)) continue;
     if (MODE == 2) {
 #pragma unroll
@@ -131,11 +136,11 @@ __device__ __forceinline__ void store_row(float* p, const Cols<MODE>& c, const f
     } else {
       const floatx4 lo = {v[j], v[j + 1], v[j + 2], v[j + 3]}, hi = {v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
       if (MODE == 0) {
-        *reinterpret_cast<floatx4*>(p + at) = lo;
-        *reinterpret_cast<floatx4*>(p + at + 4) = hi;
+        *reinterpret_cast<floatx4*>(at) = lo;
+        *reinterpret_cast<floatx4*>(at + 4) = hi;
       } else {
-        *reinterpret_cast<f32x4_u4*>(p + at) = lo;
-        *reinterpret_cast<f32x4_u4*>(p + at + 4) = hi;
+        *reinterpret_cast<f32x4_u4*>(at) = lo;
+        *reinterpret_cast<f32x4_u4*>(at + 4) = hi;
       }
     }
   }
@@ -145,7 +150,7 @@ template <int N, int MODE>
 __device__ __forceinline__ void store_row(uint16_t* p, const Cols<MODE>& c, const float* v) {
 #pragma unroll
   for (int j = 0; j < N; j += 8) {
-    const int at = c.at(j >> 3);
+    uint16_t* at = c.column(p, j >> 3);
     if (!c.on(j >> 3)) continue;
     if (MODE == 2) {
 #pragma unroll
@@ -154,18 +159,18 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Cols<MODE>& c, cons
     } else {
       u32x4 o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = pack2(float_to_bf16(v[j + 2 * i]), float_to_bf16(v[j + 2 * i + 1]));
+      for (int i = 0; i < 4; ++i) o[i] = bf16_pair(v[j + 2 * i], v[j + 2 * i + 1]);
       if (MODE == 0)
-        *reinterpret_cast<u32x4*>(p + at) = o;
+        *reinterpret_cast<u32x4*>(at) = o;
       else
-        *reinterpret_cast<u32x4_u2*>(p + at) = o;
+        *reinterpret_cast<u32x4_u2*>(at) = o;
     }
   }
 }
 
 // Sums of M values over a row's threads (the waves first .. first + waves - 1
 // of a workgroup), the same bits in all of them: in a wave by lanes, between
-// waves through LDS in the waves' order.  Two buffers in turn: one barrier a sum.
+// waves through LDS, a wave's sum to each of 16 lanes and by lanes again.  Two buffers in turn: one barrier a sum.
 template <bool ONE, int M>
 struct RowSums {
   float (*buf)[M][kNormMaxWaves];
@@ -181,9 +186,8 @@ struct RowSums {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-      float t = buf[turn][i][first];
-      for (int w = 1; w < waves; ++w) t += buf[turn][i][first + w];
-      s[i] = t;
+      const int w = threadIdx.x & 15;
+      s[i] = row16_sum(w < waves ? buf[turn][i][first + w] : 0.f);
     }
     turn ^= 1;
   }
@@ -232,7 +236,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
   __shared__ float buf[2][1][kNormMaxWaves];
   RowSums<ONE, 1> sums{buf, 0, (int)(blockDim.x >> 6), 0};
   const Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
-  const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
   for (int64_t row = first; row < a.T; row += step) {
     float v[N];
@@ -286,7 +290,8 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   constexpr bool AHEAD = VPT == 1 || MOST == 512;
   __shared__ float buf[2][3][kNormMaxWaves];
   extern __shared__ __align__(16) float lds[];  // the vectors in use (up to 8192 columns), [teams][H]
-  const int wave = threadIdx.x >> 6, team = wave / waves, teams = (blockDim.x >> 6) / waves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (rows' addresses in scalar registers)
+  const int team = wave / waves, teams = (blockDim.x >> 6) / waves;
   RowSums<ONE, 3> sums{buf, team * waves, waves, 0};
   const Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H};
   const bool layer = a.kind == KT_NORM_LAYER;

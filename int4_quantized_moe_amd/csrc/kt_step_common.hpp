@@ -20,6 +20,13 @@ __device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
   a = r.x, b = r.y;
 }
 
+// Two numbers rounded to nearest even, a in the low half, by one instruction; a NaN stays one.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 pair __attribute__((ext_vector_type(2)));
+  const pair p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
 // The sum or maximum over a wave's lanes, the same bits in every lane.
 __device__ __forceinline__ float rows_sum(float v) {
   uint32_t a = __float_as_uint(v), b = a;
