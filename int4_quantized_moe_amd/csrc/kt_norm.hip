@@ -47,19 +47,44 @@ struct Cols {
     return (T*)((char*)row + (uint32_t)at(chunk) * (uint32_t)sizeof(T));
   }
   __device__ __forceinline__ bool on(int chunk) const { return own(chunk) < H; }
-  // value j, or 0 where it does not exist; for a sum over the row, or where another thread counts it
-  __device__ __forceinline__ float real(int j, float v) const {
-    return on(j >> 3) && (MODE < 2 || (j & 7) < H) ? v : 0.f;
+  // 0 for what does not exist
+  template <int N>
+  __device__ __forceinline__ void mask(float* v) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = on(j >> 3) && (MODE < 2 || (j & 7) < H) ? v[j] : 0.f;
   }
-  __device__ __forceinline__ float once(int j, float v) const {
-    return MODE != 1 || at(j >> 3) + (j & 7) >= own(j >> 3) ? v : 0.f;
+  // a thread's part of a sum over the row: without what another thread counts
+  __device__ __forceinline__ float once(int j, float v) const { return at(j >> 3) + (j & 7) >= own(j >> 3) ? v : 0.f; }
+  template <int N>
+  __device__ __forceinline__ float sum(const float* v) const {
+    float s = 0.f;
+    if (MODE != 1) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) s += v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) s += once(j, v[j]);
+    }
+    return s;
+  }
+  template <int N>
+  __device__ __forceinline__ float dot(const float* u, const float* v) const {
+    float s = 0.f;
+    if (MODE != 1) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) s = fmaf(u[j], v[j], s);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) s = fmaf(once(j, u[j]), once(j, v[j]), s);
+    }
+    return s;
   }
 };
 
 typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
 typedef float f32x4_u4 __attribute__((ext_vector_type(4), aligned(4)));
 
-// A chunk as it lies in memory, and as numbers; what is not in the row is 0.
+// A chunk as it lies in memory, and as numbers.
 template <typename T>
 struct Raw;
 template <>
@@ -76,17 +101,9 @@ struct Raw<uint16_t> {
         w[i] = (uint32_t)p[min(2 * i, c.H - 1)] | (uint32_t)p[min(2 * i + 1, c.H - 1)] << 16;
     }
   }
-  template <int MODE>
-  __device__ __forceinline__ void numbers(const Cols<MODE>& c, int chunk, float* v) const {
+  __device__ __forceinline__ void numbers(float* v) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t t = c.on(chunk) ? w[i] : 0u;
-      v[2 * i] = __uint_as_float(t << 16), v[2 * i + 1] = __uint_as_float(t & 0xffff0000u);
-    }
-    if (MODE == 2) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < c.H ? v[i] : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 };
 template <>
@@ -102,14 +119,9 @@ struct Raw<float> {
       for (int i = 0; i < 4; ++i) lo[i] = p[min(i, c.H - 1)], hi[i] = p[min(4 + i, c.H - 1)];
     }
   }
-  template <int MODE>
-  __device__ __forceinline__ void numbers(const Cols<MODE>& c, int chunk, float* v) const {
+  __device__ __forceinline__ void numbers(float* v) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = c.on(chunk) ? lo[i] : 0.f, v[4 + i] = c.on(chunk) ? hi[i] : 0.f;
-    if (MODE == 2) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < c.H ? v[i] : 0.f;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
   }
 };
 
@@ -119,8 +131,9 @@ __device__ __forceinline__ void load_row(const T* p, const Cols<MODE>& c, float*
   for (int j = 0; j < N; j += 8) {
     Raw<T> r;
     r.load(p, c, j >> 3);
-    r.numbers(c, j >> 3, v + j);
+    r.numbers(v + j);
   }
+  c.template mask<N>(v);
 }
 
 template <int N, int MODE>
@@ -196,35 +209,68 @@ struct RowSums {
 // v normalised in place
 template <int N, typename Sums, int MODE>
 __device__ __forceinline__ void normalise(const NormArgs& a, const Cols<MODE>& c, Sums& sums, float* v) {
-  float s = 0.f, mean = 0.f;
+  float s, mean;
   if (a.kind == KT_NORM_LAYER) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) s += c.once(j, v[j]);
+    s = c.template sum<N>(v);
     sums(&s);
     mean = s * a.inv_h;
-    s = 0.f;
-  }
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    v[j] = c.real(j, v[j] - mean);
-    s = fmaf(c.once(j, v[j]), v[j], s);
+    for (int j = 0; j < N; ++j) v[j] -= mean;
+    c.template mask<N>(v);
   }
+  s = c.template dot<N>(v, v);
   sums(&s);
   const float r = 1.f / sqrtf(s * a.inv_h + a.eps);
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] *= r;
 }
 
+// The vectors into LDS as the threads' chunks read them: the first four columns of every
+// chunk, then the last four, so that neighbours' reads meet in no bank.  All loads first.
+template <int MODE>
+__device__ __forceinline__ void spread(const float* const* v, int H, float* out) {
+  const int chunks = (H + 7) / 8;
+  for (int chunk = threadIdx.x; chunk < chunks; chunk += blockDim.x) {
+    const Cols<MODE> c{chunk, 0, H};
+    Raw<float> r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (v[i]) r[i].load(v[i], c, 0);
+    float* to = out + 4 * chunk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!v[i]) continue;
+      *reinterpret_cast<floatx4*>(to) = r[i].lo;
+      *reinterpret_cast<floatx4*>(to + 4 * chunks) = r[i].hi;
+      to += 8 * chunks;
+    }
+  }
+}
 template <int N, int MODE>
+__device__ __forceinline__ void load_spread(const float* p, const Cols<MODE>& c, float* v) {
+  const int chunks = (c.H + 7) / 8;
+#pragma unroll
+  for (int j = 0; j < N; j += 8) {
+    const int chunk = min(c.tid + (j >> 3) * c.nt, chunks - 1);
+    const floatx4 lo = *reinterpret_cast<const floatx4*>(p + 4 * chunk);
+    const floatx4 hi = *reinterpret_cast<const floatx4*>(p + 4 * (chunks + chunk));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[j + i] = lo[i], v[j + 4 + i] = hi[i];
+  }
+  c.template mask<N>(v);
+}
+
+// (SPREAD: the vectors are as spread() leaves them)
+template <int N, bool SPREAD = false, int MODE>
 __device__ __forceinline__ void affine(const Cols<MODE>& c, const float* w, const float* bias, float* v) {
   float t[N];
   if (w) {
-    load_row<N>(w, c, t);
+    SPREAD ? load_spread<N>(w, c, t) : load_row<N>(w, c, t);
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] *= t[j];
   }
   if (bias) {
-    load_row<N>(bias, c, t);
+    SPREAD ? load_spread<N>(bias, c, t) : load_row<N>(bias, c, t);
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] += t[j];
   }
@@ -235,7 +281,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
   constexpr int N = 8 * VPT;
   __shared__ float buf[2][1][kNormMaxWaves];
   RowSums<ONE, 1> sums{buf, 0, (int)(blockDim.x >> 6), 0};
-  const Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
+  Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
   const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
   for (int64_t row = first; row < a.T; row += step) {
@@ -293,7 +339,7 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (rows' addresses in scalar registers)
   const int team = wave / waves, teams = (blockDim.x >> 6) / waves;
   RowSums<ONE, 3> sums{buf, team * waves, waves, 0};
-  const Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H};
+  Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H};
   const bool layer = a.kind == KT_NORM_LAYER;
   float dw[N], dc[N], dbw[N], dbc[N], dg[N];
 #pragma unroll
@@ -302,17 +348,12 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   const float* vec[4] = {NEXT ? a.w : nullptr, POST ? a.bw : nullptr, POST ? a.bc : nullptr, BR ? a.gate : nullptr};
   float* join = lds;
   if (AHEAD) {
+    spread<MODE>(vec, a.H, lds);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (!vec[i]) continue;
-      if (MODE == 0) {
-        for (int j = threadIdx.x * 4; j < a.H; j += blockDim.x * 4)
-          *reinterpret_cast<floatx4*>(join + j) = *reinterpret_cast<const floatx4*>(vec[i] + j);
-      } else {
-        for (int j = threadIdx.x; j < a.H; j += blockDim.x) join[j] = vec[i][j];
-      }
       vec[i] = join;
-      join += (a.H + 3) & ~3;
+      join += (a.H + 7) & ~7;
     }
     __syncthreads();
   }
@@ -324,6 +365,7 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   for (int64_t base = (int64_t)blockIdx.x * teams; base < a.T; base += step, row += step) {
     const bool mine = row < a.T;
     const int64_t here = min(row, a.T - 1);
+    asm volatile("" : "+v"(c.tid));  // (no addresses kept in registers from row to row)
     if (!AHEAD) in.load(a, c, here);
     float v[N], d[N], b[N], e[N];
     Raw<S> gh[VPT];
@@ -331,44 +373,38 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
     const float sc = BR ? a.scale * in.tg : 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (NEXT) in.h[i].numbers(c, i, v + 8 * i), in.y[i].numbers(c, i, e + 8 * i);
-      if (BR) in.b[i].numbers(c, i, b + 8 * i);
+      if (NEXT) in.h[i].numbers(v + 8 * i), in.y[i].numbers(e + 8 * i);
+      if (BR) in.b[i].numbers(b + 8 * i);
       // (wanted late in the row, which hides its way; without grad_h: not used)
       gh[i].load(static_cast<const S*>(a.gh ? a.gh : a.x) + here * a.H, c, i);
     }
     if (AHEAD) in.load(a, c, min(row + step, a.T - 1));
+    if (NEXT) c.template mask<N>(v), c.template mask<N>(e);
+    if (BR) c.template mask<N>(b);
     // means and deviations of h and b; d = grad_y * weight
     float r1 = 0.f, r2 = 0.f, m1 = 0.f, m2 = 0.f;
     if (NEXT) {
 #pragma unroll
       for (int j = 0; j < N; ++j) d[j] = e[j];
-      affine<N>(c, vec[0], nullptr, d);
+      affine<N, AHEAD>(c, vec[0], nullptr, d);
     }
     if (layer && (NEXT || POST)) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (NEXT) s[0] += c.once(j, v[j]), s[1] += c.once(j, d[j]);
-        if (POST) s[2] += c.once(j, b[j]);
-      }
+      if (NEXT) s[0] = c.template sum<N>(v), s[1] = c.template sum<N>(d);
+      if (POST) s[2] = c.template sum<N>(b);
       sums(s);
       m1 = s[1] * a.inv_h;
       const float mv = s[0] * a.inv_h, mb = s[2] * a.inv_h;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        if (NEXT) v[j] = c.real(j, v[j] - mv);
-        if (POST) b[j] = c.real(j, b[j] - mb);
+        if (NEXT) v[j] -= mv;
+        if (POST) b[j] -= mb;
       }
-      s[0] = s[1] = s[2] = 0.f;
+      if (NEXT) c.template mask<N>(v);
+      if (POST) c.template mask<N>(b);
     }
     if (NEXT || POST) {
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (NEXT) {
-          const float o = c.once(j, v[j]);
-          s[0] = fmaf(o, v[j], s[0]), s[1] = fmaf(d[j], o, s[1]);
-        }
-        if (POST) s[2] = fmaf(c.once(j, b[j]), b[j], s[2]);
-      }
+      if (NEXT) s[0] = c.template dot<N>(v, v), s[1] = c.template dot<N>(d, v);
+      if (POST) s[2] = c.template dot<N>(b, b);
       sums(s);
       if (NEXT) {
         r1 = 1.f / sqrtf(s[0] * a.inv_h + a.eps);
@@ -390,13 +426,11 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
 #pragma unroll
       for (int j = 0; j < N; ++j) d[j] = r1 * (d[j] - m1 - v[j] * m2);
     }
+    if (a.gh) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      if (a.gh) {
-        gh[i].numbers(c, i, e + 8 * i);
+      for (int i = 0; i < VPT; ++i) gh[i].numbers(e + 8 * i);
 #pragma unroll
-        for (int j = 8 * i; j < 8 * i + 8; ++j) d[j] = NEXT ? d[j] + e[j] : e[j];
-      }
+      for (int j = 0; j < N; ++j) d[j] = NEXT ? d[j] + e[j] : e[j];
     }
     if (a.h && mine) store_row<N>(static_cast<S*>(a.h) + here * a.H, c, d);
     if (!BR) continue;
@@ -406,25 +440,24 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
       if (POST) b[j] *= r2;
       e[j] = b[j];
     }
-    if (POST) affine<N>(c, vec[1], vec[2], e);
-    s[0] = s[1] = s[2] = 0.f;
+    if (POST) affine<N, AHEAD>(c, vec[1], vec[2], e);
     // the token gate's gradient is without it, the channel gate's with it
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      e[j] = c.real(j, e[j] * d[j]);
+      e[j] *= d[j];
       if (mine) dg[j] = fmaf(sc, e[j], dg[j]);
     }
+    c.template mask<N>(e);
     if (vec[3]) {
       float g[N];
-      load_row<N>(vec[3], c, g);
+      AHEAD ? load_spread<N>(vec[3], c, g) : load_row<N>(vec[3], c, g);
 #pragma unroll
       for (int j = 0; j < N; ++j) d[j] *= g[j], e[j] *= g[j];
     }
+    s[0] = s[1] = 0.f;
+    s[2] = c.template sum<N>(e);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      s[2] += c.once(j, e[j]);
-      d[j] *= sc;
-    }
+    for (int j = 0; j < N; ++j) d[j] *= sc;
     if (POST) {
       if (mine) {
 #pragma unroll
@@ -433,14 +466,10 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
           if (BIAS) dbc[j] += d[j];
         }
       }
-      affine<N>(c, vec[1], nullptr, d);
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        d[j] = c.real(j, d[j]);
-        const float o = c.once(j, d[j]);
-        s[0] += o;
-        s[1] = fmaf(o, b[j], s[1]);
-      }
+      affine<N, AHEAD>(c, vec[1], nullptr, d);
+      c.template mask<N>(d);
+      s[0] = c.template sum<N>(d);
+      s[1] = c.template dot<N>(d, b);
     }
     if (POST || a.gtg) sums(s);
     if (a.gtg && mine && c.tid == 0) a.gtg[here] = a.scale * s[2];
@@ -598,7 +627,7 @@ static void launch_norm_bwd(const NormArgs& a, hipStream_t st) {
   const NormTeams t = norm_teams(a.H, a.T);
   const unsigned grid = (unsigned)t.groups, threads = (unsigned)(t.teams * t.waves * 64);
   const int vectors = (NEXT && a.w) + (POST && a.bw) + (POST && a.bc) + (BR && a.gate);
-  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (a.H <= 8192 ? (size_t)vectors * ((a.H + 3) & ~3) * 4 : 0);
+  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (a.H <= 8192 ? (size_t)vectors * ((a.H + 7) & ~7) * 4 : 0);
   if (a.H < 8)
     k_norm_bwd<S, 2, 1, 1024, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
   else if (t.waves == 1)
