@@ -30,7 +30,8 @@ struct AdamTensor {
 
 // What a step's kernels read, made by k_adamw_begin at the head of the workspace.
 struct AdamControl {
-  float grad_mult, step_size, root_c2, decay;
+  double grad_mult64;
+  float grad_mult, step_size, inv_root_c2, decay;
   int32_t skip;
 };
 
@@ -39,6 +40,7 @@ struct AdamArgs {
   int64_t chunks;
   int count;
   float b1, b1c, b2, b2c, eps;
+  double b1d, b1cd;
   double* part;
   AdamTensor t[kAdamPerLaunch];
 };
@@ -69,7 +71,7 @@ __device__ __forceinline__ void store4(void* p, bool f32, int64_t i, int64_t n, 
       *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
     else
       *reinterpret_cast<u32pair*>(static_cast<uint16_t*>(p) + i) =
-          u32pair{pack2(float_to_bf16(v.x), float_to_bf16(v.y)), pack2(float_to_bf16(v.z), float_to_bf16(v.w))};
+          u32pair{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
     return;
   }
   const float f[4] = {v.x, v.y, v.z, v.w};
@@ -100,28 +102,158 @@ __device__ __forceinline__ void store_codes(void* p, int64_t i, int64_t n, uint3
     if (i + j < n) b[j] = (uint8_t)(w >> (8 * j));
 }
 
-__device__ __forceinline__ float4 decode4(uint32_t w, float scale) {
+__device__ __forceinline__ float4 decode4(uint32_t w) {
   const float2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
-  return float4{a.x * scale, a.y * scale, b.x * scale, b.y * scale};
+  return float4{a.x, a.y, b.x, b.y};
+}
+__device__ __forceinline__ uint32_t codes4(const float* f) {
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+}
+__device__ __forceinline__ float most4(const float* f) {
+  return wave_max(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
 }
 
-// Codes of a block's values and their scale; ROOT: not negative, and positive ones keep a code that is not 0.
-template <bool ROOT>
-__device__ __forceinline__ uint32_t encode4(float4 v, float& scale) {
-  const float amax = wave_max(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+// Codes of a block's roots of v and their scale; positive ones keep a code that is not 0.
+__device__ __forceinline__ uint32_t encode_roots(const float* v, float& scale) {
+  const float amax = most4(v);
   const bool some = !(amax < kTiny);
   const float inv = some ? 448.f / amax : 0.f;
   scale = some ? amax / 448.f : 0.f;
-  float f[4] = {v.x, v.y, v.z, v.w};
+  float f[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float w = f[j] * inv;
-    if (ROOT && some && f[j] > 0.f) w = fmaxf(w, 0x1p-9f);
+    float w = v[j] * inv;
+    if (some && v[j] > 0.f) w = fmaxf(w, 0x1p-9f);
     // (a NaN keeps its place: comparisons with it are false)
-    f[j] = w > 448.f ? 448.f : w < -448.f ? -448.f : w;
+    f[j] = w > 448.f ? 448.f : w;
   }
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true);
+  return codes4(f);
+}
+
+// Codes of a block's m and their scale.  m comes in 64 bits (its parts are exact, so its code is the nearest
+// one; in 32 bits one in 700000 came out on the other side of a tie).
+__device__ __forceinline__ uint32_t encode_means(const double* m, float& scale) {
+  const double mine = fmax(fmax(fabs(m[0]), fabs(m[1])), fmax(fabs(m[2]), fabs(m[3])));
+  const float most = wave_max((float)mine);
+  const bool some = !(most < kTiny);
+  // the largest |m| itself: what it has beyond its 32 bits
+  const float rest = wave_max((float)mine == most ? (float)(mine - (double)most) : -INFINITY);
+  const double amax = (double)most + (double)rest;
+  // (one quotient of 32 bits, made a double's by a step of its equation)
+  double inv = some ? (double)(1.f / most) : 0.0;
+  inv = 448.0 * (inv * fma(-amax, inv, 2.0));
+  scale = some ? most / 448.f : 0.f;
+  float c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    // cut to 32 bits, the last one set if anything was cut: the code's rounding then is that of w (at most 448, or a NaN)
+    const double w = m[j] * inv;
+    const float t = (float)w;
+    const uint32_t b = __float_as_uint(t) - (fabs((double)t) > fabs(w));
+    c[j] = __uint_as_float(b | ((double)t != w));
+  }
+  return codes4(c);
+}
+
+// A lane's four values of a block as they lie in memory.  P: the parameter is 0: bf16, 1: fp32, 2: bf16 with an fp32 master.
+template <int P, bool GF32, bool E8, bool WHOLE>
+struct AdamValues {
+  float4 g, p, m, v;
+  u32pair gw, pw;
+  uint32_t mw, vw;
+  float ms, vs;
+  __device__ __forceinline__ void load(const AdamTensor& t, int64_t block, int64_t i) {
+    const int64_t n = WHOLE ? INT64_MAX : t.n;
+    if (!WHOLE) {
+      g = load4(t.g, GF32, i, n);
+      p = load4(P == 2 ? t.master : t.p, P != 0, i, n);
+    } else {
+      if (GF32) g = *reinterpret_cast<const float4*>(static_cast<const float*>(t.g) + i);
+      if (!GF32) gw = *reinterpret_cast<const u32pair*>(static_cast<const uint16_t*>(t.g) + i);
+      if (P != 0) p = *reinterpret_cast<const float4*>(static_cast<const float*>(P == 2 ? t.master : t.p) + i);
+      if (P == 0) pw = *reinterpret_cast<const u32pair*>(static_cast<const uint16_t*>(t.p) + i);
+    }
+    if (E8) {
+      const int64_t s = block / KT_ADAMW_BLOCK;
+      mw = load_codes(t.m, i, n), ms = t.ms[s];
+      vw = load_codes(t.v, i, n), vs = t.vs[s];
+    } else {
+      m = load4(t.m, true, i, n);
+      v = load4(t.v, true, i, n);
+    }
+  }
+  __device__ __forceinline__ void widen() {
+    if (WHOLE && !GF32) g = wide(gw);
+    if (WHOLE && P == 0) p = wide(pw);
+    if (E8) m = decode4(mw), v = decode4(vw);
+  }
+  static __device__ __forceinline__ float4 wide(u32pair w) {
+    return float4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+  }
+};
+
+template <int P, bool GF32, bool E8, bool WHOLE>
+__device__ __forceinline__ void adam_block(const AdamArgs& a, const AdamControl& ctl, const AdamTensor& t, float decay, int64_t block,
+                                           int64_t i, AdamValues<P, GF32, E8, WHOLE>& x) {
+  const int64_t n = WHOLE ? INT64_MAX : t.n;
+  x.widen();
+  float *pf = &x.p.x, *mf = &x.m.x, *vf = &x.v.x, root[4];
+  const float* gf = &x.g.x;
+  double md[4];
+  const double km = a.b1d * (E8 ? (double)x.ms : 0.0), kg = a.b1cd * ctl.grad_mult64;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float g = gf[j] * ctl.grad_mult;
+    if (E8) {
+      md[j] = fma(km, (double)mf[j], kg * gf[j]);
+      mf[j] = (float)md[j];
+      vf[j] = vf[j] * x.vs;
+      vf[j] = vf[j] * vf[j];
+    } else {
+      mf[j] = a.b1 * mf[j] + a.b1c * g;
+    }
+    vf[j] = a.b2 * vf[j] + a.b2c * (g * g);
+    root[j] = sqrtf(vf[j]);
+    pf[j] = pf[j] * decay - ctl.step_size * mf[j] / (root[j] * ctl.inv_root_c2 + a.eps);
+  }
+  if (P == 2) store4(t.master, true, i, n, x.p);
+  store4(t.p, P == 1, i, n, x.p);
+  if (E8) {
+    float ms, vs;
+    store_codes(t.m, i, n, encode_means(md, ms));
+    store_codes(t.v, i, n, encode_roots(root, vs));
+    const int64_t s = block / KT_ADAMW_BLOCK;
+    if ((threadIdx.x & 63) == 0) t.ms[s] = ms, t.vs[s] = vs;
+  } else {
+    store4(t.m, true, i, n, x.m);
+    store4(t.v, true, i, n, x.v);
+  }
+}
+
+// A wave's blocks of a chunk: all loads of whole ones first.
+template <int P, bool GF32, bool E8>
+__device__ __forceinline__ void adam_chunk(const AdamArgs& a, const AdamControl& ctl, const AdamTensor& t, int64_t base) {
+  const int lane = threadIdx.x & 63;
+  const float decay = t.decay ? ctl.decay : 1.f;
+  constexpr int64_t kStep = 4 * KT_ADAMW_BLOCK;
+  if (base + (kAdamUnits - 1) * kStep + KT_ADAMW_BLOCK <= t.n) {
+    AdamValues<P, GF32, E8, true> x[kAdamUnits];
+#pragma unroll
+    for (int u = 0; u < kAdamUnits; ++u) x[u].load(t, base + u * kStep, base + u * kStep + lane * 4);
+#pragma unroll
+    for (int u = 0; u < kAdamUnits; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+      adam_block(a, ctl, t, decay, base + u * kStep, base + u * kStep + lane * 4, x[u]);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int64_t block = base; block < t.n && block < base + kAdamUnits * kStep; block += kStep) {
+    AdamValues<P, GF32, E8, false> x;
+    x.load(t, block, block + lane * 4);
+    adam_block(a, ctl, t, decay, block, block + lane * 4, x);
+  }
 }
 
 template <bool E8>
@@ -129,47 +261,14 @@ __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   const AdamControl ctl = *a.ctl;
   if (ctl.skip) return;
   const AdamTensor& t = a.t[find_tensor(a, blockIdx.x)];
-  const int64_t n = t.n;
-  const int64_t base = ((int64_t)blockIdx.x - t.first) * kAdamChunk + (threadIdx.x >> 6) * KT_ADAMW_BLOCK;
-  const int lane = threadIdx.x & 63;
-  const float decay = t.decay ? ctl.decay : 1.f;
-#pragma unroll 1
-  for (int u = 0; u < kAdamUnits; ++u) {
-    const int64_t block = base + u * 4 * KT_ADAMW_BLOCK, i = block + lane * 4;
-    if (block >= n) return;
-    float4 g = load4(t.g, t.g_f32, i, n), p = t.master ? load4(t.master, true, i, n) : load4(t.p, t.p_f32, i, n), m, v;
-    if (E8) {
-      const int64_t s = block / KT_ADAMW_BLOCK;
-      m = decode4(load_codes(t.m, i, n), t.ms[s]);
-      v = decode4(load_codes(t.v, i, n), t.vs[s]);
-    } else {
-      m = load4(t.m, true, i, n);
-      v = load4(t.v, true, i, n);
-    }
-    float *pf = &p.x, *mf = &m.x, *vf = &v.x, root[4];
-    const float gf[4] = {g.x, g.y, g.z, g.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float x = gf[j] * ctl.grad_mult;
-      mf[j] = a.b1 * mf[j] + a.b1c * x;
-      if (E8) vf[j] = vf[j] * vf[j];
-      vf[j] = a.b2 * vf[j] + a.b2c * (x * x);
-      root[j] = sqrtf(vf[j]);
-      pf[j] = pf[j] * decay - ctl.step_size * mf[j] / (root[j] / ctl.root_c2 + a.eps);
-    }
-    if (t.master) store4(t.master, true, i, n, p);
-    store4(t.p, t.p_f32, i, n, p);
-    if (E8) {
-      const int64_t s = block / KT_ADAMW_BLOCK;
-      float ms, vs;
-      store_codes(t.m, i, n, encode4<false>(m, ms));
-      store_codes(t.v, i, n, encode4<true>(float4{root[0], root[1], root[2], root[3]}, vs));
-      if (lane == 0) t.ms[s] = ms, t.vs[s] = vs;
-    } else {
-      store4(t.m, true, i, n, m);
-      store4(t.v, true, i, n, v);
-    }
-  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t base = ((int64_t)blockIdx.x - t.first) * kAdamChunk + wave * KT_ADAMW_BLOCK;
+  if (t.p_f32)
+    t.g_f32 ? adam_chunk<1, true, E8>(a, ctl, t, base) : adam_chunk<1, false, E8>(a, ctl, t, base);
+  else if (t.master)
+    t.g_f32 ? adam_chunk<2, true, E8>(a, ctl, t, base) : adam_chunk<2, false, E8>(a, ctl, t, base);
+  else
+    t.g_f32 ? adam_chunk<0, true, E8>(a, ctl, t, base) : adam_chunk<0, false, E8>(a, ctl, t, base);
 }
 
 // Sums of squares of the gradients in 64 bits: a partial sum a block, each over
@@ -233,9 +332,10 @@ __global__ __launch_bounds__(256) void k_adamw_begin(AdamBegin a) {
     b1 *= b1, b2 *= b2;
   }
   const double lr = a.lr_ptr ? (double)*a.lr_ptr : a.lr;
+  c.grad_mult64 = mult;
   c.grad_mult = (float)mult;
   c.step_size = (float)(lr / (1.0 - p1));
-  c.root_c2 = (float)sqrt(1.0 - p2);
+  c.inv_root_c2 = (float)(1.0 / sqrt(1.0 - p2));
   c.decay = (float)(1.0 - lr * a.decay);
   *a.ctl = c;
 }
@@ -318,6 +418,8 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
   a.b2 = (float)hyper->beta2;
   a.b2c = (float)(1.0 - hyper->beta2);
   a.eps = (float)hyper->eps;
+  a.b1d = hyper->beta1;
+  a.b1cd = 1.0 - hyper->beta1;
   double* part = ws_ptr<double>(workspace, 256);
   int parts = 0;
   begin_launches();
