@@ -45,10 +45,11 @@ struct AdamArgs {
   AdamTensor t[kAdamPerLaunch];
 };
 
+// The tensor of a chunk, by a lane a tensor (one after another, a load each would wait for the last).
 __device__ __forceinline__ int find_tensor(const AdamArgs& a, int64_t chunk) {
-  int t = 0;
-  while (t + 1 < a.count && chunk >= a.t[t + 1].first) ++t;
-  return t;
+  const int lane = threadIdx.x & 63, last = a.count - 1;
+  const bool before = a.t[lane < last ? lane : last].first <= chunk && lane <= last;
+  return __popcll(__ballot(before)) - 1;
 }
 
 // four values from i on; those behind n are 0
@@ -259,8 +260,8 @@ __device__ __forceinline__ void adam_chunk(const AdamArgs& a, const AdamControl&
 template <bool E8>
 __global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
   const AdamControl ctl = *a.ctl;
-  if (ctl.skip) return;
   const AdamTensor& t = a.t[find_tensor(a, blockIdx.x)];
+  if (ctl.skip) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t base = ((int64_t)blockIdx.x - t.first) * kAdamChunk + wave * KT_ADAMW_BLOCK;
   if (t.p_f32)

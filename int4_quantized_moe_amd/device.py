@@ -661,6 +661,7 @@ class DeviceAdamW:
             c.count, c.param_type, c.decay = p.numel(), _TYPES[p.dtype], int(name not in no_decay)
             c.param, c.master, c.m, c.v = ptr(p), ptr(s.get("master")), ptr(s["m"]), ptr(s["v"])
             c.m_scale, c.v_scale = ptr(s.get("m_scale")), ptr(s.get("v_scale"))
+        self._slots = [(c, name, p.shape) for c, (name, p) in zip(self._tensors, params.items())]
 
     def step(self, grads: Dict[str, torch.Tensor], grad_scale: float = 1.0, lr: Optional[torch.Tensor] = None,
              stream=None) -> None:
@@ -668,14 +669,15 @@ class DeviceAdamW:
         ``lr`` [1] fp32 on the GPU replaces self.lr, for schedules inside a graph.  Steps of one optimizer
         share its state and workspace: they run one after another."""
         dev = self.device
-        for c, (name, p) in zip(self._tensors, self.params.items()):
+        for c, name, shape in self._slots:
             g = grads.get(name)
             if g is None:
                 raise ValueError(f"grads has no {name!r}")
             kind = _TYPES.get(g.dtype)
             if kind is None:
                 raise ValueError(f"grads[{name!r}] must be torch.float32 or torch.bfloat16, not {g.dtype}")
-            _checked(f"grads[{name!r}]", g, p.shape, g.dtype, dev)
+            if g.shape != shape or g.device != dev or not g.is_contiguous():
+                _checked(f"grads[{name!r}]", g, shape, g.dtype, dev)
             c.grad, c.grad_type = g.data_ptr(), kind
         _checked("lr", lr, (1,), torch.float32, dev)
         if _elsewhere(_gpu(self.step_count)):
