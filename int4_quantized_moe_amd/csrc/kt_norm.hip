@@ -29,8 +29,10 @@ struct NormArgs {
 
 // A thread's columns: chunks of 8 neighbours, a row's threads apart.  MODE 0: rows
 // are whole chunks.  MODE 1: they are not; the last chunk then is the row's
-// last 8 columns, some of which another thread has too: both store the same
-// values, and sums over a row count them once.  Rows start at any multiple
+// last 8 columns, some of which another thread has too: sums over the row count them
+// there, and both store the same values.  Not so in a call in place over several waves: there
+// a wave may have changed them before another reads them, so that only the one that they belong to
+// stores them.  Rows start at any multiple
 // of their type (the hardware's unaligned accesses serve as well).  MODE 2: a row
 // has fewer than 8 columns, which one thread takes one by one.
 // Loads are issued whatever the thread (one without a chunk loads the row's last 8
@@ -39,8 +41,11 @@ struct NormArgs {
 template <int MODE>
 struct Cols {
   int tid, nt, H;
+  bool in_place;  // over several waves
   __device__ __forceinline__ int own(int chunk) const { return 8 * (tid + chunk * nt); }
   __device__ __forceinline__ int at(int chunk) const { return MODE == 2 ? 0 : min(own(chunk), H - 8); }
+  // columns of a chunk that the one before has too
+  __device__ __forceinline__ int shared(int chunk) const { return own(chunk) - at(chunk); }
   // (a 32-bit offset in bytes to a row's scalar address)
   template <typename T>
   __device__ __forceinline__ T* column(T* row, int chunk) const {
@@ -54,7 +59,7 @@ struct Cols {
     for (int j = 0; j < N; ++j) v[j] = on(j >> 3) && (MODE < 2 || (j & 7) < H) ? v[j] : 0.f;
   }
   // a thread's part of a sum over the row: without what another thread counts
-  __device__ __forceinline__ float once(int j, float v) const { return at(j >> 3) + (j & 7) >= own(j >> 3) ? v : 0.f; }
+  __device__ __forceinline__ float once(int j, float v) const { return (j & 7) >= shared(j >> 3) ? v : 0.f; }
   template <int N>
   __device__ __forceinline__ float sum(const float* v) const {
     float s = 0.f;
@@ -146,6 +151,10 @@ __device__ __forceinline__ void store_row(float* p, const Cols<MODE>& c, const f
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < c.H) p[i] = v[j + i];
+    } else if (MODE == 1 && c.in_place && c.shared(j >> 3) > 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= c.shared(j >> 3)) at[i] = v[j + i];
     } else {
       const floatx4 lo = {v[j], v[j + 1], v[j + 2], v[j + 3]}, hi = {v[j + 4], v[j + 5], v[j + 6], v[j + 7]};
       if (MODE == 0) {
@@ -169,6 +178,10 @@ __device__ __forceinline__ void store_row(uint16_t* p, const Cols<MODE>& c, cons
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < c.H) p[i] = float_to_bf16(v[j + i]);
+    } else if (MODE == 1 && c.in_place && c.shared(j >> 3) > 0) {
+#pragma unroll
+      for (int i = 1; i < 8; ++i)
+        if (i >= c.shared(j >> 3)) at[i] = float_to_bf16(v[j + i]);
     } else {
       u32x4 o;
 #pragma unroll
@@ -231,7 +244,7 @@ template <int MODE>
 __device__ __forceinline__ void spread(const float* const* v, int H, float* out) {
   const int chunks = (H + 7) / 8;
   for (int chunk = threadIdx.x; chunk < chunks; chunk += blockDim.x) {
-    const Cols<MODE> c{chunk, 0, H};
+    const Cols<MODE> c{chunk, 0, H, false};
     Raw<float> r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -281,7 +294,7 @@ __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
   constexpr int N = 8 * VPT;
   __shared__ float buf[2][1][kNormMaxWaves];
   RowSums<ONE, 1> sums{buf, 0, (int)(blockDim.x >> 6), 0};
-  Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H};
+  Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H, !ONE && a.h == a.x};
   const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
   for (int64_t row = first; row < a.T; row += step) {
@@ -339,7 +352,7 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // (rows' addresses in scalar registers)
   const int team = wave / waves, teams = (blockDim.x >> 6) / waves;
   RowSums<ONE, 3> sums{buf, team * waves, waves, 0};
-  Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H};
+  Cols<MODE> c{(int)threadIdx.x - team * waves * 64, waves * 64, a.H, !ONE && a.h && a.h == a.gh};
   const bool layer = a.kind == KT_NORM_LAYER;
   float dw[N], dc[N], dbw[N], dbc[N], dg[N];
 #pragma unroll

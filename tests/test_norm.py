@@ -138,6 +138,26 @@ def test_in_place_and_missing_parts(dev, h):
     assert all(torch.equal(some[k], grads[k]) for k in grads)
 
 
+@pytest.mark.parametrize("h", [513, 2049, 4099, 8191, 16383])
+@pytest.mark.parametrize("stream", [BF16, F32])
+def test_odd_rows_in_place(dev, h, stream):
+    """Rows that are no whole chunks, of several waves, without a norm between the reads and the writes."""
+    _say("odd rows in place", h, stream)
+    t = 900
+    i, v, n = _make(12, t, h, stream, post=False, gate="none", bias=False)
+    norm = dev.DeviceNorm(h, **v)
+    hh, y = norm.forward(i["x"], branch=i["branch"])
+    gh = n(t, h).to(stream).cuda()
+    gx, gb = norm.backward(hh, norm.workspace(t), {}, branch=i["branch"], grad_h=gh)
+    for need_y in (False, True):
+        x = i["x"].clone()
+        _, y2 = norm.forward(x, branch=i["branch"], h=x, need_y=need_y)
+        assert torch.equal(x, hh) and (y2 is None or torch.equal(y2, y))
+    g2 = gh.clone()
+    norm.backward(hh, norm.workspace(t), {}, branch=i["branch"], grad_h=g2, grad_x=g2)
+    assert torch.equal(g2, gx)
+
+
 @pytest.mark.parametrize("h", [96, 4096, 77])
 def test_rows_alone_and_shorter_batches(dev, h):
     """A row's outputs do not depend on the batch; one workspace serves shorter batches; empty ones run the window rule."""
