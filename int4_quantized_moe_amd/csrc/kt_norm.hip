@@ -273,6 +273,22 @@ __device__ __forceinline__ void load_spread(const float* p, const Cols<MODE>& c,
   c.template mask<N>(v);
 }
 
+// The thread's own sums of one of two vectors kept there, in the same order.
+template <int N, int MODE, typename Value>
+__device__ __forceinline__ void add_spread(float* p, const Cols<MODE>& c, Value value) {
+  const int chunks = (c.H + 7) / 8;
+#pragma unroll
+  for (int j = 0; j < N; j += 8) {
+    if (!c.on(j >> 3)) continue;
+    floatx4* lo = reinterpret_cast<floatx4*>(p + 4 * (c.tid + (j >> 3) * c.nt));
+    floatx4* hi = lo + chunks;
+    floatx4 s = *lo, t = *hi;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = value(j + i, s[i]), t[i] = value(j + 4 + i, t[i]);
+    *lo = s, *hi = t;
+  }
+}
+
 // (SPREAD: the vectors are as spread() leaves them)
 template <int N, bool SPREAD = false, int MODE>
 __device__ __forceinline__ void affine(const Cols<MODE>& c, const float* w, const float* bias, float* v) {
@@ -357,6 +373,13 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
   float dw[N], dc[N], dbw[N], dbc[N], dg[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) dw[j] = dc[j] = dbw[j] = dbc[j] = dg[j] = 0.f;
+  // (rows above 8192 columns: the registers of 16 waves do not hold all of them)
+  float* const dg_lds = lds;
+  float* const dbw_lds = lds + ((a.H + 7) & ~7);
+  if (!AHEAD) {
+    if (BR) add_spread<N>(dg_lds, c, [](int, float) { return 0.f; });
+    if (POST) add_spread<N>(dbw_lds, c, [](int, float) { return 0.f; });
+  }
   // weight, branch_weight, branch_bias, gate
   const float* vec[4] = {NEXT ? a.w : nullptr, POST ? a.bw : nullptr, POST ? a.bc : nullptr, BR ? a.gate : nullptr};
   float* join = lds;
@@ -458,8 +481,9 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       e[j] *= d[j];
-      if (mine) dg[j] = fmaf(sc, e[j], dg[j]);
+      if (AHEAD && mine) dg[j] = fmaf(sc, e[j], dg[j]);
     }
+    if (!AHEAD) add_spread<N>(dg_lds, c, [&](int j, float s) { return fmaf(sc, e[j], s); });
     c.template mask<N>(e);
     if (vec[3]) {
       float g[N];
@@ -475,10 +499,11 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
       if (mine) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          dbw[j] = fmaf(d[j], b[j], dbw[j]);
+          if (AHEAD) dbw[j] = fmaf(d[j], b[j], dbw[j]);
           if (BIAS) dbc[j] += d[j];
         }
       }
+      if (!AHEAD) add_spread<N>(dbw_lds, c, [&](int j, float s) { return fmaf(d[j], b[j], s); });
       affine<N, AHEAD>(c, vec[1], nullptr, d);
       c.template mask<N>(d);
       s[0] = c.template sum<N>(d);
@@ -511,6 +536,10 @@ __global__ __launch_bounds__(MOST) void k_norm_bwd(NormArgs a, int waves) {
       out[j] = s;
     }
   };
+  if (!AHEAD) {
+    if (BR) load_spread<N>(dg_lds, c, dg);
+    if (POST) load_spread<N>(dbw_lds, c, dbw);
+  }
   give(0, dw);
   give(1, dc);
   give(2, dbw);
@@ -640,7 +669,7 @@ static void launch_norm_bwd(const NormArgs& a, hipStream_t st) {
   const NormTeams t = norm_teams(a.H, a.T);
   const unsigned grid = (unsigned)t.groups, threads = (unsigned)(t.teams * t.waves * 64);
   const int vectors = (NEXT && a.w) + (POST && a.bw) + (POST && a.bc) + (BR && a.gate);
-  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (a.H <= 8192 ? (size_t)vectors * ((a.H + 7) & ~7) * 4 : 0);
+  const size_t lds = (t.teams > 1 ? (size_t)t.teams * a.H * 4 : 0) + (size_t)(a.H <= 8192 ? vectors : (int)BR + (int)POST) * ((a.H + 7) & ~7) * 4;
   if (a.H < 8)
     k_norm_bwd<S, 2, 1, 1024, true, BR, POST, NEXT, BIAS><<<grid, threads, lds, st>>>(a, t.waves);
   else if (t.waves == 1)

@@ -89,6 +89,22 @@ def test_forward_and_backward(dev, t, h, kind, stream, branch, post, gate, bias)
             R.within(name, x, e, 0.5 * b + 2 * R.U * (e.abs() + old[name].double().cpu().abs()))
 
 
+@pytest.mark.parametrize("t,h", [(600, 8193), (523, 16384)])
+@pytest.mark.parametrize("kind,stream,bias", [("layer", F32, True), ("rms", BF16, False)])
+def test_many_tokens_of_wide_rows(dev, t, h, kind, stream, bias):
+    """Several rows a workgroup where not all of the vectors' gradients lie in registers."""
+    _say("wide rows", t, h, kind, stream, bias)
+    i, v, n = _make(t + h, t, h, stream, True, True, "both", bias)
+    norm, hh, _, args = _forward(dev, i, v, kind, 0.75, True)
+    gh, gy = n(t, h).to(stream).cuda(), n(t, h).to(BF16).cuda()
+    grads, gtg = norm.grad_buffers(), torch.empty(t, device="cuda")
+    gx, gb = norm.backward(hh, norm.workspace(t), grads, branch=i["branch"], token_gate=i["token_gate"], grad_h=gh, grad_y=gy, grad_token_gate=gtg)
+    want = S.norm_bwd(hh, i["branch"], i["token_gate"], gh, gy, **args)
+    for name, got, half in [("x", gx, S.rounding(stream)), ("branch", gb, R.UB), ("token_gate", gtg, R.U)] + [(k, x, 2 * R.U) for k, x in grads.items()]:
+        e, b = want[name]
+        R.within(name, got, e, b + half * (e.abs() + b))
+
+
 def test_formula_against_differences(dev):
     """The reference's gradients, and with them the kernels', against central differences of its forward."""
     _say("differences")
