@@ -305,12 +305,13 @@ __device__ __forceinline__ void affine(const Cols<MODE>& c, const float* w, cons
   }
 }
 
-template <typename S, int MODE, int VPT, bool ONE>
+// (IN_PLACE: h is x, in rows of several waves that are no whole chunks)
+template <typename S, int MODE, int VPT, bool ONE, bool IN_PLACE>
 __global__ __launch_bounds__(ONE ? 256 : 1024) void k_norm_fwd(NormArgs a) {
   constexpr int N = 8 * VPT;
   __shared__ float buf[2][1][kNormMaxWaves];
   RowSums<ONE, 1> sums{buf, 0, (int)(blockDim.x >> 6), 0};
-  Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H, !ONE && a.h == a.x};
+  Cols<MODE> c{ONE ? (int)threadIdx.x & 63 : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x, a.H, IN_PLACE};
   const int64_t first = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
   const int64_t step = ONE ? (int64_t)gridDim.x * 4 : gridDim.x;
   for (int64_t row = first; row < a.T; row += step) {
@@ -653,14 +654,17 @@ template <typename S, bool WHOLE>
 static void launch_norm_fwd(const NormArgs& a, const NormShape& s, hipStream_t st) {
   const int64_t rows = s.one ? (a.T + 3) / 4 : a.T;
   const unsigned grid = (unsigned)(rows < 4096 ? rows : 4096);
+  const bool in_place = !WHOLE && !s.one && a.h == a.x;
   if (a.H < 8)
-    k_norm_fwd<S, 2, 1, true><<<grid, 256, 0, st>>>(a);
+    k_norm_fwd<S, 2, 1, true, false><<<grid, 256, 0, st>>>(a);
   else if (s.one)
-    k_norm_fwd<S, WHOLE ? 0 : 1, 1, true><<<grid, 256, 0, st>>>(a);
+    k_norm_fwd<S, WHOLE ? 0 : 1, 1, true, false><<<grid, 256, 0, st>>>(a);
   else if (s.vpt == 1)
-    k_norm_fwd<S, WHOLE ? 0 : 1, 1, false><<<grid, s.threads, 0, st>>>(a);
+    in_place ? k_norm_fwd<S, WHOLE ? 0 : 1, 1, false, !WHOLE><<<grid, s.threads, 0, st>>>(a)
+             : k_norm_fwd<S, WHOLE ? 0 : 1, 1, false, false><<<grid, s.threads, 0, st>>>(a);
   else
-    k_norm_fwd<S, WHOLE ? 0 : 1, 2, false><<<grid, s.threads, 0, st>>>(a);
+    in_place ? k_norm_fwd<S, WHOLE ? 0 : 1, 2, false, !WHOLE><<<grid, s.threads, 0, st>>>(a)
+             : k_norm_fwd<S, WHOLE ? 0 : 1, 2, false, false><<<grid, s.threads, 0, st>>>(a);
   note_launch();
 }
 
