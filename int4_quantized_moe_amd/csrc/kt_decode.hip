@@ -15,6 +15,12 @@
 // down in fp16 with a power of two for 16 columns, rounded by at most 2^-11 of
 // itself (2e-4 of the output, whose own rounding to bf16 is 1.7e-3).
 //
+// 384 experts, 8 a token, 7168 x 2048: one token 39 us (195 MB of codes and scales: 5.0 TB/s), 4 tokens with LoRA of rank
+// 64 196 us, 8 tokens on MXFP4 245 us (1.4 GB: 5.9 TB/s), 32 tokens with rank 16 888 us: the bytes once, at what reads alone reach.
+// More than two tokens an expert cost another pass of gate and up over codes that
+// then mostly lie in the caches, and the multiplications bound it: 8 experts of 4 tokens 100 us, of 8
+// 198, of 32 723; the batched forward, which is made for that, takes 148, 142 and 161.
+//
 // (The MFMAs' operand layout has another row in every lane of 16: their loads
 // touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
 #include "kt_step_common.hpp"

@@ -119,7 +119,8 @@ class DeviceLayer:
 
     def decode(self, inputs, expert_ids, route_weights, workspace, output=None, stream=None) -> torch.Tensor:
         """infer() for a few tokens (at most KT_MOE_DECODE_MAX_TOKENS, and KT_MOE_DECODE_MAX_SLOTS
-        token-slots; hidden at most KT_MOE_DECODE_MAX_HIDDEN), in a decode_workspace()."""
+        token-slots; hidden at most KT_MOE_DECODE_MAX_HIDDEN), in a decode_workspace().  The faster of the
+        two while experts have up to about two tokens each (tokens * top_k <= 2 * num_experts)."""
         dev, h, k = self.gate_packed.device, self.cfg.hidden, self.cfg.top_k
         if inputs.dim() != 2:
             raise ValueError("inputs must be [tokens, hidden]")

@@ -79,6 +79,13 @@ def test_decode_at_the_full_width(dev, r):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("t,e,k,h,i,r,fmt", [(2, 2, 2, 16384, 64, 128, "rawint4"), (1, 3, 2, 16352, 32, 0, "mxfp4"), (5, 2, 1, 32, 16416, 3, "mxfp4")])
+def test_the_widest_layers(dev, t, e, k, h, i, r, fmt):
+    _say("widest", t, e, k, h, i, r, fmt)
+    c = Case(dev, t, e, k, h, i, r, fmt, 0.0, seed=t * h)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("r", [0, 8])
 def test_dropped_and_repeated_ids(dev, r):
     """Ids outside the experts add nothing, a token may hold an expert twice, one without any gets zeros, all tokens may share one expert."""
