@@ -315,11 +315,15 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
   if (LORA) {
     // B times (A x): columns by gate and up by runs of the ranks
     const int c = tid & 15, up = tid >> 4 & 1, part = tid >> 5;
-    const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, r1 = min(a.R, r0 + len);
+    const int len = (a.R + kLoraParts - 1) / kLoraParts, r0 = part * len, n = max(min(a.R - r0, len), 0);
     float t[V] = {};
-    for (int r = r0; r < r1; ++r)
+    // (a column starts its run at its own place: side by side, the columns' ranks would lie in one bank)
+    int r = r0 + c % max(n, 1);
+    for (int i = 0; i < n; ++i) {
 #pragma unroll
       for (int p = 0; p < V; ++p) t[p] = fmaf(l.b[(up * 16 + c) * a.R + r], l.ua[(p * 2 + up) * a.R + r], t[p]);
+      r = r + 1 < r0 + n ? r + 1 : r0;
+    }
 #pragma unroll
     for (int p = 0; p < V; ++p) l.lora[part][up][p][c] = t[p];
   }
