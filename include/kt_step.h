@@ -138,7 +138,7 @@ typedef struct kt_adamw_tensor {
  * one to t, and for every tensor, with g = grad_scale * c * grad:
  *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
- * in fp32, and m of 8-bit states in fp64 (its code is the nearest one); p is the master where there is one.  c = 1, or with max_norm > 0
+ * in fp32; p is the master where there is one.  c = 1, or with max_norm > 0
  * min(1, max_norm / (norm + 1e-6)) by the global norm = |grad_scale * grad|_2 over all tensors (64-bit sums).
  * grad_norm [1] fp32 on the device, or NULL: receives that norm; needed with
  * max_norm > 0.  With it, a norm that is not finite makes the call change

@@ -41,7 +41,6 @@ struct AdamTensor {
 
 // What a step's kernels read, made by k_adamw_begin at the head of the workspace.
 struct AdamControl {
-  double grad_mult64;
   float grad_mult, step_size, inv_root_c2, decay;
   int32_t skip;
 };
@@ -51,7 +50,6 @@ struct AdamArgs {
   int64_t chunks;
   int count;
   float b1, b1c, b2, b2c, eps;
-  double b1d, b1cd;
   double* part;
   AdamTensor t[kAdamPerLaunch];
 };
@@ -126,46 +124,22 @@ __device__ __forceinline__ float most4(const float* f) {
   return wave_max(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
 }
 
-// Codes of a block's roots of v and their scale; positive ones keep a code that is not 0.
-__device__ __forceinline__ uint32_t encode_roots(const float* v, float& scale) {
+// Codes of a block's values and their scale; ROOT: not negative, and positive ones keep a code that is not 0.
+template <bool ROOT>
+__device__ __forceinline__ uint32_t encode4(const float* v, float& scale) {
   const float amax = most4(v);
   const bool some = !(amax < kTiny);
-  const float inv = some ? 448.f / amax : 0.f;
-  scale = some ? amax / 448.f : 0.f;
+  const float inv = some ? 448.f * (1.f / amax) : 0.f;
+  scale = some ? amax * (1.f / 448.f) : 0.f;
   float f[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float w = v[j] * inv;
-    if (some && v[j] > 0.f) w = fmaxf(w, 0x1p-9f);
+    if (ROOT && some && v[j] > 0.f) w = fmaxf(w, 0x1p-9f);
     // (a NaN keeps its place: comparisons with it are false)
-    f[j] = w > 448.f ? 448.f : w;
+    f[j] = w > 448.f ? 448.f : w < -448.f ? -448.f : w;
   }
   return codes4(f);
-}
-
-// Codes of a block's m and their scale.  m comes in 64 bits (its parts are exact, so its code is the nearest
-// one; in 32 bits one in 700000 came out on the other side of a tie).
-__device__ __forceinline__ uint32_t encode_means(const double* m, float& scale) {
-  const double mine = fmax(fmax(fabs(m[0]), fabs(m[1])), fmax(fabs(m[2]), fabs(m[3])));
-  const float most = wave_max((float)mine);
-  const bool some = !(most < kTiny);
-  // the largest |m| itself: what it has beyond its 32 bits
-  const float rest = wave_max((float)mine == most ? (float)(mine - (double)most) : -INFINITY);
-  const double amax = (double)most + (double)rest;
-  // (one quotient of 32 bits, made a double's by a step of its equation)
-  double inv = some ? (double)(1.f / most) : 0.0;
-  inv = 448.0 * (inv * fma(-amax, inv, 2.0));
-  scale = some ? most / 448.f : 0.f;
-  float c[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    // cut to 32 bits, the last one set if anything was cut: the code's rounding then is that of w (at most 448, or a NaN)
-    const double w = m[j] * inv;
-    const float t = (float)w;
-    const uint32_t b = __float_as_uint(t) - (fabs((double)t) > fabs(w));
-    c[j] = __uint_as_float(b | ((double)t != w));
-  }
-  return codes4(c);
 }
 
 // A lane's four values of a block as they lie in memory; the types are known where
@@ -213,19 +187,15 @@ __device__ __forceinline__ void adam_block(const AdamArgs& a, const AdamControl&
   x.widen();
   float *pf = &x.p.x, *mf = &x.m.x, *vf = &x.v.x, root[4];
   const float* gf = &x.g.x;
-  double md[4];
-  const double km = a.b1d * (E8 ? (double)x.ms : 0.0), kg = a.b1cd * ctl.grad_mult64;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float g = gf[j] * ctl.grad_mult;
     if (E8) {
-      md[j] = fma(km, (double)mf[j], kg * gf[j]);
-      mf[j] = (float)md[j];
+      mf[j] = mf[j] * x.ms;
       vf[j] = vf[j] * x.vs;
       vf[j] = vf[j] * vf[j];
-    } else {
-      mf[j] = a.b1 * mf[j] + a.b1c * g;
     }
+    mf[j] = a.b1 * mf[j] + a.b1c * g;
     vf[j] = a.b2 * vf[j] + a.b2c * (g * g);
     root[j] = sqrtf(vf[j]);
     pf[j] = pf[j] * decay - ctl.step_size * mf[j] / (root[j] * ctl.inv_root_c2 + a.eps);
@@ -234,8 +204,8 @@ __device__ __forceinline__ void adam_block(const AdamArgs& a, const AdamControl&
   store4(t.p, P == 1, i, n, x.p);
   if (E8) {
     float ms, vs;
-    store_codes(t.m, i, n, encode_means(md, ms));
-    store_codes(t.v, i, n, encode_roots(root, vs));
+    store_codes(t.m, i, n, encode4<false>(mf, ms));
+    store_codes(t.v, i, n, encode4<true>(root, vs));
     const int64_t s = block / KT_ADAMW_BLOCK;
     if ((threadIdx.x & 63) == 0) t.ms[s] = ms, t.vs[s] = vs;
   } else {
@@ -345,7 +315,6 @@ __global__ __launch_bounds__(256) void k_adamw_begin(AdamBegin a) {
     b1 *= b1, b2 *= b2;
   }
   const double lr = a.lr_ptr ? (double)*a.lr_ptr : a.lr;
-  c.grad_mult64 = mult;
   c.grad_mult = (float)mult;
   c.step_size = (float)(lr / (1.0 - p1));
   c.inv_root_c2 = (float)(1.0 / sqrt(1.0 - p2));
@@ -431,8 +400,6 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
   a.b2 = (float)hyper->beta2;
   a.b2c = (float)(1.0 - hyper->beta2);
   a.eps = (float)hyper->eps;
-  a.b1d = hyper->beta1;
-  a.b1cd = 1.0 - hyper->beta1;
   double* part = ws_ptr<double>(workspace, 256);
   int parts = 0;
   begin_launches();
