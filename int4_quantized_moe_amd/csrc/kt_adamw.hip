@@ -8,9 +8,9 @@
 // before.  So one launch takes the chunks of up to 32 tensors, whatever their sizes, a wave has all its
 // loads in flight before the first is used, and what the whole step shares (the steps made, the
 // clipping, both bias corrections) is worked out once, by a kernel of one workgroup.
-// 170 million values: fp32 with clipping 1010 us, 5.4 TB/s of 32 bytes a value; 8-bit states 516 us, 5.3
-// TB/s; 47 million bf16 ones with masters 262 us, 5.4 TB/s (a copy of 1 GiB: 4.9 to 5.1).
-// Six small tensors: 11 us, 7.4 of them on the GPU (2.4 for what is shared, 5.0).
+// 170 million values: fp32 with clipping 1007 us, 5.4 TB/s of 32 bytes a value; 8-bit states 491 us, 5.5
+// TB/s; 47 million bf16 ones with masters 263 us, 5.3 TB/s (a copy of 1 GiB: 4.9 to 5.1).
+// Six small tensors: 10 to 11 us, 7.4 of them on the GPU (2.4 for what is shared, 5.0).
 #include "kt_step_common.hpp"
 
 #include <math.h>
@@ -239,8 +239,10 @@ __device__ __forceinline__ void adam_chunk(const AdamArgs& a, const AdamControl&
   }
 }
 
+// (Three waves a SIMD: with more, reads and writes of more places are mixed in memory; 8-bit states, fp32
+// parameters and gradients: 491 us, with 4 506, with 6 527, with 2 525; both bf16 398, 393, 380, 463.)
 template <bool E8>
-__global__ __launch_bounds__(256) void k_adamw(AdamArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void k_adamw(AdamArgs a) {
   const AdamControl ctl = *a.ctl;
   const AdamTensor& t = a.t[find_tensor(a, blockIdx.x)];
   if (ctl.skip) return;
