@@ -32,6 +32,7 @@
 namespace kt {
 
 typedef u32x4 u32x4_u2 __attribute__((aligned(2)));
+typedef u32pair u32pair_u2 __attribute__((aligned(2)));
 
 struct DecodeArgs {
   int S, k, T;  // slots, slots a token, tokens
@@ -51,6 +52,8 @@ struct DecodeArgs {
   int32_t* lead;  // [S]: whether the slot is its expert's first
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
   float* ud;      // [S][R]: h A_d^T
+  float* part;    // [parts][T][H]: down's sums, where it is split
+  int by_slot;    // down: a wave's unit is a slot, not an expert
 };
 
 // The slots of an expert, in order, by the masks of all slots that chose it.
@@ -520,7 +523,8 @@ constexpr int kDownLds = kDownK * (64 + 16 + 32);  // bytes a wave: h, sums and 
 // Down and the sum over the slots.  A workgroup has 16 columns of H; its waves
 // take the experts in turn (a wave per expert, the whole contraction), a slot at a
 // time, and add to sums of their own per token, which the end joins in the waves'
-// order.  A wave goes through its slots' contractions in chunks without a stop:
+// order.  Where that leaves the chip idle, the experts are split over the grid's y too,
+// with sums that k_decode_join adds, and by_slot a wave takes single slots.  A wave goes through its slots' contractions in chunks without a stop:
 // while it multiplies one, the codes, scales and h of the next are on their way.
 template <bool MX, bool LORA>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a) {
@@ -540,9 +544,9 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   for (int w = wave; w < words; w += kDownWaves) {
     const int s = w * 64 + lane, i = min(s, a.S - 1);
     const int lead = a.lead[i], after = a.next[i], id = (int)a.ids[i];
-    const uint64_t m = __ballot(s < a.S && lead);
+    const uint64_t m = __ballot(s < a.S && (a.by_slot ? a.ids[i] >= 0 && a.ids[i] < a.E : lead));
     if (lane == 0) mask[w] = m;
-    next[s] = (int16_t)after;
+    next[s] = (int16_t)(a.by_slot ? -1 : after);
     expert[s] = (uint16_t)id;
   }
   for (int i = threadIdx.x; i < kDownWaves * a.T * 16; i += 64 * kDownWaves) acc[i] = 0.f;
@@ -554,12 +558,13 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
     U += __popcll(m);
   }
   __syncthreads();
-  if (wave < U) {
+  const int first = blockIdx.y * kDownWaves + wave, stride = gridDim.y * kDownWaves;
+  if (first < U) {
     const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 2), fb = buffer_of(a.hsf, (size_t)a.S * (a.I / 16) * 8);
     const uint32_t at = (uint32_t)(h0 + row) * G, rows8 = 128u * G;
     const size_t n = (size_t)a.H * G;
     // the chunk whose loads are issued next
-    int j = wave, s = __builtin_amdgcn_readfirstlane(order[j]), k0 = 0;
+    int j = first, s = __builtin_amdgcn_readfirstlane(order[j]), k0 = 0;
     size_t e = __builtin_amdgcn_readfirstlane(expert[s]);
     bool more = true;  // (there is one)
     u32x4 cd[kDownUnits][2], hn[2], sn;
@@ -618,7 +623,7 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
         k0 = 0;
         int t = __builtin_amdgcn_readfirstlane(next[s]);
         if (t < 0) {
-          j += kDownWaves;
+          j += stride;
           more = j < U;
           if (more) {
             t = __builtin_amdgcn_readfirstlane(order[j]);
@@ -679,14 +684,33 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   for (int i = threadIdx.x; i < a.T * 16; i += 64 * kDownWaves) {
     float v = 0.f;
     for (int w = 0; w < kDownWaves; ++w) v += acc[w * a.T * 16 + i];
-    a.out[(size_t)(i >> 4) * a.H + h0 + (i & 15)] = float_to_bf16(v);
+    const size_t o = (size_t)(i >> 4) * a.H + h0 + (i & 15);
+    if (gridDim.y == 1)
+      a.out[o] = float_to_bf16(v);
+    else
+      a.part[(size_t)blockIdx.y * a.T * a.H + o] = v;
   }
+}
+
+__global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a, int parts) {
+  const int n = a.T * a.H, i = (blockIdx.x * 256 + threadIdx.x) * 4;  // (H is a multiple of 32)
+  if (i >= n) return;
+  floatx4 v = *reinterpret_cast<const floatx4*>(a.part + i);
+#pragma unroll 4
+  for (int p = 1; p < parts; ++p) v += *reinterpret_cast<const floatx4*>(a.part + (size_t)p * n + i);
+  *reinterpret_cast<u32pair_u2*>(a.out + i) = u32pair{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
 }
 
 // ---------------------------------------------------------------- host
 
+// Down's parts: two workgroups a unit of the chip, as far as the slots reach.
+static int down_parts(int64_t H, int64_t S) {
+  const int64_t columns = H / 16, want = (512 + columns - 1) / columns, most = (S + kDownWaves - 1) / kDownWaves;
+  return (int)(columns >= 256 ? 1 : want < most ? want : most);
+}
+
 struct DecodePlan {
-  size_t hs, hsf, h, next, lead, ua, ud, total;
+  size_t hs, hsf, h, next, lead, ua, ud, part, total;
 };
 static DecodePlan plan_decode(const Dims& d) {
   DecodePlan p;
@@ -698,7 +722,9 @@ static DecodePlan plan_decode(const Dims& d) {
   p.h = p.hsf + round256(8 * S * (d.I / 16));
   p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
-  p.total = p.ud + round256(4 * S * d.R);
+  p.part = p.ud + round256(4 * S * d.R);
+  const int parts = S ? down_parts(d.H, d.Ms) : 1;
+  p.total = p.part + (parts > 1 ? round256((size_t)4 * parts * d.qlen * d.H) : 0);
   return p;
 }
 
@@ -724,8 +750,14 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  k_decode_down<MX, LORA><<<(unsigned)(a.H / 16), 64 * kDownWaves, kDownWaves * (kDownLds + (size_t)a.T * 64), st>>>(a);
+  const int parts = down_parts(a.H, a.S);
+  k_decode_down<MX, LORA>
+      <<<dim3((unsigned)(a.H / 16), (unsigned)parts), 64 * kDownWaves, kDownWaves * (kDownLds + (size_t)a.T * 64), st>>>(a);
   note_launch();
+  if (parts > 1) {
+    k_decode_join<<<(unsigned)((a.T * a.H / 4 + 255) / 256), 256, 0, st>>>(a, parts);
+    note_launch();
+  }
 }
 
 }  // namespace kt
@@ -775,6 +807,9 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.lead = ws_ptr<int32_t>(workspace, p.lead);
   a.ua = ws_ptr<float>(workspace, p.ua);
   a.ud = ws_ptr<float>(workspace, p.ud);
+  a.part = ws_ptr<float>(workspace, p.part);
+  // (more than two slots an expert: the codes come from the caches all the same)
+  a.by_slot = a.S > 2 * a.E;
   hipStream_t st = static_cast<hipStream_t>(stream);
   begin_launches();
   if (d.fmt == KT_RAWINT4_FORMAT_MXFP4)
