@@ -19,7 +19,8 @@
 // 64 196 us, 8 tokens on MXFP4 245 us (1.4 GB: 5.9 TB/s), 32 tokens with rank 16 888 us: the bytes once, at what reads alone reach.
 // More than two tokens an expert cost another pass of gate and up over codes that
 // then mostly lie in the caches, and the multiplications bound it: 8 experts of 4 tokens 100 us, of 8
-// 198, of 32 723; the batched forward, which is made for that, takes 148, 142 and 161.
+// 198, of 32 718; the batched forward, which is made for that, takes 148, 142 and 161.  Short rows leave the
+// memory idle while a workgroup looks for its slots and fills LDS: 8 tokens of 279 experts, 576 x 2016, 80 us (floor 29).
 //
 // (The MFMAs' operand layout has another row in every lane of 16: their loads
 // touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
@@ -53,7 +54,7 @@ struct DecodeArgs {
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
   float* ud;      // [S][R]: h A_d^T
   float* part;    // [parts][T][H]: down's sums, where it is split
-  int by_slot;    // down: a wave's unit is a slot, not an expert
+  int by_slot;    // a workgroup of gate and up takes two slots, a wave of down one, not all of an expert's
 };
 
 // The slots of an expert, in order, by the masks of all slots that chose it.
@@ -74,9 +75,10 @@ struct Slots {
            (uint32_t)__builtin_amdgcn_readfirstlane((int)m);
   }
 };
-// A workgroup's slots: those of slot s's expert e, if s is its first (count > 0); next: the one after s, or -1.
-// Ends with a barrier.
-__device__ __forceinline__ Slots find_slots(const DecodeArgs& a, int s, int64_t e, uint64_t* mask, int& count, int& next) {
+// A workgroup's slots: those of slot s's expert e, if s is its first (count > 0); next: the one after s, or -1; rank: how many
+// are before s.  Ends with a barrier.
+__device__ __forceinline__ Slots find_slots(const DecodeArgs& a, int s, int64_t e, uint64_t* mask, int& count, int& next,
+                                            int& rank) {
   const int words = (a.S + 63) / 64, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, lane = threadIdx.x & 63;
   for (int w = wave; w < words; w += waves) {
     const int i = w * 64 + lane;
@@ -88,21 +90,21 @@ __device__ __forceinline__ Slots find_slots(const DecodeArgs& a, int s, int64_t 
   r.rest = r.get(0);
   next = -1;
   int n = 0;
-  bool led = false;
+  rank = 0;
   for (int w = 0; w < words; ++w) {
     uint64_t m = r.get(w);
     n += __popcll(m);
     if (w < s >> 6) {
-      led |= m != 0;
+      rank += __popcll(m);
       continue;
     }
     if (w == s >> 6) {
-      led |= (m & ((1ull << (s & 63)) - 1)) != 0;
+      rank += __popcll(m & ((1ull << (s & 63)) - 1));
       m &= ~((2ull << (s & 63)) - 1);
     }
     if (m && next < 0) next = w * 64 + __ffsll((unsigned long long)m) - 1;
   }
-  count = led ? 0 : n;
+  count = rank ? 0 : n;
   return r;
 }
 
@@ -383,7 +385,8 @@ static __host__ __device__ inline size_t up_lds(int H, int R, int V) {
 
 // Gate and up.  A workgroup has 16 columns of I of one expert (its first
 // slot's block; the others leave at once) for all of its tokens, one or two at a time,
-// which lie in LDS.  Its four waves split the contraction.
+// which lie in LDS.  Its four waves split the contraction.  by_slot (more than two slots an expert): every
+// other slot's workgroup stays, with that slot and the next.
 template <bool MX, bool LORA>
 __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -392,8 +395,9 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   __shared__ float lora[LORA ? kLoraParts : 1][2][kUpVecs][16];
   const int slot = blockIdx.y, i0 = blockIdx.x * 16;
   const int64_t e = a.ids[slot];
-  int next = -1, M = 0;
-  Slots slots = find_slots(a, slot, e, mask, M, next);
+  int next = -1, M = 0, rank = 0;
+  Slots slots = find_slots(a, slot, e, mask, M, next, rank);
+  if (a.by_slot) M = rank & 1 ? 0 : next < 0 ? 1 : 2;
   if (e < 0 || e >= a.E) M = 0;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     a.next[slot] = next;
@@ -412,8 +416,12 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   for (int m0 = 0; m0 < M; m0 += kUpVecs) {
     const int nt = min(kUpVecs, M - m0);
     int sl[kUpVecs];
-    sl[0] = slots.take();
-    sl[1] = nt > 1 ? slots.take() : sl[0];
+    if (a.by_slot) {
+      sl[0] = slot, sl[1] = nt > 1 ? next : slot;
+    } else {
+      sl[0] = slots.take();
+      sl[1] = nt > 1 ? slots.take() : sl[0];
+    }
     if (nt == 1)
       gate_up_pass<MX, LORA, 1>(a, e, i0, sl, m0 == 0, l);
     else
@@ -495,8 +503,8 @@ template <bool DOWN>
 __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   __shared__ uint64_t mask[kSlotWords];
   const int64_t e = a.ids[blockIdx.y];
-  int next, M;
-  Slots slots = find_slots(a, blockIdx.y, e, mask, M, next);
+  int next, M, rank;
+  Slots slots = find_slots(a, blockIdx.y, e, mask, M, next, rank);
   if (!M || e < 0 || e >= a.E) return;
   const int rows = DOWN ? a.R : 2 * a.R, r = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (r >= rows) return;
@@ -703,7 +711,8 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a, int parts) {
 
 // ---------------------------------------------------------------- host
 
-// Down's parts: two workgroups a unit of the chip, as far as the slots reach.
+// Down's parts: two workgroups a unit of the chip, as far as the slots reach (8 tokens of 279 experts, 576 x 2016: 116 -> 79 us;
+// 11 of 272, 416 x 1280, rank 64: 182 -> 100); columns that fill the chip by themselves are not split.
 static int down_parts(int64_t H, int64_t S) {
   const int64_t columns = H / 16, want = (512 + columns - 1) / columns, most = (S + kDownWaves - 1) / kDownWaves;
   return (int)(columns >= 256 ? 1 : want < most ? want : most);
@@ -808,7 +817,8 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.ua = ws_ptr<float>(workspace, p.ua);
   a.ud = ws_ptr<float>(workspace, p.ud);
   a.part = ws_ptr<float>(workspace, p.part);
-  // (more than two slots an expert: the codes come from the caches all the same)
+  // (more than two slots an expert on average: codes come from the caches all the same, and one workgroup after the other would
+  // wait for the longest list; 21 tokens of 4 experts, 160 x 1216: 85 -> 65 us, 13 of 8, 6880 x 2912: 205 -> 193)
   a.by_slot = a.S > 2 * a.E;
   hipStream_t st = static_cast<hipStream_t>(stream);
   begin_launches();
