@@ -413,11 +413,12 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
   l.ua = l.b + 32 * a.R;
   l.red = red;
   l.lora = lora;
-  for (int m0 = 0; m0 < M; m0 += kUpVecs) {
-    const int nt = min(kUpVecs, M - m0);
+  // (V: a single token may name an expert twice, but LDS has room for it once)
+  for (int m0 = 0; m0 < M; m0 += V) {
+    const int nt = min(V, M - m0);
     int sl[kUpVecs];
     if (a.by_slot) {
-      sl[0] = slot, sl[1] = nt > 1 ? next : slot;
+      sl[0] = m0 ? next : slot, sl[1] = nt > 1 ? next : sl[0];
     } else {
       sl[0] = slots.take();
       sl[1] = nt > 1 ? slots.take() : sl[0];
@@ -453,7 +454,7 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
       if (c == 0) a.hsf[(size_t)s * (a.I / 16) + blockIdx.x] = float2_t{MX ? 0.f : -1.5f * sum, ldexpf(MX ? 1.f : 16.f, -ex)};
       if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
     }
-    if (m0 + kUpVecs < M) __syncthreads();
+    if (m0 + V < M) __syncthreads();
   }
 }
 

@@ -104,6 +104,15 @@ def test_dropped_and_repeated_ids(dev, r):
     assert not c.run().any()
 
 
+@pytest.mark.parametrize("h,i,e,fmt", [(128, 160, 6, "rawint4"), (2112, 96, 6, "mxfp4"), (7168, 2048, 8, "rawint4"), (64, 64, 1100, "rawint4")])
+@pytest.mark.parametrize("r", [0, 8])
+def test_one_token_that_repeats_an_expert(dev, h, i, e, fmt, r):
+    _say("one token, repeated", h, i, e, fmt, r)
+    c = Case(dev, 1, e, 5, h, i, r, fmt)
+    c.ids[0] = torch.tensor([3, 1, 3, 3, 1])
+    c.check(c.run())
+
+
 def test_decode_equals_itself_anywhere(dev):
     """Results repeat bit for bit, from any workspace, and a larger workspace serves fewer tokens."""
     _say("repeat")
