@@ -19,8 +19,8 @@
 // 64 196 us, 8 tokens on MXFP4 245 us (1.4 GB: 5.9 TB/s), 32 tokens with rank 16 888 us: the bytes once, at what reads alone reach.
 // More than two tokens an expert cost another pass of gate and up over codes that
 // then mostly lie in the caches, and the multiplications bound it: 8 experts of 4 tokens 100 us, of 8
-// 198, of 32 718; the batched forward, which is made for that, takes 148, 142 and 161.  Short rows leave the
-// memory idle while a workgroup looks for its slots and fills LDS: 8 tokens of 279 experts, 576 x 2016, 80 us (floor 29).
+// 198, of 32 718; the batched forward, which is made for that, takes 148, 142 and 161.  Short rows have a kernel of
+// their own for gate and up, and down split over the experts: 8 tokens of 279 experts, 576 x 2016, 58 us (floor 29).
 //
 // (The MFMAs' operand layout has another row in every lane of 16: their loads
 // touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
@@ -377,6 +377,24 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
     }
 }
 
+// Column i0 + c (c: the lane in its 16) of slot s from its two sums: clamp, SwiGLU, and h as down reads it.
+template <bool MX, bool LORA>
+__device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, float uv, int s, int i0, int c) {
+  if (a.limit > 0.f) {
+    // (comparisons that keep a NaN)
+    gv = gv > a.limit ? a.limit : gv;
+    uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
+  }
+  // h in fp16 times a power of two that brings the largest of the 16 below 2^15: a rounding of 2^-11 of the value
+  const float h = gv * sigmoid_f(gv) * uv;
+  const int ex = pow2_exponent_for(row16_max(fabsf(h)));
+  const uint16_t bits = float_to_half_bits(ldexpf(h, ex));
+  a.hs[(size_t)s * a.I + i0 + (MX ? c : perm_pos(c))] = bits;
+  const float sum = row16_sum(half_bits_to_float(bits));
+  if (c == 0) a.hsf[(size_t)s * (a.I / 16) + i0 / 16] = float2_t{MX ? 0.f : -1.5f * sum, ldexpf(MX ? 1.f : 16.f, -ex)};
+  if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
+}
+
 // bytes of dynamic LDS: V tokens, scales, and with LoRA B and ua
 static __host__ __device__ inline size_t up_lds(int H, int R, int V) {
   const size_t G = (size_t)H / 32, Gp = ((G + 7) / 8 + 3) / 4 * 32;
@@ -440,20 +458,188 @@ __global__ __launch_bounds__(256, 4) void k_decode_gate_up(DecodeArgs a) {
         for (int r = 0; r < kLoraParts; ++r) lg += lora[r][0][p][c], lu += lora[r][1][p][c];
         gv = fmaf(a.sc, lg, gv), uv = fmaf(a.sc, lu, uv);
       }
-      if (a.limit > 0.f) {
-        // (comparisons that keep a NaN)
-        gv = gv > a.limit ? a.limit : gv;
-        uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
-      }
-      // h in fp16 times a power of two that brings the largest of the 16 below 2^15: a rounding of 2^-11 of the value
-      const float h = gv * sigmoid_f(gv) * uv;
-      const int ex = pow2_exponent_for(row16_max(fabsf(h)));
-      const uint16_t bits = float_to_half_bits(ldexpf(h, ex));
-      a.hs[(size_t)s * a.I + i0 + (MX ? c : perm_pos(c))] = bits;
-      const float sum = row16_sum(half_bits_to_float(bits));
-      if (c == 0) a.hsf[(size_t)s * (a.I / 16) + blockIdx.x] = float2_t{MX ? 0.f : -1.5f * sum, ldexpf(MX ? 1.f : 16.f, -ex)};
-      if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
+      finish_column<MX, LORA>(a, gv, uv, s, i0, c);
     }
+    if (m0 + V < M) __syncthreads();
+  }
+}
+
+// Gate and up for short rows.  There the time of the kernel above is that of its barriers and of workgroups coming and
+// going, so a workgroup has 64 columns here, 16 a wave, and a wave the whole contraction: one
+// barrier a pair of tokens, and what follows is each wave's own (8 tokens of 279 experts, 576 x 2016: 78 -> 58
+// us; 29 of 78, 1056 x 2496: 242 -> 171; 32 of 384 on MXFP4, 2048 x 3040: 458 -> 388).  Rows are up to 2048 values (one piece
+// of a token a thread, four of the scales).  Few workgroups leave units idle (one token, 2048 x 1024: 22.2 us, here
+// 22.8; two, 2048 x 512: 16.3 and 16.8; one, 1024 x 2048: 16.8 and 14.8), and rows of B above rank 64 are better
+// shared through LDS (16 tokens, rank 128, 1024 x 512: 108, here 117).
+constexpr int kShort = 2048, kShortRank = 64;
+constexpr int64_t kShortColumns = 12288;  // of all slots
+
+template <bool MX, bool LORA, int V>
+__device__ __forceinline__ void gate_up_short(const DecodeArgs& a, int64_t e, int i0, int columns, const int* sl, bool rows,
+                                              const UpLds& l) {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int kw = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c8 = lane & 7, row = lane >> 3;
+  const int G = a.H / 32, units = (G + 7) / 8, Gp = units * 8, plane = Gp * 16;
+  const size_t n = (size_t)a.I * G;
+  const Buffer wg = buffer_of(a.wg + e * n * 16, n * 16), wu = buffer_of(a.wu + e * n * 16, n * 16);
+  // (a wave behind the last column reads the last 16)
+  const int j0 = min(i0 + 16 * kw, a.I - 16);
+  const uint32_t at = (uint32_t)(j0 + row) * G, rows8 = 128u * G;
+  u32x4 tv[V], sv[kStage];
+  float uv[V];
+#pragma unroll
+  for (int p = 0; p < V; ++p)  // (a row has at most 256 pieces)
+    tv[p] = *(reinterpret_cast<const u32x4*>(a.x + (size_t)(sl[p] / a.k) * a.H) + min(tid, G * 4 - 1));
+  if (LORA) {
+#pragma unroll
+    for (int p = 0; p < V; ++p) uv[p] = a.ua[(size_t)sl[p] * 2 * a.R + min(tid, 2 * a.R - 1)];
+  }
+  const int pieces = columns * G / 8;
+  if (rows) stage_load<u32x4_u2>(a.sg + e * n + (size_t)i0 * G, a.su + e * n + (size_t)i0 * G, pieces, tid, sv);
+  __builtin_amdgcn_sched_barrier(0);
+  u32x4 cd[kUpDepth][4];
+  auto load = [&](int u, int b) {
+    const uint32_t o = (u < units ? at + min(8 * u + c8, G - 1) : (uint32_t)j0 * G) * 16;
+    cd[b][0] = buffer16<kCodes>(wg, o, 0);
+    cd[b][1] = buffer16<kCodes>(wg, o, rows8);
+    cd[b][2] = buffer16<kCodes>(wu, o, 0);
+    cd[b][3] = buffer16<kCodes>(wu, o, rows8);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int b = 0; b < kUpDepth; ++b) load(b, b);
+  if (rows) stage_store(l.scales, pieces, tid, sv);
+#pragma unroll
+  for (int p = 0; p < V; ++p) {
+    u32x4 w = tv[p];
+    if (tid >= G * 4) w = u32x4{0, 0, 0, 0};
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += bf_lo(w[j]) + bf_hi(w[j]);
+    s += dpp_f<0xB1>(s);
+    s += dpp_f<0x4E>(s);
+    if (tid < Gp * 4) {
+      *reinterpret_cast<u32x4*>(l.x + p * 4 * plane + ((tid & 3) * Gp + (tid >> 2)) * 16) = MX ? w : order8(w);
+      if ((tid & 3) == 0) l.sums[p * Gp + (tid >> 2)] = MX ? 0.f : -1.5f * s;
+    }
+    if (LORA && tid < 2 * a.R) l.ua[p * 2 * a.R + tid] = uv[p];
+  }
+  __syncthreads();
+  float lg[V] = {}, lu[V] = {};
+  if (LORA) {
+    // B times (A x): a lane takes every fourth rank of a column
+    const int c = lane & 15;
+    const float *bg = a.bg + ((size_t)e * a.I + j0 + c) * a.R, *bu = a.bu + ((size_t)e * a.I + j0 + c) * a.R;
+#pragma unroll 4
+    for (int r = lane >> 4; r < a.R; r += 4) {
+      const float g = bg[r], u = bu[r];
+#pragma unroll
+      for (int p = 0; p < V; ++p) {
+        lg[p] = fmaf(g, l.ua[p * 2 * a.R + r], lg[p]);
+        lu[p] = fmaf(u, l.ua[(p * 2 + 1) * a.R + r], lu[p]);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < V; ++p) lg[p] = rows_sum(lg[p]), lu[p] = rows_sum(lu[p]);
+  }
+  const DotConsts dc = dot_consts<false>();
+  const uint16_t* sc = l.scales + (j0 - i0 + row) * G;
+  float acc[4][V] = {};
+  for (int v = 0; v < units; v += kUpDepth) {
+#pragma unroll
+    for (int b = 0; b < kUpDepth; ++b) {
+      if (v + b < units) {
+        const int g = 8 * (v + b) + c8;
+        Vec x[V];
+        float sum[V];
+#pragma unroll
+        for (int p = 0; p < V; ++p) {
+          read_vec(l.x + p * 4 * plane, g, plane, x[p]);
+          sum[p] = l.sums[p * Gp + g];
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float s = bf16_to_float(sc[((t >> 1) * columns + (t & 1) * 8) * G + min(g, G - 1)]);
+          float d[V];
+#pragma unroll
+          for (int p = 0; p < V; ++p) d[p] = sum[p];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const u32x4 w = decode8<MX, false>(cd[b][t][j], dc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int p = 0; p < V; ++p) d[p] = dot2<false>(w[i], x[p].v[j][i], d[p]);
+          }
+#pragma unroll
+          for (int p = 0; p < V; ++p) acc[t][p] = fmaf(s, d[p], acc[t][p]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      load(v + b + kUpDepth, b);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int p = 0; p < V; ++p) {
+      const float v = eight_sum(acc[t][p]);
+      if (c8 == 0) l.red[t >> 1][kw][p][(t & 1) * 8 + row] = v;
+    }
+  wave_fence();
+  if (lane < 16 * V && 16 * kw < columns) {
+    const int c = lane & 15, p = lane >> 4;
+    const float by = MX ? 1.f : 16.f;
+    float gv = by * l.red[0][kw][p][c], uw = by * l.red[1][kw][p][c];
+    if (LORA) gv = fmaf(a.sc, V > 1 && p ? lg[V - 1] : lg[0], gv), uw = fmaf(a.sc, V > 1 && p ? lu[V - 1] : lu[0], uw);
+    finish_column<MX, LORA>(a, gv, uw, p ? sl[V - 1] : sl[0], j0, c);
+  }
+}
+
+// bytes of dynamic LDS: V tokens, scales of 64 columns, and with LoRA ua
+static __host__ __device__ inline size_t short_lds(int H, int R, int V) {
+  const size_t G = (size_t)H / 32, Gp = (G + 7) / 8 * 8;
+  return V * Gp * 68 + 256 * G + 8 * (size_t)V * R;
+}
+
+template <bool MX, bool LORA>
+__global__ __launch_bounds__(256, 4) void k_decode_gate_up_short(DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint64_t mask[kSlotWords];
+  __shared__ float red[2][4][kUpVecs][16];
+  const int slot = blockIdx.y, i0 = blockIdx.x * 64, columns = min(64, a.I - i0);
+  const int64_t e = a.ids[slot];
+  int next = -1, M = 0, rank = 0;
+  Slots slots = find_slots(a, slot, e, mask, M, next, rank);
+  if (a.by_slot) M = rank & 1 ? 0 : next < 0 ? 1 : 2;
+  if (e < 0 || e >= a.E) M = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.next[slot] = next;
+    a.lead[slot] = M > 0;
+  }
+  if (!M) return;
+  const int G = a.H / 32, Gp = (G + 7) / 8 * 8, V = min(kUpVecs, a.T);
+  UpLds l{};
+  l.x = lds;
+  l.sums = reinterpret_cast<float*>(lds + V * Gp * 64);
+  l.scales = reinterpret_cast<uint16_t*>(l.sums + V * Gp);
+  l.ua = reinterpret_cast<float*>(l.scales + 128 * G);
+  l.red = red;
+  // (V: a single token may name an expert twice, but LDS has room for it once)
+  for (int m0 = 0; m0 < M; m0 += V) {
+    const int nt = min(V, M - m0);
+    int sl[kUpVecs];
+    if (a.by_slot) {
+      sl[0] = m0 ? next : slot, sl[1] = nt > 1 ? next : sl[0];
+    } else {
+      sl[0] = slots.take();
+      sl[1] = nt > 1 ? slots.take() : sl[0];
+    }
+    if (nt == 1)
+      gate_up_short<MX, LORA, 1>(a, e, i0, columns, sl, m0 == 0, l);
+    else
+      gate_up_short<MX, LORA, kUpVecs>(a, e, i0, columns, sl, m0 == 0, l);
     if (m0 + V < M) __syncthreads();
   }
 }
@@ -753,8 +939,11 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     k_decode_lora_a<false><<<dim3((unsigned)((2 * a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  k_decode_gate_up<MX, LORA>
-      <<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, up_lds(a.H, a.R, a.T < kUpVecs ? a.T : kUpVecs), st>>>(a);
+  const int V = a.T < kUpVecs ? a.T : kUpVecs;
+  if (a.H <= kShort && a.R <= kShortRank && (int64_t)a.I * a.S >= kShortColumns)
+    k_decode_gate_up_short<MX, LORA><<<dim3((unsigned)((a.I + 63) / 64), (unsigned)a.S), 256, short_lds(a.H, a.R, V), st>>>(a);
+  else
+    k_decode_gate_up<MX, LORA><<<dim3((unsigned)(a.I / 16), (unsigned)a.S), 256, up_lds(a.H, a.R, V), st>>>(a);
   note_launch();
   if (LORA) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);

@@ -113,6 +113,18 @@ def test_one_token_that_repeats_an_expert(dev, h, i, e, fmt, r):
     c.check(c.run())
 
 
+# above and below what short rows take: slots x intermediate, hidden, rank; intermediates that end inside a workgroup's columns
+@pytest.mark.parametrize("t,e,k,h,i", [(2, 6, 3, 160, 2048), (2, 6, 3, 160, 2080), (9, 40, 4, 2048, 352), (9, 40, 4, 2080, 352), (33, 8, 2, 224, 224),
+                                       (64, 5, 3, 32, 96)])
+@pytest.mark.parametrize("r,fmt,limit", [(0, "rawint4", 0.5), (0, "mxfp4", 0.0), (7, "mxfp4", 1.0), (64, "rawint4", 0.0), (65, "rawint4", 0.0)])
+def test_short_rows(dev, t, e, k, h, i, r, fmt, limit):
+    _say("short", t, e, k, h, i, r, fmt, limit)
+    c = Case(dev, t, e, k, h, i, r, fmt, limit, seed=t + h)
+    c.ids[0, 0] = c.ids[0, -1]
+    c.ids[-1, 0] = -1
+    c.check(c.run())
+
+
 def test_decode_equals_itself_anywhere(dev):
     """Results repeat bit for bit, from any workspace, and a larger workspace serves fewer tokens."""
     _say("repeat")
