@@ -898,10 +898,12 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a, int parts) {
 
 // ---------------------------------------------------------------- host
 
-// Down's parts: two workgroups a unit of the chip, as far as the slots reach (8 tokens of 279 experts, 576 x 2016: 116 -> 79 us;
+// Down's parts: two workgroups a unit of the chip, as far as experts or slots reach (8 tokens of 279 experts, 576 x 2016: 116 -> 79 us;
 // 11 of 272, 416 x 1280, rank 64: 182 -> 100); columns that fill the chip by themselves are not split.
-static int down_parts(int64_t H, int64_t S) {
-  const int64_t columns = H / 16, want = (512 + columns - 1) / columns, most = (S + kDownWaves - 1) / kDownWaves;
+static bool down_by_slot(int64_t E, int64_t S) { return S > 2 * E; }
+static int down_parts(int64_t H, int64_t E, int64_t S) {
+  const int64_t units = down_by_slot(E, S) || S < E ? S : E, columns = H / 16;  // (experts or slots for the waves, at most)
+  const int64_t want = (512 + columns - 1) / columns, most = (units + kDownWaves - 1) / kDownWaves;
   return (int)(columns >= 256 ? 1 : want < most ? want : most);
 }
 
@@ -919,7 +921,7 @@ static DecodePlan plan_decode(const Dims& d) {
   p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
   p.part = p.ud + round256(4 * S * d.R);
-  const int parts = S ? down_parts(d.H, d.Ms) : 1;
+  const int parts = S ? down_parts(d.H, d.E, d.Ms) : 1;
   p.total = p.part + (parts > 1 ? round256((size_t)4 * parts * d.qlen * d.H) : 0);
   return p;
 }
@@ -949,7 +951,7 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
     k_decode_lora_a<true><<<dim3((unsigned)((a.R + 3) / 4), (unsigned)a.S), 256, 0, st>>>(a);
     note_launch();
   }
-  const int parts = down_parts(a.H, a.S);
+  const int parts = down_parts(a.H, a.E, a.S);
   k_decode_down<MX, LORA>
       <<<dim3((unsigned)(a.H / 16), (unsigned)parts), 64 * kDownWaves, kDownWaves * (kDownLds + (size_t)a.T * 64), st>>>(a);
   note_launch();
@@ -1009,7 +1011,7 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.part = ws_ptr<float>(workspace, p.part);
   // (more than two slots an expert on average: codes come from the caches all the same, and one workgroup after the other would
   // wait for the longest list; 21 tokens of 4 experts, 160 x 1216: 85 -> 65 us, 13 of 8, 6880 x 2912: 205 -> 193)
-  a.by_slot = a.S > 2 * a.E;
+  a.by_slot = down_by_slot(a.E, a.S);
   hipStream_t st = static_cast<hipStream_t>(stream);
   begin_launches();
   if (d.fmt == KT_RAWINT4_FORMAT_MXFP4)
