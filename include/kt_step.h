@@ -160,7 +160,7 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
 /*
  * kt_rawint4_moe_infer for up to KT_MOE_DECODE_MAX_TOKENS tokens (and a hidden
  * of up to KT_MOE_DECODE_MAX_HIDDEN): the same arguments and formula, in two
- * kernels (four with LoRA), without sorting, converted scales or staged rows.
+ * or three kernels (two more with LoRA), without sorting, converted scales or staged rows.
  * The packed rows of each chosen expert are read once for two of its tokens: the
  * faster of the two while experts have up to about two tokens each
  * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  Inputs

@@ -1,5 +1,6 @@
 // The routed experts for a few tokens (decoding): gate and up in one kernel,
-// down with the weighted sum over the slots in another, two small ones more with LoRA.
+// down with the weighted sum over the slots in another, two small ones more with LoRA, and one
+// that adds down's parts where it is split.
 //
 // With few tokens an expert has one or two of them, and the time is that of
 // reading its packed rows once.  So the loads decide the layout: eight lanes
@@ -898,9 +899,10 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a, int parts) {
 
 // ---------------------------------------------------------------- host
 
+static bool down_by_slot(int64_t E, int64_t S) { return S > 2 * E; }
+
 // Down's parts: two workgroups a unit of the chip, as far as experts or slots reach (8 tokens of 279 experts, 576 x 2016: 116 -> 79 us;
 // 11 of 272, 416 x 1280, rank 64: 182 -> 100); columns that fill the chip by themselves are not split.
-static bool down_by_slot(int64_t E, int64_t S) { return S > 2 * E; }
 static int down_parts(int64_t H, int64_t E, int64_t S) {
   const int64_t units = down_by_slot(E, S) || S < E ? S : E, columns = H / 16;  // (experts or slots for the waves, at most)
   const int64_t want = (512 + columns - 1) / columns, most = (units + kDownWaves - 1) / kDownWaves;
