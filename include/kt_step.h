@@ -165,8 +165,8 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
  * faster of the two while experts have up to about two tokens each
  * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  Inputs
  * and bf16 scales keep their whole range (no numeric domain); products and
- * sums are fp32, h is rounded to fp16 in between (2^-11 of a value; a power of
- * two keeps its range); an input that is not finite makes its token's output
+ * sums are fp32; h is kept in between to 2^-22 of the largest of 16 neighbours
+ * and better; an input that is not finite makes its token's output
  * NaN.  tokens == 0 is a valid no-op.  A workspace of the size for some
  * number of tokens serves every smaller number too.
  */

@@ -12,9 +12,12 @@
 //   by dot products of two with fp32 sums that start from -3/2 sum x of the group.
 //   MXFP4: a code is converted to bf16 as it is, the sum starts from 0.
 // The scale then multiplies the group's sum in fp32.  Products are exact,
-// whatever the inputs' and scales' size.  Inputs are bf16 as given; h enters
-// down in fp16 with a power of two for 16 columns, rounded by at most 2^-11 of
-// itself (2e-4 of the output, whose own rounding to bf16 is 1.7e-3).
+// whatever the inputs' and scales' size.  Inputs are bf16 as given.  h enters down with
+// a power of two for 16 columns: for RAWINT4 as integers of 24 bits, whose three bytes are multiplied
+// with the codes by dot products of four, exactly,
+//     sum (c - 8) q = 2^16 sum c q2 + 2^8 sum c q1 + sum c q0 - 8 sum q
+// (fewer instructions than fp16 takes, and 2^-23 of the largest of the 16), for MXFP4 as the sum of two fp16
+// numbers (2^-22 of itself).  One fp16 number would do 2^-11, which shows in outputs that are small differences.
 //
 // 384 experts, 8 a token, 7168 x 2048: one token 39 us (195 MB of codes and scales: 5.0 TB/s), 4 tokens with LoRA of rank
 // 64 196 us, 8 tokens on MXFP4 245 us (1.4 GB: 5.9 TB/s), 32 tokens with rank 16 888 us: the bytes once, at what reads alone reach.
@@ -48,8 +51,8 @@ struct DecodeArgs {
   const uint16_t *sg, *su, *sd;
   const float *ag, *bg, *au, *bu, *ad, *bd;
   float* h;       // [S][I], with LoRA
-  uint16_t* hs;   // [S][I]: h in fp16 times a power of two, in the codes' order
-  float2_t* hsf;  // [S][I / 16]: -3/2 of the sum of 16 of them, and what their products with the codes are to be multiplied by
+  uint8_t* hs;    // [S][I / 1024, upwards][planes][32][16 bytes]: h as down reads it (finish_column)
+  float2_t* hsf;  // [S][I / 16]: RAWINT4: -8 times the sum of 16 columns (an int); what their products with the codes are to be multiplied by
   int32_t* next;  // [S]: the next slot of the same expert, -1 for none
   int32_t* lead;  // [S]: whether the slot is its expert's first
   float* ua;      // [S][2 R]: x A_g^T | x A_u^T
@@ -109,32 +112,31 @@ __device__ __forceinline__ Slots find_slots(const DecodeArgs& a, int s, int64_t 
   return r;
 }
 
-// 8 codes of a dword as two-byte floats (bf16, or fp16 with HALF): RAWINT4 1 + c / 16 in the order k0 k4 k1 k5 k2 k6 k3 k7,
-// MXFP4 their values in order.
+// 8 codes of a dword as two-byte floats: RAWINT4 1 + c / 16 in bf16, in the order k0 k4 k1 k5 k2 k6 k3 k7,
+// MXFP4 their values in order, in bf16 or fp16 (HALF).
 struct DotConsts {
   uint32_t m, o;
 };
-template <bool HALF>
 __device__ __forceinline__ DotConsts dot_consts() {
   // (values the compiler cannot see through, in a scalar and a vector register: (w & m) | o is then one instruction)
-  uint32_t m = HALF ? 0x03c003c0u : 0x00780078u, o = HALF ? 0x3c003c00u : 0x3f803f80u;
+  uint32_t m = 0x00780078u, o = 0x3f803f80u;
   asm volatile("" : "+s"(m));
   asm volatile("" : "+v"(o));
   return DotConsts{m, o};
 }
-template <bool MX, bool HALF>
+template <bool HALF>
+__device__ __forceinline__ u32x4 decode8_mx(uint32_t w) {
+  auto two = [&](auto sel) {
+    constexpr int k = decltype(sel)::value;
+    if (HALF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, k));
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, k));
+  };
+  return u32x4{two(std::integral_constant<int, 0>()), two(std::integral_constant<int, 1>()),
+               two(std::integral_constant<int, 2>()), two(std::integral_constant<int, 3>())};
+}
+template <bool MX>
 __device__ __forceinline__ u32x4 decode8(uint32_t w, DotConsts dc) {
-  if (MX) {
-    auto two = [&](auto sel) {
-      constexpr int k = decltype(sel)::value;
-      if (HALF) return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.f, k));
-      return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.f, k));
-    };
-    return u32x4{two(std::integral_constant<int, 0>()), two(std::integral_constant<int, 1>()),
-                 two(std::integral_constant<int, 2>()), two(std::integral_constant<int, 3>())};
-  }
-  if (HALF)
-    return u32x4{((w << 6) & dc.m) | dc.o, ((w << 2) & dc.m) | dc.o, ((w >> 2) & dc.m) | dc.o, ((w >> 6) & dc.m) | dc.o};
+  if (MX) return decode8_mx<false>(w);
   return u32x4{((w << 3) & dc.m) | dc.o, ((w >> 1) & dc.m) | dc.o, ((w >> 5) & dc.m) | dc.o, ((w >> 9) & dc.m) | dc.o};
 }
 
@@ -333,7 +335,7 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
 #pragma unroll
     for (int p = 0; p < V; ++p) l.lora[part][up][p][c] = t[p];
   }
-  const DotConsts dc = dot_consts<false>();
+  const DotConsts dc = dot_consts();
   float acc[4][V] = {};
   for (int v = 0; v < per; v += kUpDepth) {
 #pragma unroll
@@ -355,7 +357,7 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
           for (int p = 0; p < V; ++p) d[p] = sum[p];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const u32x4 w = decode8<MX, false>(cd[b][t][j], dc);
+            const u32x4 w = decode8<MX>(cd[b][t][j], dc);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -378,6 +380,25 @@ __device__ __forceinline__ void gate_up_pass(const DecodeArgs& a, int64_t e, int
     }
 }
 
+constexpr int kDownUnits = 4;           // units of a chunk of down: the loads ahead
+constexpr int kDownK = kDownUnits * 8;  // its groups
+constexpr int kDownPlane = kDownK * 16;
+// h lies as a wave of down has it in LDS: chunks of planes of 16 bytes a group.  Bytes of a chunk, and where one is.
+template <bool MX>
+constexpr int kChunkBytes = (MX ? 8 : 6) * kDownPlane;
+static __host__ __device__ inline size_t h_chunks(int64_t I) { return (size_t)(I / 32 + kDownK - 1) / kDownK; }
+template <bool MX>
+__device__ __forceinline__ size_t h_chunk(int I, int s, int chunk) {
+  return ((size_t)s * h_chunks(I) + chunk) * kChunkBytes<MX>;
+}
+// row16_sum for integers
+__device__ __forceinline__ int row16_isum(int v) {
+  v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true);
+  v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true);
+  v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);
+  return v + __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);
+}
+
 // Column i0 + c (c: the lane in its 16) of slot s from its two sums: clamp, SwiGLU, and h as down reads it.
 template <bool MX, bool LORA>
 __device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, float uv, int s, int i0, int c) {
@@ -386,13 +407,30 @@ __device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, flo
     gv = gv > a.limit ? a.limit : gv;
     uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
   }
-  // h in fp16 times a power of two that brings the largest of the 16 below 2^15: a rounding of 2^-11 of the value
   const float h = gv * sigmoid_f(gv) * uv;
-  const int ex = pow2_exponent_for(row16_max(fabsf(h)));
-  const uint16_t bits = float_to_half_bits(ldexpf(h, ex));
-  a.hs[(size_t)s * a.I + i0 + (MX ? c : perm_pos(c))] = bits;
-  const float sum = row16_sum(half_bits_to_float(bits));
-  if (c == 0) a.hsf[(size_t)s * (a.I / 16) + i0 / 16] = float2_t{MX ? 0.f : -1.5f * sum, ldexpf(MX ? 1.f : 16.f, -ex)};
+  // brings the largest of the 16 below 2^15 (118: the factor that undoes it is no subnormal)
+  const int ex = min(pow2_exponent_for(row16_max(fabsf(h))), 118);
+  const float hx = ldexpf(h, ex);
+  const int g = i0 / 32, half = i0 >> 4 & 1;
+  uint8_t* at = a.hs + h_chunk<MX>(a.I, s, g / kDownK) + (g & (kDownK - 1)) * 16;
+  float2_t f;
+  if (MX) {
+    // fp16, and in fp16 what that left (of what is finite): planes of 8 columns
+    const uint16_t hi = float_to_half_bits(hx);
+    const float high = half_bits_to_float(hi);
+    uint16_t* to = reinterpret_cast<uint16_t*>(at + (2 * half + (c >> 3)) * kDownPlane) + (c & 7);
+    to[0] = hi;
+    to[2 * kDownPlane] = float_to_half_bits(fabsf(high) < INFINITY ? hx - high : 0.f);
+    f = float2_t{0.f, ldexpf(1.f, -ex)};
+  } else {
+    // integers of 24 bits: planes of a byte of 16 columns, each 8 of which in the codes' order (even ones, odd ones).  One
+    // that is not finite makes its 16 columns' products NaN.
+    const int q = (int)rintf(fminf(fmaxf(hx * 256.f, -0x1p23f), 0x1p23f - 1.f));
+    uint8_t* to = at + 3 * half * kDownPlane + ((c & 8) | (c & 1) << 2 | (c & 7) >> 1);
+    to[0] = (uint8_t)q, to[kDownPlane] = (uint8_t)(q >> 8), to[2 * kDownPlane] = (uint8_t)(q >> 16);
+    f = float2_t{__int_as_float(-8 * row16_isum(q)), ldexpf(1.f, -8 - ex) + row16_sum(fabsf(h) < INFINITY ? 0.f : NAN)};
+  }
+  if (c == 0) a.hsf[(size_t)s * (a.I / 16) + i0 / 16] = f;
   if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
 }
 
@@ -544,7 +582,7 @@ __device__ __forceinline__ void gate_up_short(const DecodeArgs& a, int64_t e, in
 #pragma unroll
     for (int p = 0; p < V; ++p) lg[p] = rows_sum(lg[p]), lu[p] = rows_sum(lu[p]);
   }
-  const DotConsts dc = dot_consts<false>();
+  const DotConsts dc = dot_consts();
   const uint16_t* sc = l.scales + (j0 - i0 + row) * G;
   float acc[4][V] = {};
   for (int v = 0; v < units; v += kUpDepth) {
@@ -567,7 +605,7 @@ __device__ __forceinline__ void gate_up_short(const DecodeArgs& a, int64_t e, in
           for (int p = 0; p < V; ++p) d[p] = sum[p];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const u32x4 w = decode8<MX, false>(cd[b][t][j], dc);
+            const u32x4 w = decode8<MX>(cd[b][t][j], dc);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -711,10 +749,45 @@ __global__ __launch_bounds__(256) void k_decode_lora_a(DecodeArgs a) {
   }
 }
 
+// 16 codes times their h (x: its planes, of MXFP4 the second fp16 numbers four planes on).
+template <bool MX>
+__device__ __forceinline__ float half_product(uint32_t w0, uint32_t w1, const u32x4* x, uint32_t sum) {
+  const uint32_t w[2] = {w0, w1};
+  if (MX) {
+    float d = 0.f, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 v = decode8_mx<true>(w[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d = dot2<true>(v[j], x[i][j], d), l = dot2<true>(v[j], x[4 + i][j], l);
+    }
+    return d + l;
+  }
+  // (32 bits hold the whole: 15 x 16 x 2^23; the parts may wrap)
+  uint32_t d0 = sum, d1 = 0;
+  int d2 = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t c[2] = {w[i] & 0x0f0f0f0fu, w[i] >> 4 & 0x0f0f0f0fu};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      d0 = __builtin_amdgcn_udot4(c[j], x[0][2 * i + j], d0, false);
+      d1 = __builtin_amdgcn_udot4(c[j], x[1][2 * i + j], d1, false);
+      d2 = __builtin_amdgcn_sdot4((int)c[j], (int)x[2][2 * i + j], d2, false);
+    }
+  }
+  return (float)(int)(((((uint32_t)d2 << 8) + d1) << 8) + d0);
+}
+
 constexpr int kDownWaves = 8;
-constexpr int kDownUnits = 4;               // units of a chunk: the loads ahead
-constexpr int kDownK = kDownUnits * 8;      // its groups
-constexpr int kDownLds = kDownK * (64 + 16 + 32);  // bytes a wave: h, sums and factors, scales of 16 rows
+template <bool MX>
+constexpr int kDownLds = kChunkBytes<MX> + kDownK * (16 + 32);  // bytes a wave: h, sums and factors, scales of 16 rows
+
+// bytes of dynamic LDS (64 tokens of 8 slots each leave room for a second workgroup)
+template <bool MX>
+static inline size_t down_lds(int T, int S) {
+  return kDownWaves * (kDownLds<MX> + (size_t)T * 64) + (size_t)(S + 63) / 64 * 64 * 6;
+}
 
 // Down and the sum over the slots.  A workgroup has 16 columns of H; its waves
 // take the experts in turn (a wave per expert, the whole contraction), a slot at a
@@ -725,18 +798,19 @@ constexpr int kDownLds = kDownK * (64 + 16 + 32);  // bytes a wave: h, sums and 
 template <bool MX, bool LORA>
 __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  __shared__ uint16_t order[KT_MOE_DECODE_MAX_SLOTS], expert[KT_MOE_DECODE_MAX_SLOTS];
-  __shared__ int16_t next[KT_MOE_DECODE_MAX_SLOTS];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, c8 = lane & 7, row = lane >> 3;
   const int h0 = blockIdx.x * 16, G = a.I / 32;
-  constexpr int plane = kDownK * 16;
-  uint8_t* hl = lds + wave * kDownLds;                             // four planes of h
-  u32x4* sf = reinterpret_cast<u32x4*>(hl + 4 * plane);            // [group]: sum and factor of its halves
+  constexpr int kLoads = kChunkBytes<MX> / 1024;  // of h, a chunk
+  uint8_t* hl = lds + wave * kDownLds<MX>;                         // planes of h
+  u32x4* sf = reinterpret_cast<u32x4*>(hl + kChunkBytes<MX>);      // [group]: sum and factor of its halves
   uint16_t* sl = reinterpret_cast<uint16_t*>(sf + kDownK);         // [16][kDownK] scales
-  float* acc = reinterpret_cast<float*>(lds + kDownWaves * kDownLds);  // [waves][T][16]
+  float* acc = reinterpret_cast<float*>(lds + kDownWaves * kDownLds<MX>);  // [waves][T][16]
   // the experts' first slots, in order
   __shared__ uint64_t mask[kSlotWords];
   const int words = (a.S + 63) / 64;
+  uint16_t* order = reinterpret_cast<uint16_t*>(acc + kDownWaves * a.T * 16);  // [words][64], as the next two
+  uint16_t* expert = order + words * 64;
+  int16_t* next = reinterpret_cast<int16_t*>(expert + words * 64);
   for (int w = wave; w < words; w += kDownWaves) {
     const int s = w * 64 + lane, i = min(s, a.S - 1);
     const int lead = a.lead[i], after = a.next[i], id = (int)a.ids[i];
@@ -756,14 +830,14 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
   __syncthreads();
   const int first = blockIdx.y * kDownWaves + wave, stride = gridDim.y * kDownWaves;
   if (first < U) {
-    const Buffer hb = buffer_of(a.hs, (size_t)a.S * a.I * 2), fb = buffer_of(a.hsf, (size_t)a.S * (a.I / 16) * 8);
+    const Buffer hb = buffer_of(a.hs, h_chunk<MX>(a.I, a.S, 0)), fb = buffer_of(a.hsf, (size_t)a.S * (a.I / 16) * 8);
     const uint32_t at = (uint32_t)(h0 + row) * G, rows8 = 128u * G;
     const size_t n = (size_t)a.H * G;
     // the chunk whose loads are issued next
     int j = first, s = __builtin_amdgcn_readfirstlane(order[j]), k0 = 0;
     size_t e = __builtin_amdgcn_readfirstlane(expert[s]);
     bool more = true;  // (there is one)
-    u32x4 cd[kDownUnits][2], hn[2], sn;
+    u32x4 cd[kDownUnits][2], hn[kLoads], sn;
     float2_t fn;
     auto load_codes = [&](int b) {
       const Buffer w = buffer_of(a.wd + e * n * 16, n * 16);
@@ -786,10 +860,10 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
 #pragma unroll
         for (int i = 0; i < 4; ++i) sn[i] = v[2 * i] | v[2 * i + 1] << 16;
       }
-      // h: quarters of groups; sums and factors: halves
-      const uint32_t last = (uint32_t)(s + 1) * G * 64 - 16, ho = ((uint32_t)s * G + k0) * 64 + l * 16;
-      hn[0] = buffer16<kKept>(hb, min(ho, last), 0);
-      hn[1] = buffer16<kKept>(hb, min(ho + 1024, last), 0);
+      // h as it lies; sums and factors: halves of groups
+      const uint32_t ho = (uint32_t)h_chunk<MX>(a.I, s, k0 / kDownK) + l * 16;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) hn[i] = buffer16<kKept>(hb, ho + 1024 * i, 0);
       const uint32_t fo = min(((uint32_t)s * G + k0) * 16 + l * 8, (uint32_t)(s + 1) * G * 16 - 8);
       fn = __builtin_bit_cast(float2_t, __builtin_amdgcn_raw_buffer_load_b64(fb, (int)fo, 0, 0));
       __builtin_amdgcn_sched_barrier(0);
@@ -797,7 +871,6 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
     load_rest();
 #pragma unroll
     for (int b = 0; b < kDownUnits; ++b) load_codes(b);
-    const DotConsts dc = dot_consts<true>();
     float y[2] = {0.f, 0.f};
     while (more) {
       // this chunk's h, sums, factors and scales to LDS, 0 behind the contraction's end
@@ -806,10 +879,8 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
       const u32x4 zero = {0, 0, 0, 0};
       wave_fence();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = lane + 64 * i;
-        *reinterpret_cast<u32x4*>(hl + (c & 3) * plane + (c >> 2) * 16) = c < 4 * len ? hn[i] : zero;
-      }
+      for (int i = 0; i < kLoads; ++i)
+        *reinterpret_cast<u32x4*>(hl + (lane + 64 * i) * 16) = (lane & (kDownK - 1)) < len ? hn[i] : zero;
       reinterpret_cast<float2_t*>(sf)[lane] = lane < 2 * len ? fn : float2_t{0.f, 0.f};
       *reinterpret_cast<u32x4*>(sl + lane * 8) = sn;
       wave_fence();
@@ -836,18 +907,16 @@ __global__ __launch_bounds__(64 * kDownWaves, 4) void k_decode_down(DecodeArgs a
       for (int b = 0; b < kDownUnits; ++b) {
         if (b < units) {
           const int g = 8 * b + c8;
-          Vec x;
-          read_vec(hl, g, plane, x);
           const u32x4 f = sf[g];
+          u32x4 x[kChunkBytes<MX> / kDownPlane];
+#pragma unroll
+          for (int j = 0; j < kChunkBytes<MX> / kDownPlane; ++j)
+            x[j] = *reinterpret_cast<const u32x4*>(hl + j * kDownPlane + g * 16);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            float d[2] = {__uint_as_float(f.x), __uint_as_float(f.z)};
+            float d[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const u32x4 w = decode8<MX, true>(cd[b][t][i], dc);
-#pragma unroll
-              for (int v = 0; v < 4; ++v) d[i / 2] = dot2<true>(w[v], x.v[i][v], d[i / 2]);
-            }
+            for (int h = 0; h < 2; ++h) d[h] = half_product<MX>(cd[b][t][2 * h], cd[b][t][2 * h + 1], x + (MX ? 2 : 3) * h, f[2 * h]);
             const float sc = bf16_to_float(sl[(t * 8 + row) * kDownK + g]);
             y[t] = fmaf(sc, fmaf(__uint_as_float(f.y), d[0], __uint_as_float(f.w) * d[1]), y[t]);
             __builtin_amdgcn_sched_barrier(0);
@@ -918,7 +987,7 @@ static DecodePlan plan_decode(const Dims& d) {
   p.next = 0;
   p.lead = round256(4 * S);
   p.hs = p.lead + round256(4 * S);
-  p.hsf = p.hs + round256(2 * S * d.I);
+  p.hsf = p.hs + round256(S * h_chunks(d.I) * (d.fmt == KT_RAWINT4_FORMAT_MXFP4 ? kChunkBytes<true> : kChunkBytes<false>));
   p.h = p.hsf + round256(8 * S * (d.I / 16));
   p.ua = p.h + (d.R ? round256(4 * S * d.I) : 0);
   p.ud = p.ua + round256(4 * S * 2 * d.R);
@@ -955,7 +1024,7 @@ static void launch_decode(const DecodeArgs& a, hipStream_t st) {
   }
   const int parts = down_parts(a.H, a.E, a.S);
   k_decode_down<MX, LORA>
-      <<<dim3((unsigned)(a.H / 16), (unsigned)parts), 64 * kDownWaves, kDownWaves * (kDownLds + (size_t)a.T * 64), st>>>(a);
+      <<<dim3((unsigned)(a.H / 16), (unsigned)parts), 64 * kDownWaves, down_lds<MX>(a.T, a.S), st>>>(a);
   note_launch();
   if (parts > 1) {
     k_decode_join<<<(unsigned)((a.T * a.H / 4 + 255) / 256), 256, 0, st>>>(a, parts);
@@ -1004,7 +1073,7 @@ int kt_moe_decode(const kt_rawint4_moe_layer* layer, int32_t tokens, const uint1
   a.ag = layer->gate_lora_a, a.bg = layer->gate_lora_b, a.au = layer->up_lora_a, a.bu = layer->up_lora_b;
   a.ad = layer->down_lora_a, a.bd = layer->down_lora_b;
   a.h = ws_ptr<float>(workspace, p.h);
-  a.hs = ws_ptr<uint16_t>(workspace, p.hs);
+  a.hs = ws_ptr<uint8_t>(workspace, p.hs);
   a.hsf = ws_ptr<float2_t>(workspace, p.hsf);
   a.next = ws_ptr<int32_t>(workspace, p.next);
   a.lead = ws_ptr<int32_t>(workspace, p.lead);
