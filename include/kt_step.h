@@ -163,11 +163,14 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
  * or three kernels (two more with LoRA), without sorting, converted scales or staged rows.
  * The packed rows of each chosen expert are read once for two of its tokens: the
  * faster of the two while experts have up to about two tokens each
- * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  Inputs
- * and bf16 scales keep their whole range (no numeric domain); products and
+ * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  bf16
+ * scales have no numeric domain; inputs are up to 2^120 in magnitude (of larger
+ * ones sums may leave fp32's range and become infinite or NaN).  Products and
  * sums are fp32; h is kept in between to 2^-22 of the largest of 16 neighbours
- * and better; an input that is not finite makes its token's output
- * NaN.  tokens == 0 is a valid no-op.  A workspace of the size for some
+ * and better.  An input that is NaN makes its token's output NaN, and with
+ * RAWINT4 so does an infinite one; with MXFP4 that goes by the formula (infinite
+ * or NaN sums; infinite ones are clamped as others are).  A token without a
+ * valid id gets zeros whatever its input.  tokens == 0 is a valid no-op.  A workspace of the size for some
  * number of tokens serves every smaller number too.
  */
 size_t kt_moe_decode_workspace_bytes(const kt_rawint4_moe_layer* layer, int32_t tokens);

@@ -11,8 +11,9 @@
 //     sum (c - 8) x = 16 (sum (1 + c / 16) x - 3/2 sum x)
 //   by dot products of two with fp32 sums that start from -3/2 sum x of the group.
 //   MXFP4: a code is converted to bf16 as it is, the sum starts from 0.
-// The scale then multiplies the group's sum in fp32.  Products are exact,
-// whatever the inputs' and scales' size.  Inputs are bf16 as given.  h enters down with
+// The scale then multiplies the group's sum in fp32.  Products are exact, subnormal inputs
+// and scales among them, and sums stay in fp32's range for inputs up to 2^120
+// (3/2 of 32 of them).  Inputs are bf16 as given.  h enters down with
 // a power of two for 16 columns: for RAWINT4 as integers of 24 bits, whose three bytes are multiplied
 // with the codes by dot products of four, exactly,
 //     sum (c - 8) q = 2^16 sum c q2 + 2^8 sum c q1 + sum c q0 - 8 sum q
@@ -408,8 +409,9 @@ __device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, flo
     uv = uv > a.limit ? a.limit : uv < -a.limit ? -a.limit : uv;
   }
   const float h = gv * sigmoid_f(gv) * uv;
-  // brings the largest of the 16 below 2^15 (118: the factor that undoes it is no subnormal)
-  const int ex = min(pow2_exponent_for(row16_max(fabsf(h))), 118);
+  // brings the largest finite one of the 16 below 2^15 (118: the factor that undoes it is no subnormal)
+  const bool finite = fabsf(h) < INFINITY;
+  const int ex = min(pow2_exponent_for(row16_max(finite ? fabsf(h) : 0.f)), 118);
   const float hx = ldexpf(h, ex);
   const int g = i0 / 32, half = i0 >> 4 & 1;
   uint8_t* at = a.hs + h_chunk<MX>(a.I, s, g / kDownK) + (g & (kDownK - 1)) * 16;
@@ -420,7 +422,7 @@ __device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, flo
     const float high = half_bits_to_float(hi);
     uint16_t* to = reinterpret_cast<uint16_t*>(at + (2 * half + (c >> 3)) * kDownPlane) + (c & 7);
     to[0] = hi;
-    to[2 * kDownPlane] = float_to_half_bits(fabsf(high) < INFINITY ? hx - high : 0.f);
+    to[2 * kDownPlane] = float_to_half_bits(finite ? hx - high : 0.f);
     f = float2_t{0.f, ldexpf(1.f, -ex)};
   } else {
     // integers of 24 bits: planes of a byte of 16 columns, each 8 of which in the codes' order (even ones, odd ones).  One
@@ -428,7 +430,7 @@ __device__ __forceinline__ void finish_column(const DecodeArgs& a, float gv, flo
     const int q = (int)rintf(fminf(fmaxf(hx * 256.f, -0x1p23f), 0x1p23f - 1.f));
     uint8_t* to = at + 3 * half * kDownPlane + ((c & 8) | (c & 1) << 2 | (c & 7) >> 1);
     to[0] = (uint8_t)q, to[kDownPlane] = (uint8_t)(q >> 8), to[2 * kDownPlane] = (uint8_t)(q >> 16);
-    f = float2_t{__int_as_float(-8 * row16_isum(q)), ldexpf(1.f, -8 - ex) + row16_sum(fabsf(h) < INFINITY ? 0.f : NAN)};
+    f = float2_t{__int_as_float(-8 * row16_isum(q)), ldexpf(1.f, -8 - ex) + row16_sum(finite ? 0.f : NAN)};
   }
   if (c == 0) a.hsf[(size_t)s * (a.I / 16) + i0 / 16] = f;
   if (LORA) a.h[(size_t)s * a.I + i0 + c] = h;
