@@ -24,6 +24,8 @@ constexpr int kAdamPerLaunch = 32;  // tensors in a launch's arguments
 constexpr int kAdamUnits = 4;       // blocks of 256 values a wave takes
 constexpr int kAdamChunk = 4 * kAdamUnits * KT_ADAMW_BLOCK;  // values of a workgroup
 constexpr int kNormBlocks = 1024;  // of the norm, a launch
+constexpr int64_t kAdamLaunch = 1 << 20;  // chunks a launch of the update takes: more of them in several (a launch has fewer than 2^32 threads)
+static_assert(kAdamLaunch * 256 < (int64_t)1 << 32, "threads of a launch");
 constexpr float kTiny = 0x1p-100f;
 
 struct AdamTensor {
@@ -48,6 +50,7 @@ struct AdamControl {
 struct AdamArgs {
   const AdamControl* ctl;
   int64_t chunks;
+  int64_t from;  // the launch's first chunk
   int count;
   float b1, b1c, b2, b2c, eps;
   double* part;
@@ -244,10 +247,11 @@ __device__ __forceinline__ void adam_chunk(const AdamArgs& a, const AdamControl&
 template <bool E8>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void k_adamw(AdamArgs a) {
   const AdamControl ctl = *a.ctl;
-  const AdamTensor& t = a.t[find_tensor(a, blockIdx.x)];
+  const int64_t chunk = a.from + blockIdx.x;
+  const AdamTensor& t = a.t[find_tensor(a, chunk)];
   if (ctl.skip) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t base = ((int64_t)blockIdx.x - t.first) * kAdamChunk + wave * KT_ADAMW_BLOCK;
+  const int64_t base = (chunk - t.first) * kAdamChunk + wave * KT_ADAMW_BLOCK;
   if (t.p_f32)
     t.g_f32 ? adam_chunk<1, true, E8>(a, ctl, t, base) : adam_chunk<1, false, E8>(a, ctl, t, base);
   else if (t.master)
@@ -346,7 +350,7 @@ static int check_adamw(const kt_adamw* h) {
 }
 
 static int check_adamw_tensor(const kt_adamw_tensor& t, int format) {
-  // (a launch's chunks are then at most 2^29)
+  // (a list's chunks are then at most 2^40)
   if (t.count < 0 || t.count > ((int64_t)1 << 36)) return set_error(KT_RAWINT4_EINVAL, "a tensor's count must be in [0, 2^36]");
   if ((t.param_type != KT_TYPE_BF16 && t.param_type != KT_TYPE_F32) ||
       (t.grad_type != KT_TYPE_BF16 && t.grad_type != KT_TYPE_F32))
@@ -430,12 +434,17 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
         a.part = part + parts;
         parts += blocks;
         k_grad_squares<<<blocks, 256, 0, st>>>(a);
-      } else if (hyper->state_format == KT_ADAMW_STATES_E4M3) {
-        k_adamw<true><<<(unsigned)a.chunks, 256, 0, st>>>(a);
-      } else {
-        k_adamw<false><<<(unsigned)a.chunks, 256, 0, st>>>(a);
+        note_launch();
+        continue;
       }
-      note_launch();
+      for (a.from = 0; a.from < a.chunks; a.from += kAdamLaunch) {
+        const unsigned blocks = (unsigned)(a.chunks - a.from < kAdamLaunch ? a.chunks - a.from : kAdamLaunch);
+        if (hyper->state_format == KT_ADAMW_STATES_E4M3)
+          k_adamw<true><<<blocks, 256, 0, st>>>(a);
+        else
+          k_adamw<false><<<blocks, 256, 0, st>>>(a);
+        note_launch();
+      }
     }
   }
   return finish_launches();
