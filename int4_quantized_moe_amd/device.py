@@ -596,7 +596,8 @@ class DeviceNorm:
 
 
 class DeviceAdamW:
-    """AdamW over a dict of tensors (fp32 or bf16), all in one call.
+    """AdamW over a dict of tensors (fp32 or bf16), all in one call.  No two of them share memory (tied weights stand
+    in it once, with the sum of their gradients).
 
     ``states``: "fp32", or "e4m3" for 8-bit moments with one fp32 scale per 256 values.  ``master``: bf16
     tensors keep an fp32 copy that the updates are made to.  ``max_norm`` clips the gradients by their
@@ -646,6 +647,13 @@ class DeviceAdamW:
                 _checked(f"state[{name!r}][{key!r}]", t, shape, dtype, dev)
                 have[key] = t
             self.state[name] = have
+        # all of them are updated at once: one that shares values with another would be updated twice, in no order
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), label) for name, p in params.items()
+                       for label, t in ((repr(name), p), *((f"state[{name!r}][{k!r}]", s) for k, s in self.state[name].items()))
+                       if t.numel())
+        for (_, end, one), (begin, _, other) in zip(spans, spans[1:]):
+            if begin < end:
+                raise ValueError(f"{one} and {other} share memory: a tensor stands in params once")
         if isinstance(step, torch.Tensor):
             _checked("step", step, (1,), torch.int64, dev)
             self.step_count = step
