@@ -118,6 +118,8 @@ typedef struct kt_adamw {
  * [ceil(count / 256)] what a code of 1 stands for in each block of 256
  * values: the block's largest magnitude / 448.  The code of a positive
  * sqrt(v) is never 0.  A block whose largest magnitude is below 2^-100 holds zeros.
+ * A moment that is not finite (the square of a gradient from 2^64 on is not) stays in its block, whose other
+ * moments may not be finite from then on; grad_norm finds gradients that are not finite before anything changes.
  */
 typedef struct kt_adamw_tensor {
   int64_t count;
