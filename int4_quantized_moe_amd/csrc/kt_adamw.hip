@@ -308,7 +308,7 @@ __global__ __launch_bounds__(256) void k_adamw_begin(AdamBegin a) {
   if (a.norm) {
     const double norm = sqrt(red[0]) * fabs(a.grad_scale);
     *a.norm = (float)norm;
-    skip = !isfinite(norm);
+    skip = !isfinite(*a.norm);  // (as the caller sees it)
     if (a.max_norm > 0.0) mult *= fmin(1.0, a.max_norm / (norm + 1e-6));
   }
   AdamControl c;
