@@ -658,6 +658,8 @@ class DeviceAdamW:
             _checked("step", step, (1,), torch.int64, dev)
             self.step_count = step
         else:
+            if step < 0:
+                raise ValueError(f"step must not be negative, not {step}")
             self.step_count = torch.full((1,), int(step), dtype=torch.int64, device=dev)
         self.grad_norm = None
         if max_norm is not None or check_finite:

@@ -1,4 +1,4 @@
-"""AdamW refuses tensors that share memory (on the CPU): all of them are updated at once."""
+"""What DeviceAdamW refuses before any GPU work: tensors that share memory (all of them are updated at once), negative steps."""
 
 import pytest
 
@@ -25,3 +25,9 @@ def test_neighbours_and_empty_tensors_are_not():
     w = torch.zeros(600)
     o = device.DeviceAdamW({"a": w[:300], "b": w[300:], "c": w[:0], "d": w[300:300]}, states="e4m3")
     assert set(o.state) == {"a", "b", "c", "d"}
+
+
+def test_a_negative_step_is_refused():
+    """Its bias corrections would divide by 0."""
+    with pytest.raises(ValueError, match="step must not be negative"):
+        device.DeviceAdamW({"a": torch.zeros(8)}, step=-1)
