@@ -61,7 +61,8 @@ typedef struct kt_norm {
  * token_gate [tokens] fp32 or NULL.  h [tokens, H] (stream_type) may be x itself; y [tokens, H]
  * bf16.  Either may be NULL (not wanted), h has to be without b.  y is
  * computed from h before h's rounding.  Sums are fp32; each output is rounded
- * once.  The vectors, and all tensors, 16-byte aligned, token_gate 4-byte.  tokens == 0
+ * once.  Values that N takes are up to 2^56 in magnitude, and with eps = 0 not all of a row's
+ * below 2^-50: squares of others leave fp32, and N may be 0, infinite or NaN.  The vectors, and all tensors, 16-byte aligned, token_gate 4-byte.  tokens == 0
  * is a valid no-op.
  */
 int kt_norm_fwd(const kt_norm* norm, int32_t tokens, const void* x, const uint16_t* branch, const float* token_gate,
