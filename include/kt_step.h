@@ -164,9 +164,10 @@ int kt_adamw_step(const kt_adamw* hyper, const kt_adamw_tensor* tensors, int32_t
  * kt_rawint4_moe_infer for up to KT_MOE_DECODE_MAX_TOKENS tokens (and a hidden
  * of up to KT_MOE_DECODE_MAX_HIDDEN): the same arguments and formula, in two
  * or three kernels (two more with LoRA), without sorting, converted scales or staged rows.
- * The packed rows of each chosen expert are read once for two of its tokens: the
- * faster of the two while experts have up to about two tokens each
- * (tokens * top_k <= 2 * num_experts); for more kt_rawint4_moe_infer is.  bf16
+ * Gate and up go through the packed rows of each chosen expert once for two of its token-slots, down once for each.
+ * Which of the two is faster goes by the slots that an expert in use has on average: as measured, this
+ * one up to about 2 where many experts are in use (of 64 to 384) and about 6 where 8 are; above that
+ * kt_rawint4_moe_infer, by up to 6 times (64 tokens that share 8 experts).  bf16
  * scales have no numeric domain; inputs are up to 2^120 in magnitude (of larger
  * ones sums may leave fp32's range and become infinite or NaN).  Products and
  * sums are fp32; h is kept in between to 2^-22 of the largest of 16 neighbours

@@ -8,9 +8,11 @@
 // before.  So one launch takes the chunks of up to 32 tensors, whatever their sizes, a wave has all its
 // loads in flight before the first is used, and what the whole step shares (the steps made, the
 // clipping, both bias corrections) is worked out once, by a kernel of one workgroup.
-// 170 million values: fp32 with clipping 1007 us, 5.4 TB/s of 32 bytes a value; 8-bit states 491 us, 5.5
-// TB/s; 47 million bf16 ones with masters 263 us, 5.3 TB/s (a copy of 1 GiB: 4.9 to 5.1).
-// Six small tensors: 10 to 11 us, 7.4 of them on the GPU (2.4 for what is shared, 5.0).
+// 170 million values: fp32 with clipping 1012 us, 5.4 TB/s of 32 bytes a value; 8-bit states 492 us, 5.5
+// TB/s, where instructions bind as well (vector ones about 90% busy; on bf16 parameters and gradients 392 us, 4.4
+// TB/s); 47 million bf16 ones with masters 265 us, 5.3 TB/s (a copy of 1 GiB: 4.9 to 5.1).
+// Six small tensors: 10 to 11 us, 7.4 of them on the GPU (2.4 for what is shared, 5.0); 360 of them 141 us, which is
+// the host's, 86 in a graph (13 kernels; floor 58).
 #include "kt_step_common.hpp"
 
 #include <math.h>

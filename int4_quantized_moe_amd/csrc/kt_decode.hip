@@ -20,12 +20,13 @@
 // (fewer instructions than fp16 takes, and 2^-23 of the largest of the 16), for MXFP4 as the sum of two fp16
 // numbers (2^-22 of itself).  One fp16 number would do 2^-11, which shows in outputs that are small differences.
 //
-// 384 experts, 8 a token, 7168 x 2048: one token 39 us (195 MB of codes and scales: 5.0 TB/s), 4 tokens with LoRA of rank
-// 64 196 us, 8 tokens on MXFP4 245 us (1.4 GB: 5.9 TB/s), 32 tokens with rank 16 888 us: the bytes once, at what reads alone reach.
-// More than two tokens an expert cost another pass of gate and up over codes that
-// then mostly lie in the caches, and the multiplications bound it: 8 experts of 4 tokens 100 us, of 8
-// 198, of 32 718; the batched forward, which is made for that, takes 148, 142 and 161.  Short rows have a kernel of
-// their own for gate and up, and down split over the experts: 8 tokens of 279 experts, 576 x 2016, 58 us (floor 29).
+// 384 experts, 8 a token, 7168 x 2048: one token 40 us (195 MB of codes and scales: 4.9 TB/s), 4 tokens with LoRA of rank
+// 64 196 us, 8 tokens on MXFP4 251 to 258 us (1.4 GB: 5.8 TB/s), 32 tokens with rank 16 and padded slots 888 to 907 us.
+// Gate and up read an expert's codes once for two of its slots, down once for every slot (with the
+// hint that a second pass is not expected: 32 tokens read 2.0 GB there, of 1.5 GB that are different).
+// Passes over codes that mostly lie in the caches are bound by the multiplications: 8 experts, rank 16, of 4 tokens
+// 117 us, of 8 215, of 32 797; the batched forward, which is made for that, takes 179, 180 and 202.  Short rows have a kernel of
+// their own for gate and up, and down split over the experts: 8 tokens of 279 experts, 576 x 2016, 60 us (floor 29).
 //
 // (The MFMAs' operand layout has another row in every lane of 16: their loads
 // touch 16 lines where these touch 2, which is what bounded them, 3.4 TB/s.)
@@ -973,7 +974,8 @@ __global__ __launch_bounds__(256) void k_decode_join(DecodeArgs a, int parts) {
 static bool down_by_slot(int64_t E, int64_t S) { return S > 2 * E; }
 
 // Down's parts: two workgroups a unit of the chip, as far as experts or slots reach (8 tokens of 279 experts, 576 x 2016: 116 -> 79 us;
-// 11 of 272, 416 x 1280, rank 64: 182 -> 100); columns that fill the chip by themselves are not split.
+// 11 of 272, 416 x 1280, rank 64: 182 -> 100).  256 blocks of columns, a workgroup a unit, are not split: 4 tokens with rank 16 at
+// hidden 4096 96 us both ways, 4128 131 (split 127), 6144 144 both ways, 7168 154 (158); 8 slots or fewer are one workgroup's in any case.
 static int down_parts(int64_t H, int64_t E, int64_t S) {
   const int64_t units = down_by_slot(E, S) || S < E ? S : E, columns = H / 16;  // (experts or slots for the waves, at most)
   const int64_t want = (512 + columns - 1) / columns, most = (units + kDownWaves - 1) / kDownWaves;

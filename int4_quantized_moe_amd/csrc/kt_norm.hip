@@ -10,7 +10,7 @@
 // its statistics and its outputs (deviations from the mean are squared, not
 // differences of squares), so that the bytes are those of the inputs and outputs.  Reached with
 // bf16 (a copy of 1 GiB: 4.9 to 5.1 TB/s): forward with a block's output, 16384 x 7168,
-// 184 us, 5.1 TB/s; backward without a norm behind the block, 16384 x 7168, 260 us, 5.4 TB/s.
+// 184 us, 5.1 TB/s; backward without a norm behind the block, 16384 x 7168, 258 us, 5.5 TB/s.
 // Statistics, sums and the parameters' gradients are fp32; each output is rounded once.
 #include "kt_step_common.hpp"
 
@@ -612,10 +612,10 @@ static NormShape norm_shape(int H) {
 // The backward's workgroups, one a unit of the chip, and their teams: as many as fit
 // in 16 waves, unless fewer give every unit a row.  Rows of 4097 to 8192 columns take 16
 // columns a thread and 8 waves, whose 256 registers each hold the parameters' gradients
-// and the next row (4096 rows of 7168, everything on: 121 us; 8 columns a thread in 14 waves
-// of 128 registers: 128).  Shorter rows take 8 columns a thread, in as many teams as
-// fit in 16 waves (8192 rows of 4096: 133 us, 4001 of 2049: 71; in 8 waves 172 and 98; all
-// before the steps after this one).  Longer ones take 16 columns a thread in 16 waves, without the next
+// and the next row (4096 rows, everything on: of 7168 116 us, as 8 columns a thread in 14 waves
+// of 128 registers; of 8192, bf16, 93 against 97; 2000 of 4097 66 against 61).  Shorter rows take 8 columns a
+// thread, in as many teams as fit in 16 waves (4001 of 2049: 56 us; in 8 waves 73; but 8192 of
+// 4096 126 against 118, 16384 of 1024 68 against 64).  Longer ones take 16 columns a thread in 16 waves, without the next
 // row and the vectors ahead and with two of the gradients in LDS (2048 rows of 16384: 197 us; with all
 // in registers, that is spilled, 288).
 constexpr int64_t kNormGroups = 256;

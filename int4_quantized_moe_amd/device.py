@@ -119,8 +119,9 @@ class DeviceLayer:
 
     def decode(self, inputs, expert_ids, route_weights, workspace, output=None, stream=None) -> torch.Tensor:
         """infer() for a few tokens (at most KT_MOE_DECODE_MAX_TOKENS, and KT_MOE_DECODE_MAX_SLOTS
-        token-slots; hidden at most KT_MOE_DECODE_MAX_HIDDEN), in a decode_workspace().  The faster of the
-        two while experts have up to about two tokens each (tokens * top_k <= 2 * num_experts)."""
+        token-slots; hidden at most KT_MOE_DECODE_MAX_HIDDEN), in a decode_workspace().  As measured
+        the faster of the two while the experts in use have up to about 2 token-slots each on average (about 6 where
+        8 experts are in use); for tokens that share experts more infer() is, by up to 6 times."""
         dev, h, k = self.gate_packed.device, self.cfg.hidden, self.cfg.top_k
         if inputs.dim() != 2:
             raise ValueError("inputs must be [tokens, hidden]")
